@@ -57,7 +57,8 @@ typedef enum {
   HLO_BF16 = 1,
   HLO_S8 = 2,
   HLO_F16 = 3,
-  HLO_S32 = 4
+  HLO_S32 = 4,
+  HLO_F8E4M3FN = 5 /* only as the output of hlo_rms_norm */
 } hlo_dtype;
 
 /* A dense array: logical shape plus physical layout. */
@@ -415,6 +416,170 @@ hlo_status hlo_selftest_bounded_wait(void* stream);
  * ---------------------------------------------------------------------------------------------- */
 int32_t hlo_jit_kernels(void);
 int64_t hlo_jit_source(const hlo_ew_chain* chain, int32_t dtype, char* buf, int64_t buf_len);
+
+/* ------------------------------------------------------------------------------------------------
+ * The fusions between a decoder's matrix products: root-mean-square norm with the residual's addition
+ * (and its gradient), dropout from a counter-based generator, rotary positions, and the processing of
+ * logits. The pages define none of them (except the generator's algorithm, by name); each entry point
+ * states its own formula. They follow the conventions above, with these differences:
+ *
+ *  - Arrays are hlo_views: logical dimensions with a stride (in elements) for each, so that an operand
+ *    can be a part of a larger buffer (the heads of a packed projection, rows with a pitch). The last
+ *    dimension has stride 1 unless its size is 1; strides are >= 0. An input dimension may have stride 0
+ *    (broadcast); an output's elements must be distinct. Strides of dimensions of size 1 do not matter.
+ *  - An output may be exactly an input (the same address, element type, dimensions and strides), for
+ *    in-place use: every element is read before the same thread writes it. Any other overlap of an output
+ *    with another operand is HLO_ERR_INVALID_ARG, except that two views of one buffer that provably share
+ *    no element (equal outermost strides, disjoint windows within one) may interleave.
+ *  - Arithmetic is f32 on the operands' values; every output is rounded once, to nearest even.
+ * ---------------------------------------------------------------------------------------------- */
+typedef struct {
+  int32_t rank;                    /* 1..HLO_MAX_RANK */
+  int32_t dtype;                   /* hlo_dtype */
+  int64_t dims[HLO_MAX_RANK];
+  int64_t strides[HLO_MAX_RANK];   /* elements between neighbours along each dimension */
+} hlo_view;
+
+/* A random mask that is never stored. Element i (its linear index over the operand's logical dimensions,
+ * row-major, whatever the strides) is kept iff its 32-bit word is >= round(p 2^32). The words come from
+ * Philox4x32 with 10 rounds (Salmon, Moraes, Dror, Shaw: "Parallel Random Numbers: As Easy as 1, 2, 3",
+ * SC 2011; PHILOX of "StableHLO Specification", section "rng_bit_generator"): word i mod 4 of the
+ * generator's output for the counter (low, high half of i / 4; low, high half of offset) and the key
+ * (low, high half of seed). So a mask depends on (p, seed, offset) and the index alone, and the backward
+ * pass makes it again from them. Kept values are multiplied by f32(1 / (1 - p)); the others become +0,
+ * whatever they were (NaN and infinities included).
+ *   p        0 <= p <= 1 (0 keeps everything, 1 drops everything)
+ *   state    NULL, or two 64-bit words on the DEVICE, read when the kernel runs: the seed is then
+ *            state[0] and the offset state[1] + offset, so a captured graph can draw new masks */
+typedef struct {
+  double p;
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* state;
+} hlo_dropout_params;
+
+/* ------------------------------------------------------------------------------------------------
+ * hlo_rms_norm -- over the last dimension (size n >= 1) of x:
+ *   h   = residual + drop(x)                           (f32; written to sum, rounded, if given)
+ *   r   = 1 / sqrt(mean(h^2) + eps)                    (one per row; written to rstd if given)
+ *   y   = h * r * (weight + weight_offset)             (from the unrounded h)
+ *   out = y, or y in 8 bits:
+ *     out s8 or f8E4M3FN with scales:  s = max|y| / 127 (s8) or / 448 (f8), 1 where that is 0; out is y / s
+ *                                      rounded to nearest even and saturated, scales[row] = s; a NaN
+ *                                      becomes code 0 (s8) or NaN (f8), and makes its row's s NaN
+ *     out s8 with out_q:               clamp(round_nearest_even(y / scale) + zero_point) as in
+ *                                      hlo_quant_fusion, per-tensor parameters with host copies
+ *
+ *   x, x_ptr                 [..., n], f32 / bf16 / f16
+ *   residual, residual_ptr   NULL, or dims and element type of x
+ *   dropout                  NULL, or the mask of x
+ *   weight_ptr, weight_dtype NULL (ones), or n contiguous values of x's type or f32; weight_offset is
+ *                            added to each (1 for weights stored around zero)
+ *   sum, sum_ptr             NULL, or dims and element type of x: receives h
+ *   out, out_ptr             dims of x; x's type, f32, s8 or f8E4M3FN
+ *   scales                   NULL, or one f32 per row (contiguous, rows in row-major order): the 8-bit
+ *                            output's scales, as uniform quantization parameters per row
+ *   out_q                    NULL, or static parameters (out s8, scales NULL)
+ *   rstd                     NULL, or one f32 per row: r
+ *
+ * hlo_rms_norm_backward -- the gradients of the same, for dy = dL/dout (out not quantized) and dsum =
+ * dL/dsum (what reaches h by other ways; may be NULL):
+ *   g  = dy * (weight + weight_offset),  xh = h * rstd
+ *   dh = dsum + rstd * (g - xh * mean(g * xh))         dL/dresidual, and dL/dx without dropout
+ *   dx = drop(dh)                                      dL/dx with dropout (the same parameters)
+ *   dweight = sum over rows of dy * xh                 (f32, in a fixed order: deterministic)
+ *
+ *   dy, h, dsum              [..., n], one element type (f32 / bf16 / f16)
+ *   rstd                     one f32 per row, as written by the forward pass
+ *   dh, dx                   like h; dx is required with dropout and NULL without
+ *   dweight                  NULL, or n f32
+ *   workspace                required with dweight: at least hlo_rms_norm_workspace_size(rows, n) bytes,
+ *                            16-byte aligned; contents on entry do not matter; not shared by calls that
+ *                            overlap in time
+ * ---------------------------------------------------------------------------------------------- */
+hlo_status hlo_rms_norm(const hlo_view* x, const void* x_ptr, const hlo_view* residual, const void* residual_ptr,
+                        const hlo_dropout_params* dropout, const void* weight_ptr, int32_t weight_dtype,
+                        double weight_offset, double eps, const hlo_view* sum, void* sum_ptr, const hlo_view* out,
+                        void* out_ptr, float* scales, const hlo_quant* out_q, float* rstd, void* stream);
+
+hlo_status hlo_rms_norm_backward(const hlo_view* dy, const void* dy_ptr, const hlo_view* h, const void* h_ptr,
+                                 const float* rstd, const void* weight_ptr, int32_t weight_dtype, double weight_offset,
+                                 const hlo_view* dsum, const void* dsum_ptr, const hlo_dropout_params* dropout,
+                                 const hlo_view* dh, void* dh_ptr, const hlo_view* dx, void* dx_ptr, float* dweight,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+size_t hlo_rms_norm_workspace_size(int64_t rows, int64_t n);
+
+/* ------------------------------------------------------------------------------------------------
+ * hlo_dropout -- out = residual + drop(x), any rank; residual may be NULL. x, residual and out have the
+ * same dims and one element type (f32 / bf16 / f16). Its backward pass is the same call on the gradient,
+ * with the same parameters and no residual.
+ * ---------------------------------------------------------------------------------------------- */
+hlo_status hlo_dropout(const hlo_view* x, const void* x_ptr, const hlo_view* residual, const void* residual_ptr,
+                       const hlo_dropout_params* dropout, const hlo_view* out, void* out_ptr, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * hlo_rotary -- rotary positions: in the first rot = 2 n_pairs elements of every head, pair i turns by
+ * the angle a = 2 pi frac(position * turns[i] / 2^64):
+ *   (u, v) -> (scale (u cos a - v sin a), scale (v cos a + u sin a)),  with -a when inverse != 0
+ * The pair is (u, v) = elements (i, i + rot / 2), or (2 i, 2 i + 1) when interleaved != 0. The other
+ * dim - rot elements are copied. The backward pass of a rotation is the same call on the gradient with
+ * inverse flipped.
+ *
+ *   x, x_ptr, x_out, x_out_ptr   [batch, seq, heads, dim] or [seq, heads, dim], f32 / bf16 / f16; the
+ *                                output's strides are its own, so heads can be written first
+ *   y, ... y_out_ptr             NULL, or a second array (the keys) with the same batch, seq, dim and type
+ *   positions, positions_ptr     s32, [batch, seq] or [seq] as x; any sign; stride 0 repeats them
+ *   turns                        n_pairs 64-bit words on the device: the angle for position 1, in units of
+ *                                2^-64 turn. position * turns is formed mod 2^64, which is exact mod one
+ *                                turn, so angles keep full precision at any position
+ *
+ * hlo_rotary_turns writes such a table to HOST memory: theta_i / (2 pi) * 2^64 for theta_i = base^(-2i/rot),
+ * changed for longer contexts by
+ *   HLO_ROTARY_PLAIN        nothing
+ *   HLO_ROTARY_LINEAR       theta_i / factor (position interpolation)
+ *   HLO_ROTARY_BASE         base * factor^(rot / (rot - 2)): the slowest pair slows by factor, the fastest
+ *                           stays
+ *   HLO_ROTARY_BY_PARTS     theta_i (g + (1 - g) / factor) with g = clamp((w - low) / (high - low), 0, 1) and
+ *                           w = original_length theta_i / (2 pi), the turns the pair makes over the
+ *                           original context: pairs of more than `high` turns stay, those of fewer than
+ *                           `low` are interpolated, those between are mixed
+ * ---------------------------------------------------------------------------------------------- */
+typedef enum { HLO_ROTARY_PLAIN = 0, HLO_ROTARY_LINEAR = 1, HLO_ROTARY_BASE = 2, HLO_ROTARY_BY_PARTS = 3 } hlo_rotary_scaling;
+
+hlo_status hlo_rotary(const hlo_view* x, const void* x_ptr, const hlo_view* x_out, void* x_out_ptr, const hlo_view* y,
+                      const void* y_ptr, const hlo_view* y_out, void* y_out_ptr, const hlo_view* positions,
+                      const int32_t* positions_ptr, const uint64_t* turns, int32_t n_pairs, int32_t interleaved,
+                      int32_t inverse, double scale, void* stream);
+
+hlo_status hlo_rotary_turns(int32_t n_pairs, double base, int32_t scaling, double factor, double original_length,
+                            double low, double high, uint64_t* turns);
+
+/* ------------------------------------------------------------------------------------------------
+ * hlo_logits_process -- for every row b of logits [batch, vocab], token v, in this order (f32 steps):
+ *   l = logits[b, v] + bias[b, v]
+ *   if v occurs among the row's history:  l = l > 0 ? l / repetition[b] : l * repetition[b]
+ *   l = l - frequency[b] * c;  l = l - presence[b] * (c > 0)     c: occurrences at places >= prompt_lengths[b]
+ *   l = -inf where the mask's bit is 0
+ *   out[b, v] = l (rounded to out's type);  token[b] = the v of the greatest unrounded l, the lowest on
+ *   ties; NaN and -inf are never chosen, and token[b] = -1 if nothing else is left (a mask of no tokens)
+ *
+ *   logits, logits_ptr   [batch, vocab], f32 / bf16 / f16
+ *   bias, bias_ptr       NULL, or f32 [batch, vocab] (stride 0 over the batch repeats one row)
+ *   history, history_ptr NULL, or s32 [batch, max_length]; entries outside 0..vocab-1 are ignored
+ *   lengths              NULL (max_length), or s32[batch]: entries used; clamped to 0..max_length
+ *   prompt_lengths       NULL (0), or s32[batch]: the first entries, which count for repetition alone
+ *   repetition, frequency, presence   NULL (1, 0, 0), or f32[batch]
+ *   mask, mask_ptr       NULL, or s32 [batch, ceil(vocab / 32)]: bit v mod 32 of word v / 32 allows v;
+ *                        stride 0 over the batch repeats one row
+ *   out, out_ptr         NULL, or [batch, vocab] in logits' type or f32
+ *   token                NULL, or s32[batch]
+ * ---------------------------------------------------------------------------------------------- */
+hlo_status hlo_logits_process(const hlo_view* logits, const void* logits_ptr, const hlo_view* bias, const float* bias_ptr,
+                              const hlo_view* history, const int32_t* history_ptr, const int32_t* lengths,
+                              const int32_t* prompt_lengths, const float* repetition, const float* frequency,
+                              const float* presence, const hlo_view* mask, const int32_t* mask_ptr, const hlo_view* out,
+                              void* out_ptr, int32_t* token, void* stream);
 
 /* ------------------------------------------------------------------------------------------------
  * Fault injection for tests of the error path (no counterpart in the pages: the library's own test

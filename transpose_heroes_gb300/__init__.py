@@ -25,6 +25,8 @@ LIB_PATH = os.path.join(_PKG, "_lib", "libhlofusion.so")
 MAX_RANK = 8
 MAX_EW_OPS = 16
 DTYPES = {"f32": 0, "bf16": 1, "s8": 2, "f16": 3, "s32": 4}
+VIEW_DTYPES = {**DTYPES, "f8e4m3fn": 5}
+ROTARY_SCALING = {None: 0, "linear": 1, "base": 2, "by_parts": 3}
 OPS = {"exp": 1, "log": 2, "abs": 3, "neg": 4, "add_bcast": 5, "tanh": 6, "add_const": 7, "mul_const": 8,
        "add_input": 9, "mul_input": 10}
 REDUCE_KINDS = {"add": 0, "max": 1}
@@ -35,7 +37,8 @@ STATUS = {0: "HLO_OK", 1: "HLO_ERR_INVALID_ARG", 2: "HLO_ERR_UNSUPPORTED", 3: "H
 EXPORTS = ("hlo_reduce_fusion", "hlo_reduce_fusion_noalloc", "hlo_reduce_workspace_size", "hlo_transpose_fusion",
            "hlo_layout_convert",
            "hlo_quant_fusion", "hlo_quant_binary", "hlo_quant_broadcast_in_dim", "hlo_quant_reshape",
-           "hlo_reduce_max_argmax", "hlo_device_faults",
+           "hlo_reduce_max_argmax", "hlo_rms_norm", "hlo_rms_norm_backward", "hlo_rms_norm_workspace_size",
+           "hlo_dropout", "hlo_rotary", "hlo_rotary_turns", "hlo_logits_process", "hlo_device_faults",
            "hlo_selftest_bounded_wait", "hlo_jit_kernels", "hlo_jit_source", "hlo_last_error", "hlo_version")
 QUANT_BINARY_OPS = {"add": 0, "divide": 1, "maximum": 2, "minimum": 3, "multiply": 4}
 
@@ -63,6 +66,24 @@ class Quant(ctypes.Structure):
                 ("scales", ctypes.c_void_p), ("zero_points", ctypes.c_void_p),
                 ("host_scales", ctypes.c_void_p), ("host_zero_points", ctypes.c_void_p),
                 ("storage_min", ctypes.c_int32), ("storage_max", ctypes.c_int32)]
+
+
+class View(ctypes.Structure):
+    _fields_ = [("rank", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("dims", ctypes.c_int64 * MAX_RANK), ("strides", ctypes.c_int64 * MAX_RANK)]
+
+
+class Dropout(ctypes.Structure):
+    """hlo_dropout_params: element i is dropped with probability p, by the counter-based generator's word
+    for (seed, offset, i). `state` (a device tensor of two int64, or None) holds a seed that replaces
+    `seed` and an offset that `offset` is added to, read when the kernel runs."""
+
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("state", ctypes.c_void_p)]
+
+    def __init__(self, p: float, seed: int = 0, offset: int = 0, state=None):
+        super().__init__(p, seed, offset, _ptr(state))
+        self.keep = state
 
 
 _lib = None
@@ -108,6 +129,24 @@ def lib() -> ctypes.CDLL:
             h.hlo_quant_broadcast_in_dim.restype = ctypes.c_int
             h.hlo_quant_reshape.argtypes = [P(Array), vp, P(Quant), P(Array), i32, vp, vp]
             h.hlo_quant_reshape.restype = ctypes.c_int
+            V, D = P(View), P(Dropout)
+            h.hlo_rms_norm.argtypes = [V, vp, V, vp, D, vp, i32, ctypes.c_double, ctypes.c_double, V, vp, V, vp, vp,
+                                       P(Quant), vp, vp]
+            h.hlo_rms_norm.restype = ctypes.c_int
+            h.hlo_rms_norm_backward.argtypes = [V, vp, V, vp, vp, vp, i32, ctypes.c_double, V, vp, D, V, vp, V, vp, vp,
+                                                vp, ctypes.c_size_t, vp]
+            h.hlo_rms_norm_backward.restype = ctypes.c_int
+            h.hlo_rms_norm_workspace_size.argtypes = [i64, i64]
+            h.hlo_rms_norm_workspace_size.restype = ctypes.c_size_t
+            h.hlo_dropout.argtypes = [V, vp, V, vp, D, V, vp, vp]
+            h.hlo_dropout.restype = ctypes.c_int
+            h.hlo_rotary.argtypes = [V, vp, V, vp, V, vp, V, vp, V, vp, vp, i32, i32, i32, ctypes.c_double, vp]
+            h.hlo_rotary.restype = ctypes.c_int
+            h.hlo_rotary_turns.argtypes = [i32, ctypes.c_double, i32, ctypes.c_double, ctypes.c_double,
+                                           ctypes.c_double, ctypes.c_double, vp]
+            h.hlo_rotary_turns.restype = ctypes.c_int
+            h.hlo_logits_process.argtypes = [V, vp, V, vp, V, vp, vp, vp, vp, vp, vp, V, vp, V, vp, vp, vp]
+            h.hlo_logits_process.restype = ctypes.c_int
             h.hlo_device_faults.argtypes = [P(ctypes.c_uint32), i32]
             h.hlo_device_faults.restype = ctypes.c_int
             h.hlo_selftest_bounded_wait.argtypes = [vp]
@@ -386,3 +425,223 @@ def quant_fusion(inp, dims, in_q, out_m2m, out, out_dtype="s8", out_q=None, in_m
     _check(lib().hlo_quant_fusion(ctypes.byref(a), _ptr(inp), qi.ref(), _ref(ch), _i64(out_m2m), ctypes.byref(o),
                                   _ptr(out), qo.ref(), _stream(stream)))
     return out
+
+
+# ---- the fusions between a decoder's matrix products ---------------------------------------------------------
+# Their operands are views: torch tensors (dims, strides and element type are the tensor's own) or
+# DeviceViews of raw device pointers. Vectors (a weight, scales, lengths, ...) are contiguous tensors, or
+# raw pointers.
+class DeviceView:
+    """A view of device memory at `ptr` (an address or a tensor that carries the bits)."""
+
+    __slots__ = ("ptr", "ref", "dims", "keep")
+
+    def __init__(self, ptr, dims, dtype: str, strides=None):
+        dims = [int(d) for d in dims]
+        if strides is None:
+            strides, s = [0] * len(dims), 1
+            for i in range(len(dims) - 1, -1, -1):
+                strides[i] = s
+                s *= dims[i]
+        self.ptr, self.dims, self.keep = _ptr(ptr), tuple(dims), ptr
+        self.ref = ctypes.byref(_make_view(dims, strides, VIEW_DTYPES[dtype]))
+
+
+def _make_view(dims, strides, dtype: int) -> View:
+    v = View()
+    v.rank, v.dtype = len(dims), dtype
+    if len(dims) > MAX_RANK or len(strides) != len(dims):
+        raise HloError(STATUS_INVALID_ARG, f"a view holds 1..{MAX_RANK} dimensions with a stride each")
+    for i, (d, s) in enumerate(zip(dims, strides)):
+        v.dims[i], v.strides[i] = int(d), int(s)
+    return v
+
+
+_views = {}  # (shape, strides, element type) -> the marshalled descriptor; descriptors hold no address
+_torch_dtypes = {}
+
+
+def _view(t):
+    """(descriptor reference, address) of a tensor or DeviceView; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if type(t) is DeviceView:
+        return t.ref, t.ptr
+    key = (t.shape, t.stride(), t.dtype)
+    ref = _views.get(key)
+    if ref is None:
+        if not _torch_dtypes:
+            import torch
+
+            _torch_dtypes.update({torch.float32: 0, torch.bfloat16: 1, torch.int8: 2, torch.float16: 3, torch.int32: 4,
+                                  torch.float8_e4m3fn: 5})
+        if t.dtype not in _torch_dtypes:
+            raise HloError(STATUS_INVALID_ARG, f"no element type for {t.dtype}")
+        if len(_views) >= 4096:
+            _views.clear()
+        ref = _views[key] = ctypes.byref(_make_view(t.shape, t.stride(), _torch_dtypes[t.dtype]))
+    return ref, t.data_ptr()
+
+
+def _vector(t, count: int, dtype: str, what: str) -> int:
+    """Address of a contiguous device vector of `count` elements (raw addresses are taken as they are)."""
+    if t is None or isinstance(t, int):
+        return t or 0
+    _view(t)  # the element type is known
+    if _torch_dtypes[t.dtype] != VIEW_DTYPES[dtype] or t.numel() != count or not t.is_contiguous():
+        raise HloError(STATUS_INVALID_ARG, f"{what}: a contiguous {dtype} vector of {count} elements is wanted")
+    return t.data_ptr()
+
+
+def _dims(t):
+    return t.dims if type(t) is DeviceView else t.shape
+
+
+def _weight(weight, weight_dtype, n):
+    if weight is None or isinstance(weight, int):
+        return weight or 0, VIEW_DTYPES[weight_dtype]
+    _view(weight)
+    if weight.numel() != n or not weight.is_contiguous():
+        raise HloError(STATUS_INVALID_ARG, f"rms_norm weight: a contiguous vector of {n} elements is wanted")
+    return weight.data_ptr(), _torch_dtypes[weight.dtype]
+
+
+_raw_stream = None
+
+
+def _call_stream(stream) -> int:
+    if stream is not None:
+        return _stream(stream)
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _raw_stream = (lambda: raw(torch.cuda.current_device())) if raw else (lambda: _stream(None))
+    return _raw_stream()
+
+
+def rms_norm(x, out, weight=None, residual=None, sum_out=None, rstd=None, eps=1e-6, weight_offset=0.0, dropout=None,
+             scales=None, out_q=None, weight_dtype="f32", stream=None):
+    """hlo_rms_norm: h = residual + drop(x) (to sum_out), out = h / rms(h) * (weight + weight_offset), out in
+    x's type, f32, or 8 bits with `scales` (per row) or `out_q` (static). weight_dtype names the type of a
+    weight given as a raw address."""
+    dims = _dims(x)
+    n = int(dims[-1]) if len(dims) else 0
+    rows = 1
+    for d in dims[:-1]:
+        rows *= int(d)
+    xv, xp = _view(x)
+    rv, rp = _view(residual)
+    sv, sp = _view(sum_out)
+    ov, op = _view(out)
+    wp, wd = _weight(weight, weight_dtype, n)
+    q = _QuantKeep(out_q) if out_q is not None else None
+    st = lib().hlo_rms_norm(xv, xp, rv, rp, dropout, wp, wd, weight_offset, eps, sv, sp, ov, op,
+                            _vector(scales, rows, "f32", "scales"), None if q is None else q.ref(),
+                            _vector(rstd, rows, "f32", "rstd"), _call_stream(stream))
+    if st:
+        _check(st)
+    return out
+
+
+def rms_norm_workspace_size(rows: int, n: int) -> int:
+    """hlo_rms_norm_workspace_size: scratch bytes of rms_norm_backward with dweight."""
+    return int(lib().hlo_rms_norm_workspace_size(int(rows), int(n)))
+
+
+def rms_norm_backward(dy, h, rstd, dh, weight=None, dsum=None, dx=None, dropout=None, dweight=None, workspace=None,
+                      weight_offset=0.0, weight_dtype="f32", workspace_bytes=None, stream=None):
+    """hlo_rms_norm_backward: dh (the gradient of h), dx = drop(dh) with dropout, and dweight, from dy, the
+    forward pass's sum h and rstd, and dsum (what reaches h by other ways). The workspace is a contiguous
+    tensor, or a raw address with workspace_bytes."""
+    dims = _dims(h)
+    n = int(dims[-1]) if len(dims) else 0
+    rows = 1
+    for d in dims[:-1]:
+        rows *= int(d)
+    yv, yp = _view(dy)
+    hv, hp = _view(h)
+    sv, sp = _view(dsum)
+    dhv, dhp = _view(dh)
+    dxv, dxp = _view(dx)
+    wp, wd = _weight(weight, weight_dtype, n)
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib().hlo_rms_norm_backward(yv, yp, hv, hp, _vector(rstd, rows, "f32", "rstd"), wp, wd, weight_offset, sv, sp,
+                                     dropout, dhv, dhp, dxv, dxp, _vector(dweight, n, "f32", "dweight"), _ptr(workspace),
+                                     workspace_bytes, _call_stream(stream))
+    if st:
+        _check(st)
+    return dh
+
+
+def dropout(x, out, params, residual=None, stream=None):
+    """hlo_dropout: out = residual + drop(x) for params = Dropout(p, seed, offset). The backward pass is the
+    same call on the gradient."""
+    xv, xp = _view(x)
+    rv, rp = _view(residual)
+    ov, op = _view(out)
+    st = lib().hlo_dropout(xv, xp, rv, rp, params, ov, op, _call_stream(stream))
+    if st:
+        _check(st)
+    return out
+
+
+def rotary_turns(rot: int, base: float = 10000.0, scaling=None, factor: float = 1.0, original_length: float = 0.0,
+                 low: float = 1.0, high: float = 32.0) -> np.ndarray:
+    """hlo_rotary_turns: the table of rot / 2 angles for position 1 (64-bit fixed-point turns, as int64 bits) for
+    rotary(); scaling is None, "linear", "base" or "by_parts"."""
+    if rot % 2:
+        raise HloError(STATUS_INVALID_ARG, f"rotary_turns: {rot} elements are not pairs")
+    out = np.empty(rot // 2, dtype=np.int64)
+    _check(lib().hlo_rotary_turns(rot // 2, float(base), ROTARY_SCALING[scaling], float(factor), float(original_length),
+                                  float(low), float(high), out.ctypes.data))
+    return out
+
+
+def rotary(x, out, positions, turns, k=None, k_out=None, interleaved=False, scale=1.0, inverse=False, n_pairs=None,
+           stream=None):
+    """hlo_rotary: rotates the first 2 n_pairs elements of every head of x (and of k) by position * turns; the
+    rest is copied. turns: rotary_turns() on the device (int64), or a raw address with n_pairs. inverse
+    turns back: the backward pass."""
+    xv, xp = _view(x)
+    ov, op = _view(out)
+    kv, kp = _view(k)
+    kov, kop = _view(k_out)
+    pv, pp = _view(positions)
+    if n_pairs is None:
+        if turns.element_size() != 8 or not turns.is_contiguous():
+            raise HloError(STATUS_INVALID_ARG, "rotary turns: a contiguous vector of 64-bit words is wanted")
+        n_pairs = turns.numel()
+    st = lib().hlo_rotary(xv, xp, ov, op, kv, kp, kov, kop, pv, pp, _ptr(turns), n_pairs, interleaved, inverse, scale,
+                          _call_stream(stream))
+    if st:
+        _check(st)
+    return out
+
+
+def logits_process(logits, out=None, bias=None, history=None, lengths=None, prompt_lengths=None, repetition=None,
+                   frequency=None, presence=None, mask=None, token=None, stream=None):
+    """hlo_logits_process: bias, repetition / frequency / presence penalties for the tokens of each row's
+    history, the grammar's bit mask, and the greedy token (lowest index on ties, -1 when nothing is left).
+    A bias or mask of one dimension serves every row."""
+    batch = int(_dims(logits)[0])
+    lv, lp = _view(logits)
+    if bias is not None and len(_dims(bias)) == 1:
+        bias = bias.expand(batch, -1)
+    if mask is not None and len(_dims(mask)) == 1:
+        mask = mask.expand(batch, -1)
+    bv, bp = _view(bias)
+    hv, hp = _view(history)
+    mv, mp = _view(mask)
+    ov, op = _view(out)
+    st = lib().hlo_logits_process(lv, lp, bv, bp, hv, hp, _vector(lengths, batch, "s32", "lengths"),
+                                  _vector(prompt_lengths, batch, "s32", "prompt_lengths"),
+                                  _vector(repetition, batch, "f32", "repetition"),
+                                  _vector(frequency, batch, "f32", "frequency"),
+                                  _vector(presence, batch, "f32", "presence"), mv, mp, ov, op,
+                                  _vector(token, batch, "s32", "token"), _call_stream(stream))
+    if st:
+        _check(st)
+    return out if out is not None else token

@@ -13,6 +13,7 @@
 #include <utility>
 #include <vector>
 
+#include "hlo_api.h"
 #include "hlo_fusion.h"
 #include "hlo_internal.h"
 
@@ -432,6 +433,22 @@ int hlo::kernel_blocks_per_sm(const void* kernel, int threads, size_t smem) {
 }
 
 namespace hlo {
+hlo_status api_fail(hlo_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  g_err = buf;
+  return s;
+}
+hlo_status api_ok() { return ok(); }
+hlo_status api_cuda_status(cudaError_t e, const char* what) { return cuda_status(e, what); }
+bool api_injected(const char* site) { return injected(site); }
+hlo_status api_check_quant(const hlo_quant* q, const hlo_array& a, const char* what, QuantParams* out) {
+  return check_quant(q, a, what, out);
+}
+
 namespace {
 std::vector<FaultReader>& fault_readers() {
   static std::vector<FaultReader> readers;  // filled while the library's units are initialised
