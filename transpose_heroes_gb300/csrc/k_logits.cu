@@ -87,160 +87,286 @@ __global__ void __launch_bounds__(kThreads) logits_any_kernel(LogitsPlan p) {
   }
 }
 
-// Blocks of a cluster take slabs of one row in turn: blockDim.x U vectors each. A slab's logits are requested
-// first; while they come, the block counts the occurrences of the slab's tokens in shared memory: COUNT
-// is uint16_t (histories below 2^15) or uint32_t, its top bit says "occurs in the prompt" and the rest
-// counts what came after. Adding and or-ing whole numbers gives one result in any order. The blocks' best
-// tokens meet in the first block through distributed shared memory.
+// The greatest value of the warp's lanes; NaN only if all are.
+__device__ __forceinline__ float warp_max_of(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Dynamic shared memory for slabs of `slab` tokens: their counts, a bit for each that occurs, and the list of
+// those with their values.
+struct LogitsShared {
+  size_t bits, value, list, bytes;
+  __host__ __device__ LogitsShared(int slab, int count_bytes, int64_t max_length) {
+    const size_t listed = (size_t)(slab < max_length ? slab : max_length);
+    bits = (size_t)slab * count_bytes;
+    value = bits + slab / 8;
+    list = value + listed * 4;
+    bytes = list + listed * count_bytes;
+  }
+};
+
+// A cluster of blocks shares a row; its blocks take slabs of `batches` times blockDim.x U vectors in turn.
+// The penalties touch a few of a slab's tokens (those of the history), but nearly every warp would meet one
+// and all its lanes would run their division. So a slab has three parts:
+//  1. mark the tokens that occur in the history and count their occurrences after the prompt, in shared memory
+//     (COUNT is uint16_t for histories below 2^16, else uint32_t; adding and or-ing whole numbers gives one
+//     result in any order). Whoever finds a token first puts it on a list.
+//  2. a thread for each listed token works out its value, from the logit itself.
+//  3. stream the slab, with the listed tokens masked out; then store their values over it.
+// The slab's first logits are requested before all this. The blocks' best tokens are written to the first
+// block's shared memory, and only that block waits for them.
 template <int DT, int U, typename COUNT>
-__global__ void __launch_bounds__(kThreads) logits_kernel(LogitsPlan p, int cluster) {
+__global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_constant__ LogitsPlan p, int cluster, int batches) {
   constexpr int W = kVec<DT>, EB = 16 / W;
   constexpr int CB = sizeof(COUNT), CPW = 4 / CB;  // counts a 32-bit word
-  constexpr uint32_t TOP = CB == 2 ? 0x8000u : 0x80000000u;
-  extern __shared__ uint4 seen4[];
-  uint32_t* const seen = reinterpret_cast<uint32_t*>(seen4);
-  __shared__ unsigned long long best_of[kThreads / 32];
-  __shared__ unsigned long long block_best;
+  extern __shared__ __align__(16) char shared[];
+  __shared__ unsigned long long best_of[kThreads / 32], cluster_best[8];
+  __shared__ int listed;
+  const bool meet = cluster > 1 && p.token;
+  // the first of the cluster's two barriers: every block has started before one writes to another
+  if (meet) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int64_t b = blockIdx.x / cluster;
-  const int rank = (int)(blockIdx.x - b * cluster);
-  const int vocab = (int)p.vocab;
-  const int64_t x_off = b * p.x_stride, out_off = b * p.out_stride;
-  const int shift = (int)(((int64_t)((uintptr_t)p.x / EB) + x_off) & (W - 1));
-  int32_t len = 0, prompt = 0;
-  if (p.history) {
-    len = (int32_t)p.max_length;
-    if (p.lengths) len = max(0, min(len, p.lengths[b]));
-    if (p.prompts) prompt = p.prompts[b];
-  }
-  const float rep = p.repetition ? p.repetition[b] : 1.0f;
-  const float freq = p.frequency ? p.frequency[b] : 0.0f, pres = p.presence ? p.presence[b] : 0.0f;
-  const int words = (vocab + 31) / 32;
+  const int rank = (int)(blockIdx.x - b * cluster), tid = threadIdx.x, threads = blockDim.x;
+  const int vocab = (int)p.vocab, words = (vocab + 31) / 32;
+  const int batch = threads * U * W, slab = batches * batch;
+  const LogitsShared parts(slab, CB, p.max_length);
+  uint32_t* const seen = reinterpret_cast<uint32_t*>(shared);
+  uint32_t* const bits = reinterpret_cast<uint32_t*>(shared + parts.bits);
+  float* const value = reinterpret_cast<float*>(shared + parts.value);
+  COUNT* const list = reinterpret_cast<COUNT*>(shared + parts.list);
+  const char* const x_row = reinterpret_cast<const char*>(p.x) + b * p.x_stride * EB;
+  const int64_t out_off = b * p.out_stride;
+  const int shift = (int)(((uintptr_t)x_row / EB) & (W - 1));
   const uint32_t* const mask = p.mask ? p.mask + b * p.mask_stride : nullptr;
   const float* const bias = p.bias ? p.bias + b * p.bias_stride : nullptr;
-  const bool bias_whole = bias && shift == 0 && (uintptr_t)bias % 16 == 0;
-  const int slab = (int)blockDim.x * U * W;
+  const bool whole_rows = shift == 0 && (uintptr_t)bias % 16 == 0;
+  int len = 0, prompt = 0;
+  if (p.history) {
+    len = (int)p.max_length;
+    if (p.lengths) len = max(0, min(len, p.lengths[b]));
+    if (p.prompts) prompt = p.prompts[b];
+    for (int i = tid; i < slab * CB / 16 + slab / 128; i += threads) reinterpret_cast<uint4*>(shared)[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) listed = 0;
+  }
   float best_v = __int_as_float(0xFF800000);
   int best_i = -1;
+  float warp_best = best_v;
+  unsigned long long best = 0;
   for (int64_t start = (int64_t)rank * slab - shift; start < vocab; start += (int64_t)cluster * slab) {
     const int s0 = (int)start;
-    uint4 xr[U];
+    uint4 x[U];
+    uint32_t allowed[U];
+    const auto request = [&](int at) {
+      const int c0 = at + tid * W;
+      if (whole_rows && at + batch <= vocab) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c0 = start + (int64_t)(threadIdx.x + u * blockDim.x) * W;
-      xr[u] = c0 < vocab ? load_cut<DT>(p.x, x_off, c0, vocab) : make_uint4(0, 0, 0, 0);
-    }
+        for (int u = 0; u < U; ++u) x[u] = load16(x_row + (int64_t)(c0 + u * threads * W) * EB);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int c = c0 + u * threads * W;  // a multiple of W: its bits lie in one byte
+          allowed[u] = mask ? (uint32_t)__ldg(reinterpret_cast<const uint8_t*>(mask) + (c >> 3)) >> (c & 7) : 0xFFFFFFFFu;
+        }
+        return;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * threads * W;
+        x[u] = make_uint4(0, 0, 0, 0);
+        allowed[u] = 0xFFFFFFFFu;
+        if (c >= vocab) continue;
+        x[u] = load_cut<DT>(p.x, b * p.x_stride, c, vocab, p.x_end);
+        if (mask) {
+          const int w0 = c >> 5;  // -1 for the columns before the row
+          const uint32_t lo = w0 >= 0 ? __ldg(mask + w0) : 0;
+          const uint32_t hi = (c & 31) + W > 32 && w0 + 1 < words ? __ldg(mask + w0 + 1) : 0;
+          allowed[u] = __funnelshift_r(lo, hi, c & 31);
+        }
+      }
+    };
+    request(s0);
+    int n = 0;
     if (len > 0) {
-      for (int i = threadIdx.x; i < slab * CB / 16; i += blockDim.x) seen4[i] = make_uint4(0, 0, 0, 0);
-      __syncthreads();
+      __syncthreads();  // counts and bits are 0, the list is empty
       const int32_t* const h = p.history + b * p.history_stride;
-#pragma unroll 4
-      for (int32_t i = threadIdx.x; i < len; i += blockDim.x) {
-        const int64_t t = (int64_t)__ldg(h + i) - s0;
-        if (t < 0 || t >= slab) continue;
-        const int at = (int)t, bit = 8 * CB * (at % CPW);
-        if (i < prompt) atomicOr(&seen[at / CPW], TOP << bit);
-        else atomicAdd(&seen[at / CPW], 1u << bit);
+      const uint32_t limit = (uint32_t)min(slab, vocab - s0);
+      const int lane = tid & 31;
+#pragma unroll 2
+      for (int i0 = tid - lane; i0 < len; i0 += threads) {
+        const int i = i0 + lane;
+        const int token = i < len ? __ldg(h + i) : -1;
+        const uint32_t at = (uint32_t)token - (uint32_t)s0;
+        bool first = false;
+        if (at < limit && token >= 0) {  // not another slab's token, nor one outside the vocabulary
+          const uint32_t m = 1u << (at & 31);
+          first = !(atomicOr(&bits[at >> 5], m) & m);
+          if (i >= prompt) atomicAdd(&seen[at / CPW], 1u << (8 * CB * (int)(at % CPW)));
+        }
+        const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+        if (firsts) {  // one place on the list for all of the warp's
+          int place = 0;
+          if (lane == 0) place = atomicAdd(&listed, __popc(firsts));
+          place = __shfl_sync(0xffffffffu, place, 0) + __popc(firsts & ((1u << lane) - 1));
+          if (first) list[place] = (COUNT)at;
+        }
       }
       __syncthreads();
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int place = (int)(threadIdx.x + u * blockDim.x) * W;
-      if ((int64_t)s0 + place >= vocab) continue;
-      const int c0 = s0 + place;
-      float v[W];
-      unpack<DT>(xr[u], v);
-      if (bias) {
-        float w[W];
-        if (bias_whole && c0 + W <= vocab) {
-#pragma unroll
-          for (int q = 0; q < W / 4; ++q) {
-            const float4 f = __ldg(reinterpret_cast<const float4*>(bias + c0) + q);
-            w[4 * q] = f.x, w[4 * q + 1] = f.y, w[4 * q + 2] = f.z, w[4 * q + 3] = f.w;
+      n = listed;
+      if (n > 0) {
+        const float rep = p.repetition ? p.repetition[b] : 1.0f;
+        const float freq = p.frequency ? p.frequency[b] : 0.0f, pres = p.presence ? p.presence[b] : 0.0f;
+        float top_v = __int_as_float(0xFF800000);
+        int top_i = -1;
+        for (int i = tid; i < n; i += threads) {
+          const int at = (int)list[i], c = s0 + at;
+          float l = load_plain(x_row, DT, c);
+          const uint32_t s = reinterpret_cast<COUNT*>(seen)[at];
+          if (bias) l = __fadd_rn(l, __ldg(bias + c));
+          l = penalised(l, (float)s, rep, freq, pres);
+          if (mask && !((__ldg(mask + (c >> 5)) >> (c & 31)) & 1u)) l = __int_as_float(0xFF800000);
+          value[i] = l;
+          reinterpret_cast<COUNT*>(seen)[at] = 0;
+          if (l > top_v || (l == top_v && c < top_i)) {
+            top_v = l;
+            top_i = c;
           }
+        }
+        const unsigned long long key = top_i >= 0 ? choice_key(top_v, top_i) : 0;
+        best = key > best ? key : best;
+        __syncthreads();
+      }
+    }
+    for (int k = 0; k < batches; ++k) {
+      const int base = s0 + k * batch;
+      if (base >= vocab) break;
+      if (k > 0) request(base);
+      const auto masked = [&](float (&v)[W], uint32_t open, int place) {
+        if (n > 0) open &= ~((uint32_t)reinterpret_cast<const uint8_t*>(bits)[place >> 3] >> (place & 7));
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (!((open >> e) & 1u)) v[e] = __int_as_float(0xFF800000);
+      };
+      if (whole_rows && base + batch <= vocab) {
+        float4 w[W / 4];  // the bias of a vector, requested one vector ahead
+        const float* const bias_at = bias + base + tid * W;
+        if (bias) {
+#pragma unroll
+          for (int q = 0; q < W / 4; ++q) w[q] = __ldg(reinterpret_cast<const float4*>(bias_at) + q);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int place = k * batch + (tid + u * threads) * W, c0 = s0 + place;
+          float v[W];
+          unpack<DT>(x[u], v);
+          if (bias) {
+#pragma unroll
+            for (int q = 0; q < W / 4; ++q) {
+              const float2 a = __fadd2_rn(make_float2(v[4 * q], v[4 * q + 1]), make_float2(w[q].x, w[q].y));
+              const float2 c = __fadd2_rn(make_float2(v[4 * q + 2], v[4 * q + 3]), make_float2(w[q].z, w[q].w));
+              v[4 * q] = a.x, v[4 * q + 1] = a.y, v[4 * q + 2] = c.x, v[4 * q + 3] = c.y;
+            }
+            if (u + 1 < U) {
+#pragma unroll
+              for (int q = 0; q < W / 4; ++q) w[q] = __ldg(reinterpret_cast<const float4*>(bias_at + (u + 1) * threads * W) + q);
+            }
+          }
+          if (mask || n > 0) masked(v, allowed[u], place);
+          if (p.out) {
+            if (p.out_dt == DT) {
+              *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.out) + (out_off + c0) * EB) = pack<DT>(v);
+            } else {
+#pragma unroll
+              for (int q = 0; q < W / 4; ++q)
+                *(reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + out_off + c0) + q) =
+                    make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            }
+          }
+          if (p.token) {  // only the warps that beat their best so far (one in t at their t-th vector) look for the place
+            float top = v[0];
+#pragma unroll
+            for (int e = 1; e < W; ++e) top = fmaxf(top, v[e]);  // NaN is passed over
+            const float warp_top = warp_max_of(top);
+            if (warp_top > warp_best) {
+              warp_best = warp_top;
+              if (top == warp_top) {
+                best_v = top;
+#pragma unroll
+                for (int e = W - 1; e >= 0; --e)
+                  if (v[e] == top) best_i = c0 + e;
+              }
+            }
+          }
+        }
+        continue;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int place = k * batch + (tid + u * threads) * W, c0 = s0 + place;
+        if (c0 >= vocab) continue;
+        float v[W];
+        unpack<DT>(x[u], v);
+        if (bias) {
+#pragma unroll
+          for (int e = 0; e < W; ++e)
+            if (c0 + e >= 0 && c0 + e < vocab) v[e] = __fadd_rn(v[e], __ldg(bias + c0 + e));
+        }
+        masked(v, allowed[u], place);
+        const bool full = c0 >= 0 && c0 + W <= vocab;
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          if (!full && (c0 + e < 0 || c0 + e >= vocab)) continue;
+          if (v[e] > best_v) {  // false for NaN; the lowest token on ties
+            best_v = v[e];
+            best_i = c0 + e;
+          }
+        }
+        if (!p.out) continue;
+        if (p.out_dt == DT) {
+          store_cut<DT>(p.out, out_off, c0, vocab, v);
         } else {
 #pragma unroll
-          for (int e = 0; e < W; ++e) w[e] = c0 + e >= 0 && c0 + e < vocab ? __ldg(bias + c0 + e) : 0.0f;
+          for (int e = 0; e < W; ++e)
+            if (full || (c0 + e >= 0 && c0 + e < vocab)) reinterpret_cast<float*>(p.out)[out_off + c0 + e] = v[e];
         }
-#pragma unroll
-        for (int e = 0; e < W; ++e) v[e] = __fadd_rn(v[e], w[e]);
-      }
-      if (len > 0) {
-        uint32_t n[W / CPW], any = 0;
-#pragma unroll
-        for (int q = 0; q < W / CPW; ++q) any |= n[q] = seen[place / CPW + q];
-        if (any) {
-#pragma unroll
-          for (int e = 0; e < W; ++e) {
-            const uint32_t c = CB == 2 ? (n[e / CPW] >> (16 * (e % CPW))) & 0xFFFFu : n[e / CPW];
-            if (c) v[e] = penalised(v[e], (float)(c & (TOP - 1)), rep, freq, pres);
-          }
-        }
-      }
-      if (mask) {
-        const int w0 = c0 >> 5;  // -1 for the columns before the row, which are not stored
-        const uint32_t lo = w0 >= 0 ? __ldg(mask + w0) : 0;
-        const uint32_t hi = (c0 & 31) + W > 32 && w0 + 1 < words ? __ldg(mask + w0 + 1) : 0;
-        const uint32_t bits = __funnelshift_r(lo, hi, c0 & 31);
-#pragma unroll
-        for (int e = 0; e < W; ++e)
-          if (!((bits >> e) & 1u)) v[e] = __int_as_float(0xFF800000);
-      }
-      const bool full = c0 >= 0 && c0 + W <= vocab;
-#pragma unroll
-      for (int e = 0; e < W; ++e) {
-        if (v[e] > best_v && (full || (c0 + e >= 0 && c0 + e < vocab))) {  // false for NaN; the lowest token on ties
-          best_v = v[e];
-          best_i = c0 + e;
-        }
-      }
-      if (!p.out) continue;
-      if (p.out_dt == DT) {
-        store_cut<DT>(p.out, out_off, c0, vocab, v);
-      } else if (full) {
-#pragma unroll
-        for (int q = 0; q < W / 4; ++q)
-          *(reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + out_off + c0) + q) =
-              make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < W; ++e)
-          if (c0 + e >= 0 && c0 + e < vocab) reinterpret_cast<float*>(p.out)[out_off + c0 + e] = v[e];
       }
     }
-    if (len > 0) __syncthreads();  // the counts are zeroed for the next slab
+    if (n > 0) {
+      __syncthreads();  // the slab is stored
+      for (int i = tid; i < n; i += threads) {
+        const int at = (int)list[i];
+        if (p.out) store_from_f32(p.out, p.out_dt, out_off + s0 + at, value[i]);
+        bits[at >> 5] = 0;
+      }
+      if (tid == 0) listed = 0;
+    }
   }
   if (!p.token) return;
-  unsigned long long best = best_i >= 0 ? choice_key(best_v, best_i) : 0;
+  const unsigned long long streamed = best_i >= 0 ? choice_key(best_v, best_i) : 0;
+  best = streamed > best ? streamed : best;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     const unsigned long long o = __shfl_xor_sync(0xffffffffu, best, off);
     best = o > best ? o : best;
   }
-  if ((threadIdx.x & 31) == 0) best_of[threadIdx.x >> 5] = best;
+  if ((tid & 31) == 0) best_of[tid >> 5] = best;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) best = best_of[w] > best ? best_of[w] : best;
-    block_best = best;
+  if (tid == 0)
+    for (int w = 1; w < (threads >> 5); ++w) best = best_of[w] > best ? best_of[w] : best;
+  if (meet) {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (tid == 0) *cg::this_cluster().map_shared_rank(&cluster_best[rank], 0) = best;
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (rank != 0) return;  // nobody reads this block's shared memory
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (tid == 0)
+      for (int k = 1; k < cluster; ++k) best = cluster_best[k] > best ? cluster_best[k] : best;
   }
-  if (cluster > 1) {
-    cg::cluster_group c = cg::this_cluster();
-    c.sync();
-    if (rank == 0 && threadIdx.x < 32) {
-      best = threadIdx.x < cluster ? *c.map_shared_rank(&block_best, threadIdx.x) : 0;
-#pragma unroll
-      for (int off = 4; off > 0; off >>= 1) {
-        const unsigned long long o = __shfl_xor_sync(0xffffffffu, best, off);
-        best = o > best ? o : best;
-      }
-    }
-    c.sync();  // no block leaves before its best was read
-  }
-  if (rank == 0 && threadIdx.x == 0) p.token[b] = best ? (int32_t)~(uint32_t)best : -1;
+  if (tid == 0) p.token[b] = best ? (int32_t)~(uint32_t)best : -1;
 }
 
 template <int DT, int U, typename COUNT>
-cudaError_t run_logits(const LogitsPlan& p, int threads, int cluster, cudaStream_t s) {
+cudaError_t run_logits(const LogitsPlan& p, int threads, int cluster, int batches, cudaStream_t s) {
   const auto kernel = logits_kernel<DT, U, COUNT>;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -250,29 +376,36 @@ cudaError_t run_logits(const LogitsPlan& p, int threads, int cluster, cudaStream
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(p.batch * cluster));
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = p.history ? (size_t)threads * U * kVec<DT> * sizeof(COUNT) : 0;
+  cfg.dynamicSmemBytes = p.history ? LogitsShared(threads * U * kVec<DT> * batches, sizeof(COUNT), p.max_length).bytes : 0;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
-  if (cfg.dynamicSmemBytes > 48 * 1024) {
+  if (cfg.dynamicSmemBytes > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, kernel, p, cluster);
+  return cudaLaunchKernelEx(&cfg, kernel, p, cluster, batches);
 }
 
 template <int DT>
 cudaError_t run_logits_type(const LogitsPlan& p, cudaStream_t s) {
-  const int64_t vectors = p.vocab / kVec<DT> + 2;
+  constexpr int W = kVec<DT>;
+  const int64_t vectors = p.vocab / W + 2;
   const int threads = (int)std::min<int64_t>(kThreads, (vectors + 31) / 32 * 32);
-  // four vectors a thread once that leaves every SM two blocks; then as many blocks a row as it has slabs
-  const bool many = p.batch * vectors >= (int64_t)device_sm_count() * 2 * 4 * kThreads;
-  const int64_t slabs = (vectors + threads * (many ? 4 : 1) - 1) / (threads * (many ? 4 : 1));
+  // as many blocks a row as give every SM one and a half, but no more than the row has vectors for: 256 rows
+  // of 131072 take 70 us with one or two blocks a row, 76 us with four, 91 us with eight (a block's
+  // work on its slabs' histories does not shrink with them)
   int cluster = 1;
-  while (cluster < 8 && cluster < slabs) cluster *= 2;
-  const bool narrow = p.max_length < (1 << 15);
-  if (many) return narrow ? run_logits<DT, 4, uint16_t>(p, threads, cluster, s) : run_logits<DT, 4, uint32_t>(p, threads, cluster, s);
-  return narrow ? run_logits<DT, 1, uint16_t>(p, threads, cluster, s) : run_logits<DT, 1, uint32_t>(p, threads, cluster, s);
+  while (cluster < 8 && p.batch * cluster * 2 < 3 * device_sm_count() && cluster * threads < vectors) cluster *= 2;
+  // four vectors a thread where a block has that many
+  const int u = vectors >= (int64_t)3 * threads * cluster ? 4 : 1;
+  const bool narrow = p.max_length < (1 << 16);
+  // slabs of at most 64 KB of counts, so that an SM holds two blocks
+  const int64_t room = 64 * 1024 / (threads * u * W * (narrow ? 2 : 4));
+  const int64_t needed = (vectors + (int64_t)threads * u * cluster - 1) / ((int64_t)threads * u * cluster);
+  const int batches = (int)std::max<int64_t>(1, std::min(room, needed));
+  if (u == 4) return narrow ? run_logits<DT, 4, uint16_t>(p, threads, cluster, batches, s) : run_logits<DT, 4, uint32_t>(p, threads, cluster, batches, s);
+  return narrow ? run_logits<DT, 1, uint16_t>(p, threads, cluster, batches, s) : run_logits<DT, 1, uint32_t>(p, threads, cluster, batches, s);
 }
 
 cudaError_t launch_logits(const LogitsPlan& p, cudaStream_t s) {

@@ -3,6 +3,7 @@
 #include <mutex>
 #include <tuple>
 
+#include "async_copy.cuh"
 #include "norm_common.cuh"
 
 namespace hlo {
@@ -22,10 +23,10 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_weight_any_kernel(NormG
   p.ws[(int64_t)blockIdx.y * p.n + c] = acc;
 }
 
-__global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(NormGradPlan p) {
+template <int DROP>
+__global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(const __grid_constant__ NormGradPlan p) {
   __shared__ float red[2 * kAnyThreads / 32];
-  Philox g = {};
-  if (p.drop.on) g = philox_of(p.drop);
+  const Philox<DROP> g(p.drop);
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     int64_t off[5];
     row_offsets(p.map, row, off);
@@ -43,7 +44,8 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(NormGradPlan
       float dh = r * (gy - xh * mean);
       if (p.dsum) dh += load_plain(p.dsum, p.dt, off[2] + c);
       store_from_f32(p.dh, p.dt, off[3] + c, dh);
-      if (p.dx) store_from_f32(p.dx, p.dt, off[4] + c, drop1(p.drop, g, (uint64_t)(row * p.n + c), dh));
+      if constexpr (DROP != DROP_NONE)
+        store_from_f32(p.dx, p.dt, off[4] + c, drop1(p.drop, g, (uint64_t)(row * p.n + c), dh));
     }
     __syncthreads();  // red is used again by the next row
   }
@@ -56,16 +58,15 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(NormGradPlan
 // at c + c / W, so that threads W columns apart meet no bank twice. A thread adds to a column only behind
 // its group's barrier of that row, so two rows never add to one at once. The groups' sums go to the
 // workspace, and norm_grad_join_kernel adds them in order.
-template <int DT, int K, bool DROP, bool CUT>
-__global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(NormGradPlan p, int weight_whole, int64_t groups) {
+template <int DT, int K, int DROP, bool CUT>
+__global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(const __grid_constant__ NormGradPlan p, int weight_whole, int64_t groups) {
   constexpr int W = kVec<DT>, EB = 16 / W;
   __shared__ float red[2][64];
   extern __shared__ float dw_shared[];
   const int n = (int)p.n;
   const int64_t group = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (group >= groups) return;  // the whole group: its barrier is its own
-  Philox g = {};
-  if (DROP) g = philox_of(p.drop);
+  const Philox<DROP> g(p.drop);
   float acc[K][W];
   float* const cols = CUT ? dw_shared + (int)threadIdx.y * (n + n / W + 1) : nullptr;
   if (CUT) {
@@ -91,9 +92,9 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(Norm
       yr[k] = hr[k] = sr[k] = make_uint4(0, 0, 0, 0);
       if (c0 >= n) continue;
       if (CUT) {
-        yr[k] = load_cut<DT>(p.dy, off[0], c0, p.n);
-        hr[k] = load_cut<DT>(p.h, off[1], c0, p.n);
-        if (p.dsum) sr[k] = load_cut<DT>(p.dsum, off[2], c0, p.n);
+        yr[k] = load_cut<DT>(p.dy, off[0], c0, n, p.end[0]);
+        hr[k] = load_cut<DT>(p.h, off[1], c0, n, p.end[1]);
+        if (p.dsum) sr[k] = load_cut<DT>(p.dsum, off[2], c0, n, p.end[2]);
       } else {
         yr[k] = load16(reinterpret_cast<const char*>(p.dy) + (off[0] + c0) * EB);
         hr[k] = load16(reinterpret_cast<const char*>(p.h) + (off[1] + c0) * EB);
@@ -137,8 +138,8 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(Norm
       }
       if (CUT) store_cut<DT>(p.dh, off[3], c0, n, d);
       else *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.dh) + (off[3] + c0) * EB) = pack<DT>(d);
-      if (DROP) {
-        drop_vec<W>(p.drop, g, row * n + c0, d);
+      if constexpr (DROP != DROP_NONE) {
+        drop_vec<DROP, !CUT, W>(p.drop, g, row * n + c0, d);
         if (CUT) store_cut<DT>(p.dx, off[4], c0, n, d);
         else *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.dx) + (off[4] + c0) * EB) = pack<DT>(d);
       }
@@ -159,6 +160,142 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(Norm
       for (int q = 0; q < W / 4; ++q)
         *(reinterpret_cast<float4*>(out + c0) + q) = make_float4(acc[k][4 * q], acc[k][4 * q + 1], acc[k][4 * q + 2], acc[k][4 * q + 3]);
     }
+  }
+}
+
+// ---- gradient, rows streamed through shared memory ---------------------------------------------------------
+// For many aligned rows, a fixed stride apart: persistent blocks, a row at a time; thread 0 keeps a ring of `stages` rows (dy, h and
+// dsum) coming with bulk copies, so the loads never wait for the row's reduction. K vectors a thread.
+// One barrier a row: it joins the warps' dot products, and behind it every thread has left the row
+// before, whose stage is refilled then. Sums are formed with packed f32x2 instructions.
+constexpr int kMaxStages = 8;
+
+template <int DT, int K, int DROP, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) norm_grad_stream_kernel(const __grid_constant__ NormGradPlan p, int stages, int weight_whole) {
+  constexpr int W = kVec<DT>, EB = 16 / W, H = W / 2;
+  extern __shared__ __align__(128) char ring[];
+  __shared__ __align__(8) uint64_t full[kMaxStages];
+  __shared__ float red[2][16];
+  const int n = (int)p.n, tid = threadIdx.x, warps = blockDim.x >> 5;
+  const int row_bytes = n * EB, stage_bytes = row_bytes * (p.dsum ? 3 : 2);
+  const int mine = (int)((p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);  // rows of this block
+  const auto request = [&](int i) {
+    const int s = i % stages;
+    const int64_t row = (int64_t)blockIdx.x + (int64_t)i * gridDim.x;
+    const uint32_t bar = smem_addr(&full[s]);
+    char* const to = ring + (size_t)s * stage_bytes;
+    mbar_arrive_expect_tx(bar, stage_bytes);
+    bulk_load(to, reinterpret_cast<const char*>(p.dy) + row * p.map.stride[0][0] * EB, row_bytes, bar);
+    bulk_load(to + row_bytes, reinterpret_cast<const char*>(p.h) + row * p.map.stride[1][0] * EB, row_bytes, bar);
+    if (p.dsum) bulk_load(to + 2 * row_bytes, reinterpret_cast<const char*>(p.dsum) + row * p.map.stride[2][0] * EB, row_bytes, bar);
+  };
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(smem_addr(&full[s]), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (tid == 0)
+    for (int i = 0; i < min(stages, mine); ++i) request(i);
+  const Philox<DROP> g(p.drop);
+  float2 acc[K][H];
+  // the weights stay packed in registers where they are of the rows' type, and come from the caches otherwise
+  const bool packed = p.w && p.w_dt == DT && weight_whole;
+  uint4 wr[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c0 = (int)(tid + k * blockDim.x) * W;
+    wr[k] = packed && c0 < n ? __ldg(reinterpret_cast<const uint4*>(p.w) + c0 / W) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < H; ++e) acc[k][e] = make_float2(0.0f, 0.0f);
+  }
+  const auto weights = [&](int k, float2 (&w)[H]) {
+    if (packed) {
+      unpack2<DT>(wr[k], w);
+      if (p.w_offset != 0.0f) {
+#pragma unroll
+        for (int e = 0; e < H; ++e) w[e] = __fadd2_rn(w[e], make_float2(p.w_offset, p.w_offset));
+      }
+      return;
+    }
+    float f[W];
+    load_weights<DT>(p.w, p.w_dt, p.w_offset, (int)(tid + k * blockDim.x) * W, n, weight_whole, f);
+#pragma unroll
+    for (int e = 0; e < H; ++e) w[e] = make_float2(f[2 * e], f[2 * e + 1]);
+  };
+  float r_next = p.rstd[blockIdx.x];
+  for (int i = 0; i < mine; ++i) {
+    const int64_t row = (int64_t)blockIdx.x + (int64_t)i * gridDim.x;
+    const int s = i % stages;
+    const float r = r_next;
+    if (i + 1 < mine) r_next = p.rstd[row + gridDim.x];
+    const bool arrived = mbar_wait(smem_addr(&full[s]), (i / stages) & 1);
+    const char* const stage = ring + (size_t)s * stage_bytes;
+    float2 dot2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int at = (int)(tid + k * blockDim.x) * 16;
+      if (at >= row_bytes) continue;
+      float2 y[H], h[H], w[H];
+      unpack2<DT>(*reinterpret_cast<const uint4*>(stage + at), y);
+      unpack2<DT>(*reinterpret_cast<const uint4*>(stage + row_bytes + at), h);
+      weights(k, w);
+#pragma unroll
+      for (int e = 0; e < H; ++e) dot2 = __ffma2_rn(__fmul2_rn(y[e], w[e]), h[e], dot2);
+    }
+    const float part = warp_sum(dot2.x + dot2.y);
+    if ((tid & 31) == 0) red[i & 1][tid >> 5] = part;
+    if (!__syncthreads_and(arrived)) {  // a copy did not come: give up, when the others have come or their waits run out
+      if (tid == 0) {
+        record_fault(kFaultCopyTimeout);
+        for (int j = i; j < min(i + stages - (i > 0 ? 1 : 0), mine); ++j) mbar_wait(smem_addr(&full[j % stages]), (j / stages) & 1);
+      }
+      __syncthreads();
+      if (p.dw)
+        for (int c = tid; c < n; c += blockDim.x) p.ws[(int64_t)blockIdx.x * n + c] = __int_as_float(0x7FC00000);
+      return;
+    }
+    if (tid == 0 && i > 0 && i - 1 + stages < mine) request(i - 1 + stages);
+    float dot = 0.0f;
+    for (int q = 0; q < warps; ++q) dot += red[i & 1][q];
+    // h holds xh = h r from here on; mean(g xh) = r sum(g h) / n
+    const float mean = __fdiv_rn(dot * r, (float)n);
+    const float2 r2 = make_float2(r, r), m2 = make_float2(-mean, -mean);
+    char* const dh = reinterpret_cast<char*>(p.dh) + row * p.map.stride[3][0] * EB;
+    char* const dx = reinterpret_cast<char*>(p.dx) + row * p.map.stride[4][0] * EB;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c0 = (int)(tid + k * blockDim.x) * W;
+      if (c0 >= n) continue;
+      float2 y[H], h[H], w[H];
+      float d[W];
+      unpack2<DT>(*reinterpret_cast<const uint4*>(stage + c0 * EB), y);
+      unpack2<DT>(*reinterpret_cast<const uint4*>(stage + row_bytes + c0 * EB), h);
+      weights(k, w);
+      if (p.dsum) unpack<DT>(*reinterpret_cast<const uint4*>(stage + 2 * row_bytes + c0 * EB), d);
+#pragma unroll
+      for (int e = 0; e < H; ++e) {
+        const float2 xh = __fmul2_rn(h[e], r2);
+        acc[k][e] = __ffma2_rn(y[e], xh, acc[k][e]);
+        const float2 t = __ffma2_rn(xh, m2, __fmul2_rn(y[e], w[e]));
+        const float2 o = __ffma2_rn(t, r2, p.dsum ? make_float2(d[2 * e], d[2 * e + 1]) : make_float2(0.0f, 0.0f));
+        d[2 * e] = o.x, d[2 * e + 1] = o.y;
+      }
+      *reinterpret_cast<uint4*>(dh + c0 * EB) = pack<DT>(d);
+      if constexpr (DROP != DROP_NONE) {
+        drop_vec<DROP, true, W>(p.drop, g, row * n + c0, d);
+        *reinterpret_cast<uint4*>(dx + c0 * EB) = pack<DT>(d);
+      }
+    }
+  }
+  if (!p.dw) return;
+  float* const out = p.ws + (int64_t)blockIdx.x * n;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c0 = (int)(tid + k * blockDim.x) * W;
+    if (c0 >= n) continue;
+#pragma unroll
+    for (int q = 0; q < H; q += 2)
+      *reinterpret_cast<float4*>(out + c0 + 2 * q) = make_float4(acc[k][q].x, acc[k][q].y, acc[k][q + 1].x, acc[k][q + 1].y);
   }
 }
 
@@ -198,8 +335,8 @@ cudaError_t resident_blocks(const void* kernel, int threads, size_t smem, int* b
     *blocks = it->second;
     return cudaSuccess;
   }
-  if (smem > 48 * 1024) {  // to the most that this library asks for, whatever the order of the calls
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
+  if (smem > 40 * 1024) {  // to the most that this library asks for, whatever the order of the calls
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
     if (e != cudaSuccess) return e;
   }
   int n = 0;
@@ -210,7 +347,7 @@ cudaError_t resident_blocks(const void* kernel, int threads, size_t smem, int* b
   return cudaSuccess;
 }
 
-template <int DT, int K, bool DROP, bool CUT>
+template <int DT, int K, int DROP, bool CUT>
 cudaError_t run_norm_grad_row(const NormGradPlan& p, const RowShape& r, int whole, int64_t* groups, cudaStream_t s) {
   const auto kernel = norm_grad_row_kernel<DT, K, DROP, CUT>;
   const size_t smem = CUT && p.dw ? (size_t)r.ty * (p.n + p.n / kVec<DT> + 1) * 4 : 0;
@@ -224,16 +361,67 @@ cudaError_t run_norm_grad_row(const NormGradPlan& p, const RowShape& r, int whol
 
 template <int DT>
 cudaError_t run_norm_grad(const NormGradPlan& p, const RowShape& r, bool cut, int whole, int64_t* groups, cudaStream_t s) {
-  const bool drop = p.drop.on;
-#define HLO_CASE(KK)                                                                                             \
-  if (r.k == KK)                                                                                                 \
-    return cut ? (drop ? run_norm_grad_row<DT, KK, true, true>(p, r, whole, groups, s)                           \
-                       : run_norm_grad_row<DT, KK, false, true>(p, r, whole, groups, s))                         \
-               : (drop ? run_norm_grad_row<DT, KK, true, false>(p, r, whole, groups, s)                          \
-                       : run_norm_grad_row<DT, KK, false, false>(p, r, whole, groups, s))
-  HLO_CASE(1);
-  HLO_CASE(2);
-  HLO_CASE(4);
+#define HLO_CASE(KK, DD)                                                                                 \
+  if (r.k == KK && p.drop.mode == DD)                                                                  \
+  return cut ? run_norm_grad_row<DT, KK, DD, true>(p, r, whole, groups, s) : run_norm_grad_row<DT, KK, DD, false>(p, r, whole, groups, s)
+  HLO_CASE(1, DROP_NONE);
+  HLO_CASE(1, DROP_HOST);
+  HLO_CASE(1, DROP_DEVICE);
+  HLO_CASE(2, DROP_NONE);
+  HLO_CASE(2, DROP_HOST);
+  HLO_CASE(2, DROP_DEVICE);
+  HLO_CASE(4, DROP_NONE);
+  HLO_CASE(4, DROP_HOST);
+  HLO_CASE(4, DROP_DEVICE);
+#undef HLO_CASE
+  return cudaErrorInvalidValue;
+}
+
+template <int DT, int K, int DROP>
+cudaError_t run_norm_grad_stream(const NormGradPlan& p, int threads, int stages, size_t smem, int whole, int64_t* groups, cudaStream_t s) {
+  const auto kernel = K == 1 || (K == 2 && threads <= 256) ? norm_grad_stream_kernel<DT, K, DROP, K == 4 ? 512 : 256>
+                                                       : norm_grad_stream_kernel<DT, K, DROP, K == 1 ? 256 : 512>;
+  int per_sm = 1;
+  const cudaError_t e = resident_blocks((const void*)kernel, threads, smem, &per_sm);
+  if (e != cudaSuccess) return e;
+  *groups = std::min({p.rows, norm_grad_partials(p.rows, p.n), (int64_t)device_sm_count() * per_sm});
+  kernel<<<(unsigned)*groups, threads, smem, s>>>(p, stages, whole);
+  return cudaGetLastError();
+}
+
+// The ring's shape for rows of `vectors` vectors; 0 stages: the rows do not fit.
+struct RingShape {
+  int k, threads, stages;
+  size_t smem;
+};
+RingShape ring_shape(int64_t vectors, int arrays) {
+  RingShape r = {};
+  r.k = vectors > 1024 ? 4 : vectors > 128 ? 2 : 1;
+  r.threads = (int)((vectors + r.k - 1) / r.k + 31) / 32 * 32;
+  const size_t stage = (size_t)vectors * 16 * arrays;
+  // 768 threads an SM: 8192 x 4096 bf16 takes 52 us, with 512 threads 58 us, with 256 85 us
+  const int blocks = std::max(1, std::min(16, 768 / r.threads));
+  const size_t room = (size_t)220 * 1024 / blocks - 1024;
+  r.stages = (int)std::min<size_t>(kMaxStages, room / stage);
+  if (r.stages < 2) r.stages = (int)std::min<size_t>(2, (size_t)224 * 1024 / stage);
+  if (r.stages < 2 || r.threads > 512) r.stages = 0;
+  r.smem = stage * r.stages;
+  return r;
+}
+
+template <int DT>
+cudaError_t run_norm_grad_ring(const NormGradPlan& p, const RingShape& r, int whole, int64_t* groups, cudaStream_t s) {
+#define HLO_CASE(KK, DD) \
+  if (r.k == KK && p.drop.mode == DD) return run_norm_grad_stream<DT, KK, DD>(p, r.threads, r.stages, r.smem, whole, groups, s)
+  HLO_CASE(1, DROP_NONE);
+  HLO_CASE(1, DROP_HOST);
+  HLO_CASE(1, DROP_DEVICE);
+  HLO_CASE(2, DROP_NONE);
+  HLO_CASE(2, DROP_HOST);
+  HLO_CASE(2, DROP_DEVICE);
+  HLO_CASE(4, DROP_NONE);
+  HLO_CASE(4, DROP_HOST);
+  HLO_CASE(4, DROP_DEVICE);
 #undef HLO_CASE
   return cudaErrorInvalidValue;
 }
@@ -246,9 +434,15 @@ cudaError_t launch_norm_grad(const NormGradPlan& p, cudaStream_t s) {
   const int64_t vectors = (p.n + w - 1) / w + 1;
   int64_t groups = norm_grad_partials(p.rows, p.n);
   if (vectors <= 512 * 4 && vectors_fit<5>(p.map, ptr, ebs, p.n, w, &cut)) {
-    const RowShape r = row_shape(p.rows, vectors - (cut ? 0 : 1), 4);
+    const RowShape r = row_shape(p.rows, vectors - (cut ? 0 : 1), 4, 64);
     const int whole = p.w && (uintptr_t)p.w % 16 == 0;
-    const cudaError_t e = p.dt == F32    ? run_norm_grad<F32>(p, r, cut, whole, &groups, s)
+    // the ring pays once its blocks have several rows each
+    const RingShape ring = ring_shape(vectors - 1, p.dsum ? 3 : 2);
+    const bool stream = !cut && ring.stages > 0 && p.map.n <= 1 && p.rows >= 4 * device_sm_count();
+    const cudaError_t e = stream ? (p.dt == F32    ? run_norm_grad_ring<F32>(p, ring, whole, &groups, s)
+                                    : p.dt == BF16 ? run_norm_grad_ring<BF16>(p, ring, whole, &groups, s)
+                                                   : run_norm_grad_ring<F16>(p, ring, whole, &groups, s))
+                          : p.dt == F32    ? run_norm_grad<F32>(p, r, cut, whole, &groups, s)
                           : p.dt == BF16 ? run_norm_grad<BF16>(p, r, cut, whole, &groups, s)
                                          : run_norm_grad<F16>(p, r, cut, whole, &groups, s);
     if (e != cudaSuccess) return e;
@@ -257,7 +451,9 @@ cudaError_t launch_norm_grad(const NormGradPlan& p, cudaStream_t s) {
       const unsigned cols = (unsigned)((p.n + kAnyThreads - 1) / kAnyThreads);
       norm_grad_weight_any_kernel<<<dim3(cols, (unsigned)groups), kAnyThreads, 0, s>>>(p);
     }
-    norm_grad_any_kernel<<<any_grid(p.rows), kAnyThreads, 0, s>>>(p);
+    if (p.drop.mode == DROP_NONE) norm_grad_any_kernel<DROP_NONE><<<any_grid(p.rows), kAnyThreads, 0, s>>>(p);
+    else if (p.drop.mode == DROP_HOST) norm_grad_any_kernel<DROP_HOST><<<any_grid(p.rows), kAnyThreads, 0, s>>>(p);
+    else norm_grad_any_kernel<DROP_DEVICE><<<any_grid(p.rows), kAnyThreads, 0, s>>>(p);
   }
   if (p.dw) norm_grad_join_kernel<<<(unsigned)((p.n + 31) / 32), dim3(32, 32), 0, s>>>(p.ws, p.dw, p.n, groups);
   return cudaGetLastError();

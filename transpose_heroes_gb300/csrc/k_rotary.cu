@@ -21,8 +21,7 @@ struct Piece {
   static constexpr int EB = DT == F32 ? 4 : 2;
   static constexpr int N = V * EB >= 4 ? V * EB / 4 : 1;
   uint32_t u[N];
-  __device__ __forceinline__ void load(const void* p, int64_t i) {
-    const char* a = reinterpret_cast<const char*>(p) + i * EB;
+  __device__ __forceinline__ void load(const char* a) {
     if constexpr (V * EB == 16) {
       const uint4 w = load16(a);
       u[0] = w.x, u[1] = w.y, u[2] = w.z, u[3] = w.w;
@@ -35,8 +34,7 @@ struct Piece {
       u[0] = __ldcs(reinterpret_cast<const uint16_t*>(a));
     }
   }
-  __device__ __forceinline__ void store(void* p, int64_t i) const {
-    char* a = reinterpret_cast<char*>(p) + i * EB;
+  __device__ __forceinline__ void store(char* a) const {
     if constexpr (V * EB == 16) *reinterpret_cast<uint4*>(a) = make_uint4(u[0], u[1], u[2], u[3]);
     else if constexpr (V * EB == 8) *reinterpret_cast<uint2*>(a) = make_uint2(u[0], u[1]);
     else if constexpr (V * EB == 4) *reinterpret_cast<uint32_t*>(a) = u[0];
@@ -71,123 +69,121 @@ struct Piece {
   }
 };
 
+// How a block's 256 threads share its work: a thread has one item (two accesses of V elements) of a head, at
+// one token, in every slots-th head of the block's share.
 struct RotaryTile {
-  int tokens;        // tokens a block
-  int heads;         // heads (of both arrays together) a block
-  int per_head;      // items a head: turned ones, then copied ones
-  int turned;        // pairs / V
-  int copied;        // copied elements / V
+  int items;    // of a head: the turned ones, then the copied ones
+  int turned;   // pairs / V
+  int copied;   // copied elements / V
+  int slots;    // threads (of one item and token) that share the heads
+  int tokens;   // tokens a block
+  int heads;    // heads a block (of x's and then y's)
 };
 
-// A block turns `heads` heads (of x's and then y's) of `tokens` tokens. It first computes the cosine and sine of
-// each (token, pair) once, into shared memory; an item is then two accesses of V elements: the two halves
-// of V pairs (half layout) or V adjacent pairs (interleaved), or 2 V copied elements. Each thread issues the loads
-// of its first U items before the cosines are there.
+// A block first computes the cosine and sine of each (token, pair) once, into shared memory. An item is the
+// two halves of V pairs (half layout), V adjacent pairs (interleaved), or 2 V copied elements; a thread's
+// item and token stay, so the places of its elements and its cosines are found once for U heads. The
+// loads of the first U heads are issued before the cosines are computed.
 template <int DT, int V, int U, bool INTER>
-__global__ void __launch_bounds__(256) rotary_kernel(RotaryPlan p, RotaryTile t, int64_t total_tokens, int total_heads) {
+__global__ void __launch_bounds__(256, 3) rotary_kernel(const __grid_constant__ RotaryPlan p, const RotaryTile t, int total_tokens,
+                                                     int total_heads) {
   extern __shared__ float2 cs[];
-  const int64_t token0 = (int64_t)blockIdx.x * t.tokens;
-  const int tokens = (int)(total_tokens - token0 < t.tokens ? total_tokens - token0 : t.tokens);
-  const int head0 = blockIdx.y * t.heads;
-  const int heads = total_heads - head0 < t.heads ? total_heads - head0 : t.heads;
-  const int items = tokens * heads * t.per_head;
-  for (int base = 0; base < items; base += 256 * U) {
+  const int token0 = blockIdx.x * t.tokens;
+  const int tokens = min(t.tokens, total_tokens - token0);
+  const int head_end = min(total_heads, (int)(blockIdx.y + 1) * t.heads);
+  const int group = threadIdx.x / t.items, k = threadIdx.x - group * t.items;
+  const int tok = group / t.slots;
+  const int head0 = blockIdx.y * t.heads + group - tok * t.slots;
+  const bool busy = tok < tokens;
+  const bool turn = k < t.turned;
+  const int ea = turn ? (INTER ? 2 * k * V : k * V) : 2 * p.pairs + 2 * (k - t.turned) * V;
+  const int eb = turn ? (INTER ? ea + V : ea + p.pairs) : (2 * (k - t.turned) + 1 < t.copied ? ea + V : -1);
+  const int split = (int)p.a[0].heads;  // heads from here on are y's
+  const char* in[2] = {nullptr, nullptr};
+  char* out[2] = {nullptr, nullptr};
+  constexpr int EB = DT == F32 ? 4 : 2;
+  if (busy) {
+    const uint32_t g = (uint32_t)(token0 + tok), bi = p.batch > 1 ? g / (uint32_t)p.seq : 0, si = g - bi * (uint32_t)p.seq;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      in[a] = reinterpret_cast<const char*>(p.a[a].in) + (bi * p.a[a].in_stride[0] + si * p.a[a].in_stride[1] + ea) * EB;
+      out[a] = reinterpret_cast<char*>(p.a[a].out) + (bi * p.a[a].out_stride[0] + si * p.a[a].out_stride[1] + ea) * EB;
+    }
+  }
+  const int64_t second = (int64_t)(eb - ea) * EB;
+  float2 w[V];
+  for (int base = head0;; base += U * t.slots) {
     Piece<DT, V> a[U], b[U];
-    int64_t out_at[U];
-    int where[U];  // cosines' place, or -1: copied
-    int ea[U], eb[U], which[U];
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      const int i = base + q * 256 + threadIdx.x;
-      which[q] = -1;
-      if (i >= items) continue;
-      const int hi = i / t.per_head, k = i - hi * t.per_head;
-      const int tok = hi / heads;
-      int head = head0 + hi - tok * heads;
-      which[q] = p.arrays > 1 && head >= p.a[0].heads ? 1 : 0;
-      const RotaryArray& r = which[q] ? p.a[1] : p.a[0];
-      if (which[q]) head -= (int)p.a[0].heads;
-      const uint32_t g = (uint32_t)(token0 + tok), bi = p.batch > 1 ? g / (uint32_t)p.seq : 0, si = g - bi * (uint32_t)p.seq;
-      const int64_t in = bi * r.in_stride[0] + si * r.in_stride[1] + head * r.in_stride[2];
-      out_at[q] = bi * r.out_stride[0] + si * r.out_stride[1] + head * r.out_stride[2];
-      if (k < t.turned) {
-        where[q] = tok * p.pairs + k * V;
-        ea[q] = INTER ? 2 * k * V : k * V;
-        eb[q] = INTER ? ea[q] + V : ea[q] + p.pairs;
-      } else {
-        where[q] = -1;
-        ea[q] = 2 * p.pairs + 2 * (k - t.turned) * V;
-        eb[q] = 2 * (k - t.turned) + 1 < t.copied ? ea[q] + V : -1;
-      }
-      a[q].load(r.in, in + ea[q]);
-      if (eb[q] >= 0) b[q].load(r.in, in + eb[q]);
+      const int head = base + q * t.slots;
+      if (!busy || head >= head_end) continue;
+      const char* const at = head < split ? in[0] + head * p.a[0].in_stride[2] * EB : in[1] + (head - split) * p.a[1].in_stride[2] * EB;
+      a[q].load(at);
+      if (eb >= 0) b[q].load(at + second);
     }
-    if (base == 0) {
+    if (base == head0) {
       for (int i = threadIdx.x; i < tokens * p.pairs; i += 256) {
-        const int tok = i / p.pairs, k = i - tok * p.pairs;
-        const uint32_t g = (uint32_t)(token0 + tok), bi = p.batch > 1 ? g / (uint32_t)p.seq : 0, si = g - bi * (uint32_t)p.seq;
-        cs[i] = cos_sin(p, p.pos[bi * p.pos_stride[0] + si * p.pos_stride[1]], __ldg(reinterpret_cast<const unsigned long long*>(p.turns) + k));
+        const int tk = i / p.pairs, pair = i - tk * p.pairs;
+        const uint32_t g = (uint32_t)(token0 + tk), bi = p.batch > 1 ? g / (uint32_t)p.seq : 0, si = g - bi * (uint32_t)p.seq;
+        cs[i] = cos_sin(p, p.pos[bi * p.pos_stride[0] + si * p.pos_stride[1]], __ldg(reinterpret_cast<const unsigned long long*>(p.turns) + pair));
       }
       __syncthreads();
+      if (!busy) return;
+      if (turn) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) w[e] = cs[tok * p.pairs + k * V + e];
+      }
     }
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      if (which[q] < 0) continue;
-      void* const out = which[q] ? p.a[1].out : p.a[0].out;
-      if (where[q] >= 0) {
+      const int head = base + q * t.slots;
+      if (head >= head_end) continue;
+      if (turn) {
         float u[V], v[V];
         a[q].get(u);
         b[q].get(v);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float2 w = cs[where[q] + e];
           if constexpr (!INTER || V == 1) {
             const float x = u[e], y = v[e];
-            u[e] = x * w.x - y * w.y;
-            v[e] = y * w.x + x * w.y;
+            u[e] = x * w[e].x - y * w[e].y;
+            v[e] = y * w[e].x + x * w[e].y;
           } else {
             float& x = 2 * e < V ? u[2 * e] : v[2 * e - V];
             float& y = 2 * e < V ? u[2 * e + 1] : v[2 * e + 1 - V];
             const float x0 = x, y0 = y;
-            x = x0 * w.x - y0 * w.y;
-            y = y0 * w.x + x0 * w.y;
+            x = x0 * w[e].x - y0 * w[e].y;
+            y = y0 * w[e].x + x0 * w[e].y;
           }
         }
         a[q].set(u);
         b[q].set(v);
       }
-      a[q].store(out, out_at[q] + ea[q]);
-      if (eb[q] >= 0) b[q].store(out, out_at[q] + eb[q]);
+      char* const at = head < split ? out[0] + head * p.a[0].out_stride[2] * EB : out[1] + (head - split) * p.a[1].out_stride[2] * EB;
+      a[q].store(at);
+      if (eb >= 0) b[q].store(at + second);
     }
+    if (base + U * t.slots >= head_end) break;
   }
 }
 
+// Heads a thread turns at a time: 4 accesses of 2 x 16 bytes in flight once the device is full.
 template <int DT, int V, int U>
-cudaError_t run_rotary(const RotaryPlan& p, cudaStream_t s) {
-  const int64_t tokens = p.batch * p.seq;
-  const int64_t heads = p.a[0].heads + (p.arrays > 1 ? p.a[1].heads : 0);
-  RotaryTile t;
-  t.turned = p.pairs / V;
-  t.copied = (p.dim - 2 * p.pairs) / V;
-  bool in_place = true;
-  for (int k = 0; k < p.arrays; ++k) in_place = in_place && p.a[k].in == p.a[k].out;
-  if (in_place) t.copied = 0;
-  t.per_head = t.turned + (t.copied + 1) / 2;
-  if (t.per_head == 0) return cudaSuccess;  // nothing turns, and nothing has to be copied
-  // whole heads, then whole tokens, up to 256 U items; never more cosines than 40 KB hold
-  const int64_t most = 256 * U;
-  t.heads = (int)std::max<int64_t>(1, std::min(heads, most / t.per_head));
-  const int64_t cap = p.pairs ? std::max<int64_t>(1, 5120 / p.pairs) : most;
-  t.tokens = t.heads < heads ? 1 : (int)std::max<int64_t>(1, std::min({tokens, most / (heads * t.per_head), cap}));
-  const int64_t gx = (tokens + t.tokens - 1) / t.tokens, gy = (heads + t.heads - 1) / t.heads;
-  if (gx > INT32_MAX || gy > 65535) return cudaErrorInvalidValue;
+cudaError_t run_rotary(const RotaryPlan& p, const RotaryTile& tile, cudaStream_t s) {
+  RotaryTile t = tile;
+  const int tokens = (int)(p.batch * p.seq);
+  const int heads = (int)(p.a[0].heads + (p.arrays > 1 ? p.a[1].heads : 0));
+  const int groups = 256 / t.items;
+  // U heads a thread: then as many tokens a block as there are threads for, but not more than 40 KB of cosines
+  t.slots = std::min(groups, (heads + U - 1) / U);
+  const int cap = p.pairs ? std::max(1, 5120 / p.pairs) : groups;
+  t.tokens = std::max(1, std::min({groups / t.slots, tokens, cap}));
+  t.heads = std::min(heads, t.slots * U);
+  const int gx = (tokens + t.tokens - 1) / t.tokens, gy = (heads + t.heads - 1) / t.heads;
   const size_t smem = (size_t)t.tokens * p.pairs * sizeof(float2);
-  const auto kernel = p.interleaved ? rotary_kernel<DT, V, U, true> : rotary_kernel<DT, V, U, false>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  kernel<<<dim3((unsigned)gx, (unsigned)gy), 256, smem, s>>>(p, t, tokens, (int)heads);
+  if (p.interleaved) rotary_kernel<DT, V, U, true><<<dim3(gx, gy), 256, smem, s>>>(p, t, tokens, heads);
+  else rotary_kernel<DT, V, U, false><<<dim3(gx, gy), 256, smem, s>>>(p, t, tokens, heads);
   return cudaGetLastError();
 }
 
@@ -234,13 +230,12 @@ int access_width(const RotaryPlan& p) {
 }
 
 template <int DT>
-cudaError_t run_rotary_type(const RotaryPlan& p, cudaStream_t s) {
+cudaError_t run_rotary_type(const RotaryPlan& p, int v, const RotaryTile& t, cudaStream_t s) {
   const int64_t heads = p.a[0].heads + (p.arrays > 1 ? p.a[1].heads : 0);
-  const int v = access_width(p);
-  // several items a thread once one each fills the device
-  const bool many = p.batch * p.seq * heads * (p.dim / 2) / v >= (int64_t)device_sm_count() * 4 * 1024;
+  // several heads a thread once one each fills the device twice over
+  const bool many = p.batch * p.seq * heads * t.items >= (int64_t)device_sm_count() * 8 * 1024;
 #define HLO_CASE(VV) \
-  if (v == VV) return many ? run_rotary<DT, VV, 4>(p, s) : run_rotary<DT, VV, 1>(p, s)
+  if (v == VV) return many ? run_rotary<DT, VV, 4>(p, t, s) : run_rotary<DT, VV, 1>(p, t, s)
   if constexpr (DT != F32) HLO_CASE(8);
   HLO_CASE(4);
   HLO_CASE(2);
@@ -250,11 +245,20 @@ cudaError_t run_rotary_type(const RotaryPlan& p, cudaStream_t s) {
 }
 
 cudaError_t launch_rotary(const RotaryPlan& p, cudaStream_t s) {
+  const int v = access_width(p);
+  RotaryTile t = {};
+  t.turned = p.pairs / v;
+  t.copied = (p.dim - 2 * p.pairs) / v;
+  bool in_place = true;
+  for (int k = 0; k < p.arrays; ++k) in_place = in_place && p.a[k].in == p.a[k].out;
+  if (in_place) t.copied = 0;
+  t.items = t.turned + (t.copied + 1) / 2;
+  if (t.items == 0) return cudaSuccess;  // nothing turns, and nothing has to be copied
   const int64_t heads = std::max(p.a[0].heads, p.arrays > 1 ? p.a[1].heads : 0);
-  if (p.batch <= INT32_MAX / p.seq && p.pairs <= 8192 && heads <= 65535 / 4) {
-    if (p.dt == F32) return run_rotary_type<F32>(p, s);
-    if (p.dt == BF16) return run_rotary_type<BF16>(p, s);
-    return run_rotary_type<F16>(p, s);
+  if (t.items <= 256 && p.pairs <= 4096 && p.batch <= INT32_MAX / p.seq && heads <= 32767) {
+    if (p.dt == F32) return run_rotary_type<F32>(p, v, t, s);
+    if (p.dt == BF16) return run_rotary_type<BF16>(p, v, t, s);
+    return run_rotary_type<F16>(p, v, t, s);
   }
   for (int k = 0; k < p.arrays; ++k) {
     const int64_t total = p.batch * p.seq * p.a[k].heads * (p.dim - p.pairs);

@@ -7,6 +7,7 @@
 
 #include "hlo_api.h"
 #include "layer_plans.h"
+#include "philox.cuh"
 
 using namespace hlo;
 
@@ -28,6 +29,10 @@ int64_t numel(const hlo_view& v) {
   int64_t n = 1;
   for (int d = 0; d < v.rank; ++d) n *= v.dims[d];
   return n;
+}
+
+const char* end_of(const hlo_view* v, const void* ptr) {
+  return v ? static_cast<const char*>(ptr) + span(*v) * view_dt_bytes(v->dtype) : nullptr;
 }
 
 hlo_status check_view(const hlo_view* v, const void* ptr, const char* what, bool output) {
@@ -182,12 +187,13 @@ Rows<NV> merge_rows(const hlo_view* const (&views)[NV], int last) {
   return m;
 }
 
-hlo_status check_dropout(const hlo_dropout_params* d, DropPlan* out) {
+// `count`: the elements that are numbered.
+hlo_status check_dropout(const hlo_dropout_params* d, int64_t count, DropPlan* out) {
   std::memset(out, 0, sizeof *out);
   if (!d) return HLO_OK;
   if (!(d->p >= 0.0 && d->p <= 1.0)) return api_fail(HLO_ERR_INVALID_ARG, "dropout: p = %g outside 0..1", d->p);
   if ((uintptr_t)d->state % 8 != 0) return api_fail(HLO_ERR_INVALID_ARG, "dropout: state is not 8-byte aligned");
-  out->on = 1;
+  out->mode = d->state || count > (int64_t)1 << 34 ? DROP_DEVICE : DROP_HOST;
   const double threshold = std::floor(d->p * 4294967296.0 + 0.5);
   out->all = threshold >= 4294967296.0;
   out->threshold = out->all ? 0xFFFFFFFFu : (uint32_t)threshold;
@@ -195,6 +201,7 @@ hlo_status check_dropout(const hlo_dropout_params* d, DropPlan* out) {
   out->seed = d->seed;
   out->offset = d->offset;
   out->state = d->state;
+  philox_constants(out, d->seed, d->offset);
   return HLO_OK;
 }
 
@@ -247,7 +254,7 @@ hlo_status hlo_rms_norm(const hlo_view* x, const void* x_ptr, const hlo_view* re
   if (!(eps >= 0.0) || !std::isfinite(eps)) return api_fail(HLO_ERR_INVALID_ARG, "rms_norm: eps must be finite and >= 0");
   NormPlan p;
   std::memset(&p, 0, sizeof p);
-  TRY(check_dropout(dropout, &p.drop));
+  TRY(check_dropout(dropout, numel(*x), &p.drop));
   const int od = out->dtype;
   if (scales) {
     if (od != HLO_S8 && od != HLO_F8E4M3FN)
@@ -306,6 +313,8 @@ hlo_status hlo_rms_norm(const hlo_view* x, const void* x_ptr, const hlo_view* re
   p.eps = (float)eps;
   const hlo_view* const views[4] = {x, residual, sum, out};
   p.map = merge_rows<4>(views, x->rank - 1);
+  p.end[0] = end_of(x, x_ptr);
+  p.end[1] = end_of(residual, residual_ptr);
   INJECT("hlo_rms_norm");
   return api_cuda_status(launch_norm(p, as_stream(stream)), "rms_norm launch");
 }
@@ -332,7 +341,7 @@ hlo_status hlo_rms_norm_backward(const hlo_view* dy, const void* dy_ptr, const h
                           {dx, dx_ptr, "rms_norm_backward dx"}};
   NormGradPlan p;
   std::memset(&p, 0, sizeof p);
-  TRY(check_dropout(dropout, &p.drop));
+  TRY(check_dropout(dropout, numel(*h), &p.drop));
   if ((dx != nullptr) != (dropout != nullptr))
     return api_fail(HLO_ERR_INVALID_ARG, "rms_norm_backward: dx goes with dropout (without it dx equals dh)");
   for (int k = 0; k < 5; ++k) {
@@ -393,6 +402,7 @@ hlo_status hlo_rms_norm_backward(const hlo_view* dy, const void* dy_ptr, const h
   p.w_offset = (float)weight_offset;
   const hlo_view* const views[5] = {dy, h, dsum, dh, dx};
   p.map = merge_rows<5>(views, h->rank - 1);
+  for (int k = 0; k < 3; ++k) p.end[k] = end_of(all[k].v, all[k].p);
   return api_cuda_status(launch_norm_grad(p, as_stream(stream)), "rms_norm_backward launch");
 }
 
@@ -411,7 +421,7 @@ hlo_status hlo_dropout(const hlo_view* x, const void* x_ptr, const hlo_view* res
   DropoutPlan p;
   std::memset(&p, 0, sizeof p);
   if (!dropout) return api_fail(HLO_ERR_INVALID_ARG, "dropout: parameters are NULL");
-  TRY(check_dropout(dropout, &p.drop));
+  TRY(check_dropout(dropout, numel(*x), &p.drop));
   const Operand ins[2] = {{x, x_ptr, "dropout x"}, {residual, residual_ptr, "dropout residual"}};
   const Operand o = {out, out_ptr, "dropout out"};
   TRY(check_overlap(o, ins, 2, nullptr, 0));
@@ -423,6 +433,8 @@ hlo_status hlo_dropout(const hlo_view* x, const void* x_ptr, const hlo_view* res
   p.dt = x->dtype;
   const hlo_view* const views[3] = {x, residual, out};
   p.map = merge_rows<3>(views, x->rank - 1);
+  p.end[0] = end_of(x, x_ptr);
+  p.end[1] = end_of(residual, residual_ptr);
   p.n = x->dims[x->rank - 1];
   p.rows = numel(*x) / p.n;
   // rows that follow one another in every view are one long row
@@ -613,6 +625,7 @@ hlo_status hlo_logits_process(const hlo_view* logits, const void* logits_ptr, co
   }
   if (b == 0 || (v == 0 && !token)) return api_ok();
   p.x = logits_ptr;
+  p.x_end = end_of(logits, logits_ptr);
   p.out = out ? out_ptr : nullptr;
   p.token = token;
   p.batch = b;

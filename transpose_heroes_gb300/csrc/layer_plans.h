@@ -32,13 +32,18 @@ __host__ __device__ inline void row_offsets(const Rows<NV>& m, int64_t k, int64_
 }
 
 // The generator's key and counter words (philox.cuh) and the keep rule: keep iff word >= threshold, or
-// nothing at all (`all`: round(p 2^32) = 2^32).
+// nothing at all (`all`: round(p 2^32) = 2^32). DROP_HOST: seed and offset are known on the host and every
+// element's index is below 2^34, so a counter's high words are the same for all elements; what the first three
+// rounds make of them, and the rounds' keys, are then constants. DROP_DEVICE: anything else.
+enum DropMode : int { DROP_NONE = 0, DROP_HOST = 1, DROP_DEVICE = 2 };
 struct DropPlan {
-  int on, all;
+  int mode, all;
   uint32_t threshold;
-  float scale;  // f32(1 / (1 - p))
-  uint64_t seed, offset;
-  const uint64_t* state;
+  float scale;              // f32(1 / (1 - p))
+  const uint64_t* state;    // DROP_DEVICE: seed and offset on the device, or NULL
+  uint64_t seed, offset;    // DROP_DEVICE: the offset is added to the device's, if there is one
+  uint32_t key[20];         // DROP_HOST: round r uses key[2 r], key[2 r + 1]
+  uint32_t x1, y2, x2, y3;  // DROP_HOST: constants of the first rounds (philox_constants)
 };
 
 enum NormQuant : int { NQ_NONE = 0, NQ_ROW = 1, NQ_STATIC = 2 };
@@ -58,6 +63,7 @@ struct NormPlan {
   QuantParams q;      // NQ_STATIC
   DropPlan drop;
   Rows<4> map;        // x, residual, sum, out
+  const char* end[2]; // of x and residual
 };
 cudaError_t launch_norm(const NormPlan& p, cudaStream_t s);
 
@@ -76,6 +82,7 @@ struct NormGradPlan {
   float w_offset;
   DropPlan drop;
   Rows<5> map;        // dy, h, dsum, dh, dx
+  const char* end[3]; // of dy, h and dsum
 };
 // Row groups whose shares of dweight are summed apart (each one row of n f32 in the workspace).
 int64_t norm_grad_partials(int64_t rows, int64_t n);
@@ -89,6 +96,7 @@ struct DropoutPlan {
   int dt;
   DropPlan drop;
   Rows<3> map;        // x, residual, out
+  const char* end[2]; // of x and residual
 };
 cudaError_t launch_dropout(const DropoutPlan& p, cudaStream_t s);
 
@@ -113,6 +121,7 @@ cudaError_t launch_rotary(const RotaryPlan& p, cudaStream_t s);
 
 struct LogitsPlan {
   const void* x;
+  const char* x_end;
   void* out;
   int32_t* token;
   int64_t batch, vocab;

@@ -52,6 +52,29 @@ __device__ __forceinline__ void load_weights(const void* w, int dt, float offset
       const float4 f = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(w) + c0) + q);
       v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
     }
+  } else if (dt == DT && (uintptr_t)w % 16 == 0) {
+    // two aligned vectors, then the words and the half word that c0 asks for
+    constexpr int EW = W / 4;  // elements a word
+    const int j = (c0 + W) / W - 1, s = c0 - j * W, last = (n - 1) / W;  // j: rounded down, -1 at least
+    const uint4* const at = reinterpret_cast<const uint4*>(w);
+    const bool tail = n % W != 0;  // the last vector would end behind the weights
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    if (j >= 0 && j <= last) a = j == last && tail ? load_cut<DT>(w, 0, (int64_t)j * W, n, nullptr) : __ldg(at + j);
+    if (s && j + 1 <= last) b = j + 1 == last && tail ? load_cut<DT>(w, 0, (int64_t)(j + 1) * W, n, nullptr) : __ldg(at + j + 1);
+    uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if ((s / EW) & 2) {
+#pragma unroll
+      for (int i = 0; i < 6; ++i) u[i] = u[i + 2];
+    }
+    if ((s / EW) & 1) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) u[i] = u[i + 1];
+    }
+    if (EW == 2 && (s & 1)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = __funnelshift_r(u[i], u[i + 1], 16);
+    }
+    unpack<DT>(make_uint4(u[0], u[1], u[2], u[3]), v);
   } else {
 #pragma unroll
     for (int e = 0; e < W; ++e) v[e] = c0 + e >= 0 && c0 + e < n ? load_as_f32(w, dt, c0 + e) : 1.0f;
@@ -66,18 +89,34 @@ __device__ __forceinline__ void load_weights(const void* w, int dt, float offset
 struct RowShape {
   int k, tx, ty;
 };
-inline RowShape row_shape(int64_t rows, int64_t vectors, int max_k) {
+// For many rows, another doubling of the vectors wants `lanes` more vectors a row.
+inline RowShape row_shape(int64_t rows, int64_t vectors, int max_k, int lanes) {
   const int sms = device_sm_count();
   int k = 1;
-  // few rows: as many threads a row as there are vectors, for latency; many: more bytes in flight a thread
-  const int64_t most = rows <= 2 * sms ? 1024 : 128;
-  while (k < max_k && vectors > most * k) k *= 2;
+  if (rows > 2 * sms)
+    while (k < 4 && vectors >= 2 * (int64_t)lanes * k) k *= 2;
+  // few rows: as many threads a row as it has vectors, for latency
   while (k < max_k && vectors > (k == 1 ? 1024 : 512 * (int64_t)k)) k *= 2;
   RowShape s;
   s.k = k;
   s.tx = (int)((vectors + k - 1) / k + 31) / 32 * 32;
-  s.ty = s.tx >= 256 || rows <= sms ? 1 : (int)std::min<int64_t>(256 / s.tx, 15);
+  s.ty = s.tx >= 256 || rows <= sms ? 1 : 256 / s.tx;
   return s;
 }
+
+__device__ __forceinline__ void store_out(const NormPlan& p, int64_t i, float y, float inv) {
+  if (p.quant == NQ_ROW) {
+    if (p.out_dt == S8) reinterpret_cast<int8_t*>(p.out)[i] = s8_code(y, inv);
+    else reinterpret_cast<uint8_t*>(p.out)[i] = f8_bits(__fmul_rn(y, inv));
+  } else if (p.quant == NQ_STATIC) {
+    reinterpret_cast<int8_t*>(p.out)[i] = (int8_t)quant_code(y, p.q.scale, p.q.inv_scale, p.q.zp, p.q.smin, p.q.smax);
+  } else {
+    store_from_f32(p.out, p.out_dt, i, y);
+  }
+}
+
+cudaError_t run_norm_f32(const NormPlan& p, const RowShape& r, bool cut, int whole, cudaStream_t s);
+cudaError_t run_norm_bf16(const NormPlan& p, const RowShape& r, bool cut, int whole, cudaStream_t s);
+cudaError_t run_norm_f16(const NormPlan& p, const RowShape& r, bool cut, int whole, cudaStream_t s);
 
 }  // namespace hlo

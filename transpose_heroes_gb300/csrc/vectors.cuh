@@ -33,6 +33,15 @@ __device__ __forceinline__ void unpack(const uint4& w, float (&v)[kVec<DT>]) {
   }
 }
 
+// The same as pairs, for packed f32x2 arithmetic.
+template <int DT>
+__device__ __forceinline__ void unpack2(const uint4& w, float2 (&v)[kVec<DT> / 2]) {
+  float f[kVec<DT>];
+  unpack<DT>(w, f);
+#pragma unroll
+  for (int i = 0; i < kVec<DT> / 2; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
+
 template <int DT>
 __device__ __forceinline__ uint4 pack(const float (&v)[kVec<DT>]) {
   uint32_t u[4];
@@ -56,50 +65,74 @@ __device__ __forceinline__ uint4 pack(const float (&v)[kVec<DT>]) {
 }
 
 // The elements c0 .. c0 + W - 1 of a row of n that starts at element `off` of p; those outside 0 .. n-1
-// read as 0. off + c0 is a multiple of W (counted from address 0), so a whole vector is one access.
+// read as 0. off + c0 is a multiple of W (counted from address 0), so a whole vector is one access; so is a
+// cut one where all of it lies inside the operand, [p, end): its neighbours' elements are dropped.
 template <int DT>
-__device__ __forceinline__ uint4 load_cut(const void* p, int64_t off, int64_t c0, int64_t n) {
+__device__ __forceinline__ uint4 load_cut(const void* p, int64_t off, int64_t c0, int64_t n, const char* end) {
   constexpr int W = kVec<DT>, EB = 16 / W;
   const char* a = reinterpret_cast<const char*>(p) + (off + c0) * EB;
   if (c0 >= 0 && c0 + W <= n) return load16(a);
+  const int lo = c0 < 0 ? (int)-c0 : 0, hi = n - c0 < W ? (int)(n - c0) : W;
   uint32_t u[4] = {0, 0, 0, 0};
+  if (a >= reinterpret_cast<const char*>(p) && a + 16 <= end) {
+    const uint4 w = load16(a);
+    const uint32_t all[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int e = 0; e < W; ++e) {
-    if (c0 + e < 0 || c0 + e >= n) continue;
-    if (EB == 4) u[e & 3] = reinterpret_cast<const uint32_t*>(a)[e];
-    else u[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(a)[e] << (16 * (e & 1));
+    for (int e = 0; e < W; ++e)
+      if (e >= lo && e < hi) u[EB == 4 ? e & 3 : e >> 1] |= EB == 4 ? all[e & 3] : all[e >> 1] & (0xFFFFu << (16 * (e & 1)));
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      if (e < lo || e >= hi) continue;
+      if (EB == 4) u[e & 3] = reinterpret_cast<const uint32_t*>(a)[e];
+      else u[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(a)[e] << (16 * (e & 1));
+    }
   }
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+// Stores the elements that lie in the row: of a vector cut off at one end, in up to three accesses.
 template <int DT>
 __device__ __forceinline__ void store_cut(void* p, int64_t off, int64_t c0, int64_t n, const float (&v)[kVec<DT>]) {
   constexpr int W = kVec<DT>, EB = 16 / W;
   char* a = reinterpret_cast<char*>(p) + (off + c0) * EB;
+  const uint4 w = pack<DT>(v);
   if (c0 >= 0 && c0 + W <= n) {
-    *reinterpret_cast<uint4*>(a) = pack<DT>(v);
+    *reinterpret_cast<uint4*>(a) = w;
     return;
   }
+  const int lo = c0 < 0 ? (int)-c0 : 0, hi = n - c0 < W ? (int)(n - c0) : W;
+  if (lo == 0) {  // the first hi elements
+    const int words = hi * EB / 4;
+    if (words & 2) *reinterpret_cast<uint2*>(a) = make_uint2(w.x, w.y);
+    if (words & 1) *reinterpret_cast<uint32_t*>(a + 4 * (words & 2)) = (words & 2) ? w.z : w.x;
+    if (EB == 2 && (hi & 1)) *reinterpret_cast<uint16_t*>(a + 4 * words) = (uint16_t)((words & 2) ? ((words & 1) ? w.w : w.z) : ((words & 1) ? w.y : w.x));
+  } else if (hi == W) {  // the last W - lo
+    const int words = (W - lo) * EB / 4;
+    if (words & 2) *reinterpret_cast<uint2*>(a + 8) = make_uint2(w.z, w.w);
+    if (words & 1) *reinterpret_cast<uint32_t*>(a + 12 - 4 * (words & 2)) = (words & 2) ? w.y : w.w;
+    if (EB == 2 && (lo & 1)) *reinterpret_cast<uint16_t*>(a + 2 * lo) = (uint16_t)(((lo & 4) ? ((lo & 2) ? w.w : w.z) : ((lo & 2) ? w.y : w.x)) >> 16);
+  } else {
 #pragma unroll
-  for (int e = 0; e < W; ++e)
-    if (c0 + e >= 0 && c0 + e < n) store_from_f32(a, DT, e, v[e]);
+    for (int e = 0; e < W; ++e)
+      if (e >= lo && e < hi) store_from_f32(a, DT, e, v[e]);
+  }
 }
 
-// drop(v) for the W elements from linear index i on. Their counters are i / 4, ...: W / 4 of them when i is a
-// multiple of 4, one more otherwise, and the words wanted then start i mod 4 words in. i may be below 0 where
-// a vector starts before the first row (those elements are not stored).
-template <int W>
-__device__ __forceinline__ void drop_vec(const DropPlan& d, const Philox& g, int64_t i, float (&v)[W]) {
-  uint32_t w[W + 4];
-  const int m = (int)(i & 3);
+// The generator's words for the W elements from linear index i on. Their counters are i / 4, ...: W / 4 of them
+// when i is a multiple of 4 (WHOLE: it always is), one more otherwise, and the words wanted then start i mod 4
+// words in. i may be below 0 where a vector starts before the first row (those elements are not stored).
+template <int MODE, bool WHOLE, int W>
+__device__ __forceinline__ void drop_words(const DropPlan& d, const Philox<MODE>& g, int64_t i, uint32_t (&w)[W + 4]) {
   const int64_t quad = i >> 2;
 #pragma unroll
   for (int q = 0; q < W / 4; ++q) {
-    const uint4 r = philox4(g, (uint64_t)(quad + q));
+    const uint4 r = g.words(d, (uint64_t)(quad + q));
     w[4 * q] = r.x, w[4 * q + 1] = r.y, w[4 * q + 2] = r.z, w[4 * q + 3] = r.w;
   }
+  const int m = WHOLE ? 0 : (int)(i & 3);
   if (m) {
-    const uint4 r = philox4(g, (uint64_t)(quad + W / 4));
+    const uint4 r = g.words(d, (uint64_t)(quad + W / 4));
     w[W] = r.x, w[W + 1] = r.y, w[W + 2] = r.z, w[W + 3] = r.w;
     if (m & 1) {
 #pragma unroll
@@ -110,8 +143,29 @@ __device__ __forceinline__ void drop_vec(const DropPlan& d, const Philox& g, int
       for (int e = 0; e < W; ++e) w[e] = w[e + 2];
     }
   }
+}
+
+// v = drop(v).
+template <int MODE, bool WHOLE, int W>
+__device__ __forceinline__ void drop_vec(const DropPlan& d, const Philox<MODE>& g, int64_t i, float (&v)[W]) {
+  uint32_t w[W + 4];
+  drop_words<MODE, WHOLE, W>(d, g, i, w);
 #pragma unroll
-  for (int e = 0; e < W; ++e) v[e] = kept(d, w[e]) ? __fmul_rn(v[e], d.scale) : 0.0f;
+  for (int e = 0; e < W; ++e) v[e] = dropped(d, w[e], v[e]);
+}
+
+// v = r + drop(v): the addition happens or not (a residual of -0 stays -0 where v is dropped), which costs less than
+// a select and an addition.
+template <int MODE, bool WHOLE, int W>
+__device__ __forceinline__ void drop_add_vec(const DropPlan& d, const Philox<MODE>& g, int64_t i, float (&v)[W], const float (&r)[W]) {
+  uint32_t w[W + 4];
+  drop_words<MODE, WHOLE, W>(d, g, i, w);
+#pragma unroll
+  for (int e = 0; e < W; ++e) {
+    const float t = __fmul_rn(v[e], d.scale);
+    v[e] = r[e];
+    if (kept(d, w[e])) v[e] = __fadd_rn(r[e], t);
+  }
 }
 
 // Whether every view's rows can be read in vectors of W elements that fall on the same columns: addresses
