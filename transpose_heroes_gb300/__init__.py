@@ -430,11 +430,12 @@ def quant_fusion(inp, dims, in_q, out_m2m, out, out_dtype="s8", out_q=None, in_m
 # ---- the fusions between a decoder's matrix products ---------------------------------------------------------
 # Their operands are views: torch tensors (dims, strides and element type are the tensor's own) or
 # DeviceViews of raw device pointers. Vectors (a weight, scales, lengths, ...) are contiguous tensors, or
-# raw pointers.
+# raw addresses. A serving step makes hundreds of these calls, so their arguments are marshalled by a
+# CPython extension (csrc/call.cc) in place of ctypes.
 class DeviceView:
     """A view of device memory at `ptr` (an address or a tensor that carries the bits)."""
 
-    __slots__ = ("ptr", "ref", "dims", "keep")
+    __slots__ = ("ptr", "addr", "view", "keep")
 
     def __init__(self, ptr, dims, dtype: str, strides=None):
         dims = [int(d) for d in dims]
@@ -443,82 +444,47 @@ class DeviceView:
             for i in range(len(dims) - 1, -1, -1):
                 strides[i] = s
                 s *= dims[i]
-        self.ptr, self.dims, self.keep = _ptr(ptr), tuple(dims), ptr
-        self.ref = ctypes.byref(_make_view(dims, strides, VIEW_DTYPES[dtype]))
+        if len(dims) > MAX_RANK or len(strides) != len(dims):
+            raise HloError(STATUS_INVALID_ARG, f"a view holds 1..{MAX_RANK} dimensions with a stride each")
+        self.view = View(len(dims), VIEW_DTYPES[dtype])
+        for i, (d, s) in enumerate(zip(dims, strides)):
+            self.view.dims[i], self.view.strides[i] = d, int(s)
+        self.ptr, self.addr, self.keep = _ptr(ptr), ctypes.addressof(self.view), ptr
 
 
-def _make_view(dims, strides, dtype: int) -> View:
-    v = View()
-    v.rank, v.dtype = len(dims), dtype
-    if len(dims) > MAX_RANK or len(strides) != len(dims):
-        raise HloError(STATUS_INVALID_ARG, f"a view holds 1..{MAX_RANK} dimensions with a stride each")
-    for i, (d, s) in enumerate(zip(dims, strides)):
-        v.dims[i], v.strides[i] = int(d), int(s)
-    return v
+CALL_PATH = os.path.join(_PKG, "_lib", "_hlocall.so")
+_call = None
 
 
-_views = {}  # (shape, strides, element type) -> the marshalled descriptor; descriptors hold no address
-_torch_dtypes = {}
+def _load_call():
+    """Loads the extension (built with the library). Raises if missing."""
+    global _call
+    lib()
+    if not os.path.exists(CALL_PATH):
+        raise RuntimeError(f"_hlocall.so is not built ({CALL_PATH}); run transpose_heroes_gb300.build.build()")
+    import importlib.util
+
+    import torch
+
+    spec = importlib.util.spec_from_file_location("_hlocall", CALL_PATH)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: _stream(None))
+    m.setup(DeviceView, get_device, get_stream, torch.float32, torch.bfloat16, torch.int8, torch.float16, torch.int32,
+            torch.float8_e4m3fn)
+    _call = m
+    return m
 
 
-def _view(t):
-    """(descriptor reference, address) of a tensor or DeviceView; (None, 0) for None."""
-    if t is None:
-        return None, 0
-    if type(t) is DeviceView:
-        return t.ref, t.ptr
-    key = (t.shape, t.stride(), t.dtype)
-    ref = _views.get(key)
-    if ref is None:
-        if not _torch_dtypes:
-            import torch
-
-            _torch_dtypes.update({torch.float32: 0, torch.bfloat16: 1, torch.int8: 2, torch.float16: 3, torch.int32: 4,
-                                  torch.float8_e4m3fn: 5})
-        if t.dtype not in _torch_dtypes:
-            raise HloError(STATUS_INVALID_ARG, f"no element type for {t.dtype}")
-        if len(_views) >= 4096:
-            _views.clear()
-        ref = _views[key] = ctypes.byref(_make_view(t.shape, t.stride(), _torch_dtypes[t.dtype]))
-    return ref, t.data_ptr()
-
-
-def _vector(t, count: int, dtype: str, what: str) -> int:
-    """Address of a contiguous device vector of `count` elements (raw addresses are taken as they are)."""
-    if t is None or isinstance(t, int):
-        return t or 0
-    _view(t)  # the element type is known
-    if _torch_dtypes[t.dtype] != VIEW_DTYPES[dtype] or t.numel() != count or not t.is_contiguous():
-        raise HloError(STATUS_INVALID_ARG, f"{what}: a contiguous {dtype} vector of {count} elements is wanted")
-    return t.data_ptr()
-
-
-def _dims(t):
-    return t.dims if type(t) is DeviceView else t.shape
-
-
-def _weight(weight, weight_dtype, n):
-    if weight is None or isinstance(weight, int):
-        return weight or 0, VIEW_DTYPES[weight_dtype]
-    _view(weight)
-    if weight.numel() != n or not weight.is_contiguous():
-        raise HloError(STATUS_INVALID_ARG, f"rms_norm weight: a contiguous vector of {n} elements is wanted")
-    return weight.data_ptr(), _torch_dtypes[weight.dtype]
-
-
-_raw_stream = None
-
-
-def _call_stream(stream) -> int:
-    if stream is not None:
-        return _stream(stream)
-    global _raw_stream
-    if _raw_stream is None:
-        import torch
-
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _raw_stream = (lambda: raw(torch.cuda.current_device())) if raw else (lambda: _stream(None))
-    return _raw_stream()
+def _made(name, *args):
+    """Makes the extension's call `name` and raises its refusals as HloError."""
+    try:
+        status = getattr(_call or _load_call(), name)(*args)
+    except ValueError as e:
+        raise HloError(STATUS_INVALID_ARG, str(e)) from None
+    if status:
+        _check(status)
 
 
 def rms_norm(x, out, weight=None, residual=None, sum_out=None, rstd=None, eps=1e-6, weight_offset=0.0, dropout=None,
@@ -526,22 +492,9 @@ def rms_norm(x, out, weight=None, residual=None, sum_out=None, rstd=None, eps=1e
     """hlo_rms_norm: h = residual + drop(x) (to sum_out), out = h / rms(h) * (weight + weight_offset), out in
     x's type, f32, or 8 bits with `scales` (per row) or `out_q` (static). weight_dtype names the type of a
     weight given as a raw address."""
-    dims = _dims(x)
-    n = int(dims[-1]) if len(dims) else 0
-    rows = 1
-    for d in dims[:-1]:
-        rows *= int(d)
-    xv, xp = _view(x)
-    rv, rp = _view(residual)
-    sv, sp = _view(sum_out)
-    ov, op = _view(out)
-    wp, wd = _weight(weight, weight_dtype, n)
     q = _QuantKeep(out_q) if out_q is not None else None
-    st = lib().hlo_rms_norm(xv, xp, rv, rp, dropout, wp, wd, weight_offset, eps, sv, sp, ov, op,
-                            _vector(scales, rows, "f32", "scales"), None if q is None else q.ref(),
-                            _vector(rstd, rows, "f32", "rstd"), _call_stream(stream))
-    if st:
-        _check(st)
+    _made("rms_norm", x, out, weight, VIEW_DTYPES[weight_dtype], residual, sum_out, rstd, eps, weight_offset, dropout,
+          scales, None if q is None else q.q, None if stream is None else _stream(stream))
     return out
 
 
@@ -555,36 +508,17 @@ def rms_norm_backward(dy, h, rstd, dh, weight=None, dsum=None, dx=None, dropout=
     """hlo_rms_norm_backward: dh (the gradient of h), dx = drop(dh) with dropout, and dweight, from dy, the
     forward pass's sum h and rstd, and dsum (what reaches h by other ways). The workspace is a contiguous
     tensor, or a raw address with workspace_bytes."""
-    dims = _dims(h)
-    n = int(dims[-1]) if len(dims) else 0
-    rows = 1
-    for d in dims[:-1]:
-        rows *= int(d)
-    yv, yp = _view(dy)
-    hv, hp = _view(h)
-    sv, sp = _view(dsum)
-    dhv, dhp = _view(dh)
-    dxv, dxp = _view(dx)
-    wp, wd = _weight(weight, weight_dtype, n)
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib().hlo_rms_norm_backward(yv, yp, hv, hp, _vector(rstd, rows, "f32", "rstd"), wp, wd, weight_offset, sv, sp,
-                                     dropout, dhv, dhp, dxv, dxp, _vector(dweight, n, "f32", "dweight"), _ptr(workspace),
-                                     workspace_bytes, _call_stream(stream))
-    if st:
-        _check(st)
+    _made("rms_norm_backward", dy, h, rstd, dh, weight, VIEW_DTYPES[weight_dtype], dsum, dx, dropout, dweight,
+          _ptr(workspace), workspace_bytes, weight_offset, None if stream is None else _stream(stream))
     return dh
 
 
 def dropout(x, out, params, residual=None, stream=None):
     """hlo_dropout: out = residual + drop(x) for params = Dropout(p, seed, offset). The backward pass is the
     same call on the gradient."""
-    xv, xp = _view(x)
-    rv, rp = _view(residual)
-    ov, op = _view(out)
-    st = lib().hlo_dropout(xv, xp, rv, rp, params, ov, op, _call_stream(stream))
-    if st:
-        _check(st)
+    _made("dropout", x, out, params, residual, None if stream is None else _stream(stream))
     return out
 
 
@@ -605,19 +539,8 @@ def rotary(x, out, positions, turns, k=None, k_out=None, interleaved=False, scal
     """hlo_rotary: rotates the first 2 n_pairs elements of every head of x (and of k) by position * turns; the
     rest is copied. turns: rotary_turns() on the device (int64), or a raw address with n_pairs. inverse
     turns back: the backward pass."""
-    xv, xp = _view(x)
-    ov, op = _view(out)
-    kv, kp = _view(k)
-    kov, kop = _view(k_out)
-    pv, pp = _view(positions)
-    if n_pairs is None:
-        if turns.element_size() != 8 or not turns.is_contiguous():
-            raise HloError(STATUS_INVALID_ARG, "rotary turns: a contiguous vector of 64-bit words is wanted")
-        n_pairs = turns.numel()
-    st = lib().hlo_rotary(xv, xp, ov, op, kv, kp, kov, kop, pv, pp, _ptr(turns), n_pairs, interleaved, inverse, scale,
-                          _call_stream(stream))
-    if st:
-        _check(st)
+    _made("rotary", x, out, positions, turns, n_pairs, k, k_out, interleaved, scale, inverse,
+          None if stream is None else _stream(stream))
     return out
 
 
@@ -626,22 +549,6 @@ def logits_process(logits, out=None, bias=None, history=None, lengths=None, prom
     """hlo_logits_process: bias, repetition / frequency / presence penalties for the tokens of each row's
     history, the grammar's bit mask, and the greedy token (lowest index on ties, -1 when nothing is left).
     A bias or mask of one dimension serves every row."""
-    batch = int(_dims(logits)[0])
-    lv, lp = _view(logits)
-    if bias is not None and len(_dims(bias)) == 1:
-        bias = bias.expand(batch, -1)
-    if mask is not None and len(_dims(mask)) == 1:
-        mask = mask.expand(batch, -1)
-    bv, bp = _view(bias)
-    hv, hp = _view(history)
-    mv, mp = _view(mask)
-    ov, op = _view(out)
-    st = lib().hlo_logits_process(lv, lp, bv, bp, hv, hp, _vector(lengths, batch, "s32", "lengths"),
-                                  _vector(prompt_lengths, batch, "s32", "prompt_lengths"),
-                                  _vector(repetition, batch, "f32", "repetition"),
-                                  _vector(frequency, batch, "f32", "frequency"),
-                                  _vector(presence, batch, "f32", "presence"), mv, mp, ov, op,
-                                  _vector(token, batch, "s32", "token"), _call_stream(stream))
-    if st:
-        _check(st)
+    _made("logits_process", logits, out, bias, history, lengths, prompt_lengths, repetition, frequency, presence, mask,
+          token, None if stream is None else _stream(stream))
     return out if out is not None else token

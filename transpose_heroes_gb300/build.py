@@ -1,7 +1,8 @@
 """Build libhlofusion.so in-tree for sm_103a (nvcc only; no torch extension machinery).
 
 Every translation unit under csrc/ is compiled in parallel to an object file, then linked into
-transpose_heroes_gb300/_lib/libhlofusion.so with the CUDA runtime linked statically.
+transpose_heroes_gb300/_lib/libhlofusion.so with the CUDA runtime linked statically. csrc/call.cc becomes
+_lib/_hlocall.so, a CPython extension on top of it.
 """
 
 from __future__ import annotations
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libhlofusion.so")
+CALL = os.path.join(LIBDIR, "_hlocall.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -75,7 +78,22 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    build_call(force)
     return LIB
+
+
+def build_call(force: bool = False) -> str:
+    """The CPython extension that marshals the calls of small layers (csrc/call.cc), linked to the library."""
+    src = os.path.join(CSRC, "call.cc")
+    if force or _stale(CALL, [src, os.path.join(INCLUDE, "hlo_fusion.h")]):
+        tmp = CALL + f".tmp{os.getpid()}"
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-I", INCLUDE, "-I",
+               sysconfig.get_paths()["include"], src, "-o", tmp, "-L", LIBDIR, "-l:libhlofusion.so", "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, CALL)
+    return CALL
 
 
 if __name__ == "__main__":

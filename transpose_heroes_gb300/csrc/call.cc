@@ -1,0 +1,289 @@
+// _hlocall: the marshalling of the layer entry points (hlo_rms_norm, hlo_rms_norm_backward, hlo_dropout, hlo_rotary,
+// hlo_logits_process) as a CPython extension. A serving step makes hundreds of these calls on a few
+// kilobytes each, where building the descriptors through ctypes costs more than the kernel (measured on the
+// GPU's host: 11 us a call, of which the launch is 3); here the tensors' attributes are read directly.
+// Every function takes its operands by position and returns the hlo_status; nothing is kept between calls.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <cstring>
+
+#include "hlo_fusion.h"
+
+namespace {
+
+PyObject *s_data_ptr, *s_shape, *s_stride, *s_dtype, *s_ptr, *s_addr;
+PyObject* g_dtypes[6];    // torch's element types by hlo_dtype, once registered
+PyObject* g_view_type;    // DeviceView
+PyObject *g_get_device, *g_get_stream;
+
+// One argument: a tensor, a DeviceView or None.
+struct Operand {
+  hlo_view v;
+  void* p = nullptr;
+  bool given = false;
+  const hlo_view* view() const { return given ? &v : nullptr; }
+};
+
+bool address(PyObject* o, void** p) {
+  *p = PyLong_AsVoidPtr(o);
+  return *p || !PyErr_Occurred();
+}
+
+bool fill(PyObject* seq, int64_t* to, Py_ssize_t* n) {  // torch.Size and stride() are tuples
+  if (!PyTuple_Check(seq)) {
+    PyErr_SetString(PyExc_TypeError, "a tensor or a DeviceView is wanted");
+    return false;
+  }
+  *n = PyTuple_GET_SIZE(seq);
+  for (Py_ssize_t i = 0; i < *n && i < HLO_MAX_RANK; ++i) {
+    to[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(seq, i));
+    if (to[i] == -1 && PyErr_Occurred()) return false;
+  }
+  return true;
+}
+
+bool read(PyObject* t, Operand* o) {
+  if (t == Py_None) return true;
+  o->given = true;
+  if ((PyObject*)Py_TYPE(t) == g_view_type) {
+    PyObject *a = PyObject_GetAttr(t, s_addr), *p = a ? PyObject_GetAttr(t, s_ptr) : nullptr;
+    void* view = nullptr;
+    const bool ok = a && p && address(a, &view) && address(p, &o->p);
+    if (ok) std::memcpy(&o->v, view, sizeof o->v);
+    Py_XDECREF(a);
+    Py_XDECREF(p);
+    return ok;
+  }
+  PyObject *p = PyObject_CallMethodNoArgs(t, s_data_ptr), *shape = nullptr, *stride = nullptr, *dtype = nullptr;
+  bool ok = p && address(p, &o->p) && (shape = PyObject_GetAttr(t, s_shape)) && (stride = PyObject_CallMethodNoArgs(t, s_stride)) &&
+            (dtype = PyObject_GetAttr(t, s_dtype));
+  Py_ssize_t rank = 0, strides = 0;
+  ok = ok && fill(shape, o->v.dims, &rank) && fill(stride, o->v.strides, &strides);
+  if (ok) {
+    o->v.rank = (int32_t)rank;  // a rank that is too high is the library's to refuse
+    o->v.dtype = -1;
+    for (int k = 0; k < 6; ++k)
+      if (g_dtypes[k] == dtype) o->v.dtype = k;
+  }
+  Py_XDECREF(p);
+  Py_XDECREF(shape);
+  Py_XDECREF(stride);
+  Py_XDECREF(dtype);
+  return ok;
+}
+
+// A contiguous vector of `count` elements (count < 0: any number, stored), an address, or None. *dtype: the wanted type,
+// or -1 and then set.
+bool read_vector(PyObject* t, int64_t* count, int32_t* dtype, const char* what, void** p) {
+  *p = nullptr;
+  if (t == Py_None) return true;
+  if (PyLong_Check(t)) return address(t, p);
+  Operand o;
+  if (!read(t, &o)) return false;
+  int64_t n = 1;
+  bool dense = o.v.rank <= HLO_MAX_RANK;
+  for (int d = o.v.rank - 1; dense && d >= 0; --d) {
+    dense = o.v.dims[d] == 1 || o.v.strides[d] == n;
+    n *= o.v.dims[d];
+  }
+  if ((!dense && n != 0) || (*count >= 0 && n != *count) || (*dtype >= 0 && o.v.dtype != *dtype)) {
+    PyErr_Format(PyExc_ValueError, "%s: a contiguous vector of %lld elements of the right type is wanted", what, (long long)*count);
+    return false;
+  }
+  *count = n;
+  *dtype = o.v.dtype;
+  *p = o.p;
+  return true;
+}
+
+bool read_vector(PyObject* t, int64_t count, int32_t dtype, const char* what, void** p) {
+  return read_vector(t, &count, &dtype, what, p);
+}
+
+// The ctypes structure behind `o` (or NULL for None); its memory outlives the call, since the caller holds it.
+template <typename T>
+bool read_struct(PyObject* o, T** out) {
+  *out = nullptr;
+  if (o == Py_None) return true;
+  Py_buffer b;
+  if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE) != 0) return false;
+  const bool ok = b.len == (Py_ssize_t)sizeof(T);
+  *out = static_cast<T*>(b.buf);
+  PyBuffer_Release(&b);
+  if (!ok) PyErr_SetString(PyExc_TypeError, "a parameter structure has the wrong size");
+  return ok;
+}
+
+// A stream's handle, or None for the current stream of the current device.
+bool read_stream(PyObject* o, void** stream) {
+  if (o != Py_None) return address(o, stream);
+  PyObject* dev = PyObject_CallNoArgs(g_get_device);
+  PyObject* s = dev ? PyObject_CallOneArg(g_get_stream, dev) : nullptr;
+  const bool ok = s && address(s, stream);
+  Py_XDECREF(dev);
+  Py_XDECREF(s);
+  return ok;
+}
+
+bool count_is(Py_ssize_t n, Py_ssize_t want) {
+  if (n == want) return true;
+  PyErr_Format(PyExc_TypeError, "%zd arguments, %zd are wanted", n, want);
+  return false;
+}
+
+int64_t rows_of(const hlo_view& v) {
+  int64_t r = 1;
+  for (int d = 0; d + 1 < v.rank && d < HLO_MAX_RANK; ++d) r *= v.dims[d];
+  return r;
+}
+int64_t last_of(const hlo_view& v) { return v.rank > 0 && v.rank <= HLO_MAX_RANK ? v.dims[v.rank - 1] : 0; }
+
+PyObject* status(hlo_status s) { return PyLong_FromLong((long)s); }
+
+#define CALL(expr)                             \
+  hlo_status st;                               \
+  Py_BEGIN_ALLOW_THREADS;                      \
+  st = (expr);                                 \
+  Py_END_ALLOW_THREADS;                        \
+  return status(st)
+
+// x, out, weight, weight_dtype, residual, sum, rstd, eps, weight_offset, dropout, scales, out_q, stream
+PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 13)) return nullptr;
+  Operand x, out, res, sum;
+  if (!read(a[0], &x) || !read(a[1], &out) || !read(a[4], &res) || !read(a[5], &sum)) return nullptr;
+  const int64_t rows = x.given ? rows_of(x.v) : 0;
+  int64_t cols = x.given ? last_of(x.v) : 0;
+  int32_t wdt = -1;
+  void *w, *rstd, *scales, *stream;
+  hlo_dropout_params* drop;
+  hlo_quant* q;
+  if (!read_vector(a[2], &cols, &wdt, "weight", &w) || !read_vector(a[6], rows, HLO_F32, "rstd", &rstd) ||
+      !read_vector(a[10], rows, HLO_F32, "scales", &scales) || !read_struct(a[9], &drop) || !read_struct(a[11], &q) ||
+      !read_stream(a[12], &stream))
+    return nullptr;
+  if (wdt < 0) wdt = (int32_t)PyLong_AsLong(a[3]);
+  const double eps = PyFloat_AsDouble(a[7]), off = PyFloat_AsDouble(a[8]);
+  if (PyErr_Occurred()) return nullptr;
+  CALL(hlo_rms_norm(x.view(), x.p, res.view(), res.p, drop, w, wdt, off, eps, sum.view(), sum.p, out.view(), out.p,
+                    static_cast<float*>(scales), q, static_cast<float*>(rstd), stream));
+}
+
+// dy, h, rstd, dh, weight, weight_dtype, dsum, dx, dropout, dweight, workspace, workspace_bytes, weight_offset, stream
+PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 14)) return nullptr;
+  Operand dy, h, dh, ds, dx;
+  if (!read(a[0], &dy) || !read(a[1], &h) || !read(a[3], &dh) || !read(a[6], &ds) || !read(a[7], &dx)) return nullptr;
+  const int64_t rows = h.given ? rows_of(h.v) : 0;
+  int64_t cols = h.given ? last_of(h.v) : 0;
+  const int64_t width = cols;
+  int32_t wdt = -1;
+  void *w, *rstd, *dw, *ws, *stream;
+  hlo_dropout_params* drop;
+  if (!read_vector(a[4], &cols, &wdt, "weight", &w) || !read_vector(a[2], rows, HLO_F32, "rstd", &rstd) ||
+      !read_vector(a[9], width, HLO_F32, "dweight", &dw) || !read_struct(a[8], &drop) || !address(a[10], &ws) ||
+      !read_stream(a[13], &stream))
+    return nullptr;
+  if (wdt < 0) wdt = (int32_t)PyLong_AsLong(a[5]);
+  const size_t bytes = PyLong_AsSize_t(a[11]);
+  const double off = PyFloat_AsDouble(a[12]);
+  if (PyErr_Occurred()) return nullptr;
+  CALL(hlo_rms_norm_backward(dy.view(), dy.p, h.view(), h.p, static_cast<float*>(rstd), w, wdt, off, ds.view(), ds.p, drop, dh.view(),
+                             dh.p, dx.view(), dx.p, static_cast<float*>(dw), ws, bytes, stream));
+}
+
+// x, out, dropout, residual, stream
+PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 5)) return nullptr;
+  Operand x, out, res;
+  hlo_dropout_params* drop;
+  void* stream;
+  if (!read(a[0], &x) || !read(a[1], &out) || !read(a[3], &res) || !read_struct(a[2], &drop) || !read_stream(a[4], &stream)) return nullptr;
+  CALL(hlo_dropout(x.view(), x.p, res.view(), res.p, drop, out.view(), out.p, stream));
+}
+
+// x, out, positions, turns, n_pairs (None: turns' count), k, k_out, interleaved, scale, inverse, stream
+PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 11)) return nullptr;
+  Operand x, out, pos, k, kout;
+  if (!read(a[0], &x) || !read(a[1], &out) || !read(a[2], &pos) || !read(a[5], &k) || !read(a[6], &kout)) return nullptr;
+  int64_t pairs = -1;
+  int32_t any = -1;
+  void *turns, *stream;
+  if (!read_vector(a[3], &pairs, &any, "turns", &turns) || !read_stream(a[10], &stream)) return nullptr;
+  if (any >= 0) {
+    PyErr_SetString(PyExc_ValueError, "rotary turns: a contiguous vector of 64-bit words is wanted");
+    return nullptr;
+  }
+  if (a[4] != Py_None) pairs = PyLong_AsLongLong(a[4]);
+  const double scale = PyFloat_AsDouble(a[8]);
+  const int inter = PyObject_IsTrue(a[7]), inverse = PyObject_IsTrue(a[9]);
+  if (PyErr_Occurred()) return nullptr;
+  if (pairs > INT32_MAX) pairs = INT32_MAX;
+  CALL(hlo_rotary(x.view(), x.p, out.view(), out.p, k.view(), k.p, kout.view(), kout.p, pos.view(), static_cast<int32_t*>(pos.p),
+                  static_cast<uint64_t*>(turns), (int32_t)pairs, inter, inverse, scale, stream));
+}
+
+// A row of n dimensions serves every row of the batch.
+void repeat_row(Operand* o, int64_t batch) {
+  if (!o->given || o->v.rank != 1) return;
+  o->v.rank = 2;
+  o->v.dims[1] = o->v.dims[0];
+  o->v.strides[1] = o->v.strides[0];
+  o->v.dims[0] = batch;
+  o->v.strides[0] = 0;
+}
+
+// logits, out, bias, history, lengths, prompt_lengths, repetition, frequency, presence, mask, token, stream
+PyObject* logits_process(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 12)) return nullptr;
+  Operand x, out, bias, hist, mask;
+  if (!read(a[0], &x) || !read(a[1], &out) || !read(a[2], &bias) || !read(a[3], &hist) || !read(a[9], &mask)) return nullptr;
+  const int64_t b = x.given && x.v.rank > 0 ? x.v.dims[0] : 0;
+  repeat_row(&bias, b);
+  repeat_row(&mask, b);
+  void *len, *prompt, *rep, *freq, *pres, *token, *stream;
+  if (!read_vector(a[4], b, HLO_S32, "lengths", &len) || !read_vector(a[5], b, HLO_S32, "prompt_lengths", &prompt) ||
+      !read_vector(a[6], b, HLO_F32, "repetition", &rep) || !read_vector(a[7], b, HLO_F32, "frequency", &freq) ||
+      !read_vector(a[8], b, HLO_F32, "presence", &pres) || !read_vector(a[10], b, HLO_S32, "token", &token) ||
+      !read_stream(a[11], &stream))
+    return nullptr;
+  CALL(hlo_logits_process(x.view(), x.p, bias.view(), static_cast<float*>(bias.p), hist.view(), static_cast<int32_t*>(hist.p),
+                          static_cast<int32_t*>(len), static_cast<int32_t*>(prompt), static_cast<float*>(rep),
+                          static_cast<float*>(freq), static_cast<float*>(pres), mask.view(), static_cast<int32_t*>(mask.p), out.view(),
+                          out.p, static_cast<int32_t*>(token), stream));
+}
+
+// view_type, get_device, get_stream, then torch's element types in the order of hlo_dtype
+PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 9)) return nullptr;
+  PyObject** const to[9] = {&g_view_type, &g_get_device, &g_get_stream, g_dtypes, g_dtypes + 1, g_dtypes + 2, g_dtypes + 3, g_dtypes + 4,
+                            g_dtypes + 5};
+  for (int k = 0; k < 9; ++k) {
+    Py_INCREF(a[k]);
+    Py_XSETREF(*to[k], a[k]);
+  }
+  Py_RETURN_NONE;
+}
+
+PyMethodDef methods[] = {{"setup", (PyCFunction)(void (*)(void))setup, METH_FASTCALL, nullptr},
+                         {"rms_norm", (PyCFunction)(void (*)(void))rms_norm, METH_FASTCALL, nullptr},
+                         {"rms_norm_backward", (PyCFunction)(void (*)(void))rms_norm_backward, METH_FASTCALL, nullptr},
+                         {"dropout", (PyCFunction)(void (*)(void))dropout, METH_FASTCALL, nullptr},
+                         {"rotary", (PyCFunction)(void (*)(void))rotary, METH_FASTCALL, nullptr},
+                         {"logits_process", (PyCFunction)(void (*)(void))logits_process, METH_FASTCALL, nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hlocall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__hlocall() {
+  s_data_ptr = PyUnicode_InternFromString("data_ptr");
+  s_shape = PyUnicode_InternFromString("shape");
+  s_stride = PyUnicode_InternFromString("stride");
+  s_dtype = PyUnicode_InternFromString("dtype");
+  s_ptr = PyUnicode_InternFromString("ptr");
+  s_addr = PyUnicode_InternFromString("addr");
+  return PyModule_Create(&module);
+}
