@@ -58,58 +58,72 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(const __grid
 // at c + c / W, so that threads W columns apart meet no bank twice. A thread adds to a column only behind
 // its group's barrier of that row, so two rows never add to one at once. The groups' sums go to the
 // workspace, and norm_grad_join_kernel adds them in order.
+//
+// CUT rows are taken apart as in norm_row_kernel; their weights lie in shared memory too, in the same places.
 template <int DT, int K, int DROP, bool CUT>
 __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(const __grid_constant__ NormGradPlan p, int weight_whole, int64_t groups) {
   constexpr int W = kVec<DT>, EB = 16 / W;
   __shared__ float red[2][64];
-  extern __shared__ float dw_shared[];
-  const int n = (int)p.n;
+  extern __shared__ float cut_shared[];
+  const int n = (int)p.n, places = n + n / W + 1;
   const int64_t group = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  if (group >= groups) return;  // the whole group: its barrier is its own
+  const bool idle = group >= groups;
   const Philox<DROP> g(p.drop);
   float acc[K][W];
-  float* const cols = CUT ? dw_shared + (int)threadIdx.y * (n + n / W + 1) : nullptr;
+  float* const ws = cut_shared;
+  float* const cols = cut_shared + (1 + (int)threadIdx.y) * places;
   if (CUT) {
+    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < n; c += blockDim.x * blockDim.y) ws[c + c / W] = weight_at(p.w, p.w_dt, p.w_offset, c);
     if (p.dw)
-      for (int c = threadIdx.x; c < n + n / W + 1; c += blockDim.x) cols[c] = 0.0f;
+      for (int c = threadIdx.x; c < places; c += blockDim.x) cols[c] = 0.0f;
+    __syncthreads();
   } else {
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int e = 0; e < W; ++e) acc[k][e] = 0.0f;
   }
+  const auto weights = [&](int c0, float (&w)[W]) {
+    if (CUT) {
+#pragma unroll
+      for (int e = 0; e < W; ++e) w[e] = ws[c0 + e + (c0 + e) / W];
+    } else {
+      load_weights<DT>(p.w, p.w_dt, p.w_offset, c0, n, weight_whole, w);
+    }
+  };
   int phase = 0;
-  for (int64_t row = group; row < p.rows; row += groups, phase ^= 1) {
+  for (int64_t row = idle ? p.rows : group; row < p.rows; row += groups, phase ^= 1) {
     int64_t off[5];
     row_offsets(p.map, row, off);
-    const int shift = CUT ? (int)(((int64_t)((uintptr_t)p.dy / EB) + off[0]) & (W - 1)) : 0;
-    const bool whole_w = weight_whole && shift == 0;
+    const RowCut cut = CUT ? row_cut<W>(p.dy, EB, off[0], n) : RowCut{0, n};
+    const int edge = CUT ? cut.edge(threadIdx.x, n) : -1;
     const float r = p.rstd[row];
     uint4 yr[K], hr[K], sr[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c0 = (int)(threadIdx.x + k * blockDim.x) * W - shift;
+      const int c0 = cut.head + (int)(threadIdx.x + k * blockDim.x) * W;
       yr[k] = hr[k] = sr[k] = make_uint4(0, 0, 0, 0);
-      if (c0 >= n) continue;
-      if (CUT) {
-        yr[k] = load_cut<DT>(p.dy, off[0], c0, n, p.end[0]);
-        hr[k] = load_cut<DT>(p.h, off[1], c0, n, p.end[1]);
-        if (p.dsum) sr[k] = load_cut<DT>(p.dsum, off[2], c0, n, p.end[2]);
-      } else {
-        yr[k] = load16(reinterpret_cast<const char*>(p.dy) + (off[0] + c0) * EB);
-        hr[k] = load16(reinterpret_cast<const char*>(p.h) + (off[1] + c0) * EB);
-        if (p.dsum) sr[k] = load16(reinterpret_cast<const char*>(p.dsum) + (off[2] + c0) * EB);
-      }
+      if (c0 >= cut.end) continue;
+      yr[k] = load16(reinterpret_cast<const char*>(p.dy) + (off[0] + c0) * EB);
+      hr[k] = load16(reinterpret_cast<const char*>(p.h) + (off[1] + c0) * EB);
+      if (p.dsum) sr[k] = load16(reinterpret_cast<const char*>(p.dsum) + (off[2] + c0) * EB);
     }
-    float dot = 0.0f, none = 0.0f;
+    float dot = 0.0f, none = 0.0f, ye = 0.0f, he = 0.0f, de = 0.0f, we = 0.0f;
+    if (CUT && edge >= 0) {
+      ye = load_plain(p.dy, DT, off[0] + edge);
+      he = load_plain(p.h, DT, off[1] + edge) * r;
+      if (p.dsum) de = load_plain(p.dsum, DT, off[2] + edge);
+      we = ws[edge + edge / W];
+      dot = ye * we * he;
+    }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c0 = (int)(threadIdx.x + k * blockDim.x) * W - shift;
-      if (c0 >= n) continue;
+      const int c0 = cut.head + (int)(threadIdx.x + k * blockDim.x) * W;
+      if (c0 >= cut.end) continue;
       float y[W], h[W], w[W];
       unpack<DT>(yr[k], y);
       unpack<DT>(hr[k], h);
-      load_weights<DT>(p.w, p.w_dt, p.w_offset, c0, n, whole_w && (!CUT || c0 + W <= n), w);
+      weights(c0, w);
 #pragma unroll
       for (int e = 0; e < W; ++e) dot = fmaf(y[e] * w[e], h[e] * r, dot);
     }
@@ -118,40 +132,48 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(cons
     const float mean = __fdiv_rn(dot, (float)p.n);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c0 = (int)(threadIdx.x + k * blockDim.x) * W - shift;
-      if (c0 >= n) continue;
+      const int c0 = cut.head + (int)(threadIdx.x + k * blockDim.x) * W;
+      if (c0 >= cut.end) continue;
       float y[W], h[W], w[W], d[W];
       unpack<DT>(yr[k], y);
       unpack<DT>(hr[k], h);
       unpack<DT>(sr[k], d);
-      load_weights<DT>(p.w, p.w_dt, p.w_offset, c0, n, whole_w && (!CUT || c0 + W <= n), w);
+      weights(c0, w);
 #pragma unroll
       for (int e = 0; e < W; ++e) {
         const float xh = h[e] * r;
         if (CUT) {
-          const int c = c0 + e;
-          if (p.dw && c >= 0 && c < n) cols[c + c / W] = fmaf(y[e], xh, cols[c + c / W]);
+          const int at = c0 + e + (c0 + e) / W;
+          if (p.dw) cols[at] = fmaf(y[e], xh, cols[at]);
         } else {
           acc[k][e] = fmaf(y[e], xh, acc[k][e]);
         }
         d[e] = fmaf(r, fmaf(-xh, mean, y[e] * w[e]), d[e]);
       }
-      if (CUT) store_cut<DT>(p.dh, off[3], c0, n, d);
-      else *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.dh) + (off[3] + c0) * EB) = pack<DT>(d);
+      *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.dh) + (off[3] + c0) * EB) = pack<DT>(d);
       if constexpr (DROP != DROP_NONE) {
         drop_vec<DROP, !CUT, W>(p.drop, g, row * n + c0, d);
-        if (CUT) store_cut<DT>(p.dx, off[4], c0, n, d);
-        else *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.dx) + (off[4] + c0) * EB) = pack<DT>(d);
+        *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.dx) + (off[4] + c0) * EB) = pack<DT>(d);
       }
+    }
+    if (CUT && edge >= 0) {
+      if (p.dw) cols[edge + edge / W] = fmaf(ye, he, cols[edge + edge / W]);
+      de = fmaf(r, fmaf(-he, mean, ye * we), de);
+      store_from_f32(p.dh, DT, off[3] + edge, de);
+      if constexpr (DROP != DROP_NONE) store_from_f32(p.dx, DT, off[4] + edge, drop1(p.drop, g, (uint64_t)(row * n + edge), de));
     }
   }
   if (!p.dw) return;
-  float* const out = p.ws + group * p.n;
-  if (CUT) {
-    if (blockDim.x == 32) __syncwarp();
-    else group_barrier();
-    for (int c = threadIdx.x; c < n; c += blockDim.x) out[c] = cols[c + c / W];
-  } else {
+  if (CUT) {  // the block's groups in order, as one share
+    __syncthreads();
+    float* const out = p.ws + (int64_t)blockIdx.x * n;
+    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < n; c += blockDim.x * blockDim.y) {
+      float sum = 0.0f;
+      for (int y = 1; y <= (int)blockDim.y; ++y) sum += cut_shared[y * places + c + c / W];
+      out[c] = sum;
+    }
+  } else if (!idle) {
+    float* const out = p.ws + group * p.n;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c0 = (int)(threadIdx.x + k * blockDim.x) * W;
@@ -350,12 +372,16 @@ cudaError_t resident_blocks(const void* kernel, int threads, size_t smem, int* b
 template <int DT, int K, int DROP, bool CUT>
 cudaError_t run_norm_grad_row(const NormGradPlan& p, const RowShape& r, int whole, int64_t* groups, cudaStream_t s) {
   const auto kernel = norm_grad_row_kernel<DT, K, DROP, CUT>;
-  const size_t smem = CUT && p.dw ? (size_t)r.ty * (p.n + p.n / kVec<DT> + 1) * 4 : 0;
+  const size_t smem = CUT ? (size_t)(p.dw ? r.ty + 1 : 1) * (p.n + p.n / kVec<DT> + 1) * 4 : 0;
   int per_sm = 1;
   const cudaError_t e = resident_blocks((const void*)kernel, r.tx * r.ty, smem, &per_sm);
   if (e != cudaSuccess) return e;
-  *groups = std::min({p.rows, norm_grad_partials(p.rows, p.n), (int64_t)device_sm_count() * per_sm * r.ty});
-  kernel<<<(unsigned)((*groups + r.ty - 1) / r.ty), dim3(r.tx, r.ty), smem, s>>>(p, whole, *groups);
+  // every group with the same number of rows, give or take one
+  const int64_t most = std::min(norm_grad_partials(p.rows, p.n), (int64_t)device_sm_count() * per_sm * r.ty);
+  const int64_t rows_each = (p.rows + most - 1) / most, count = (p.rows + rows_each - 1) / rows_each;
+  const int64_t blocks = (count + r.ty - 1) / r.ty;
+  kernel<<<(unsigned)blocks, dim3(r.tx, r.ty), smem, s>>>(p, whole, count);
+  *groups = CUT ? blocks : count;
   return cudaGetLastError();
 }
 
@@ -384,7 +410,9 @@ cudaError_t run_norm_grad_stream(const NormGradPlan& p, int threads, int stages,
   int per_sm = 1;
   const cudaError_t e = resident_blocks((const void*)kernel, threads, smem, &per_sm);
   if (e != cudaSuccess) return e;
-  *groups = std::min({p.rows, norm_grad_partials(p.rows, p.n), (int64_t)device_sm_count() * per_sm});
+  const int64_t most = std::min(norm_grad_partials(p.rows, p.n), (int64_t)device_sm_count() * per_sm);
+  const int64_t rows_each = (p.rows + most - 1) / most;
+  *groups = (p.rows + rows_each - 1) / rows_each;
   kernel<<<(unsigned)*groups, threads, smem, s>>>(p, stages, whole);
   return cudaGetLastError();
 }
@@ -434,7 +462,7 @@ cudaError_t launch_norm_grad(const NormGradPlan& p, cudaStream_t s) {
   const int64_t vectors = (p.n + w - 1) / w + 1;
   int64_t groups = norm_grad_partials(p.rows, p.n);
   if (vectors <= 512 * 4 && vectors_fit<5>(p.map, ptr, ebs, p.n, w, &cut)) {
-    const RowShape r = row_shape(p.rows, vectors - (cut ? 0 : 1), 4, 64);
+    const RowShape r = row_shape(p.rows, vectors - 1, 4, 64);
     const int whole = p.w && (uintptr_t)p.w % 16 == 0;
     // the ring pays once its blocks have several rows each
     const RingShape ring = ring_shape(vectors - 1, p.dsum ? 3 : 2);

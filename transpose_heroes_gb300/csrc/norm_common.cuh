@@ -36,7 +36,24 @@ __device__ __forceinline__ void group_sum_max(float& s, float& m, float* red) {
   if (MAX) m = warp_max(v.y);
 }
 
-// W weights from column c0 on (columns outside the row: 1). `whole`: the vector may be one aligned access.
+// A row that need not start or end on a 16-byte boundary: its whole vectors are the columns [head, end), and
+// up to 2 W - 2 elements lie outside them, one each for the row's first threads.
+struct RowCut {
+  int head, end;
+  __device__ __forceinline__ int edge(int thread, int n) const {
+    if (thread < head) return thread;
+    const int c = end + thread - head;
+    return c < n ? c : -1;
+  }
+};
+template <int W>
+__device__ __forceinline__ RowCut row_cut(const void* p, int eb, int64_t off, int n) {
+  const int head = min(n, (int)(-((int64_t)((uintptr_t)p / eb) + off) & (W - 1)));
+  return {head, head + (n - head) / W * W};
+}
+
+// W weights from column c0 on, all of them in the row. `whole`: c0 is a multiple of W and the weights are
+// aligned to 16 bytes, so they are one vector (two in f32 for 16-bit rows).
 template <int DT>
 __device__ __forceinline__ void load_weights(const void* w, int dt, float offset, int c0, int n, bool whole,
                                              float (&v)[kVec<DT>]) {
@@ -55,12 +72,14 @@ __device__ __forceinline__ void load_weights(const void* w, int dt, float offset
   } else if (dt == DT && (uintptr_t)w % 16 == 0) {
     // two aligned vectors, then the words and the half word that c0 asks for
     constexpr int EW = W / 4;  // elements a word
-    const int j = (c0 + W) / W - 1, s = c0 - j * W, last = (n - 1) / W;  // j: rounded down, -1 at least
+    const int j = c0 / W, s = c0 - j * W, last = (n - 1) / W;
     const uint4* const at = reinterpret_cast<const uint4*>(w);
     const bool tail = n % W != 0;  // the last vector would end behind the weights
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    if (j >= 0 && j <= last) a = j == last && tail ? load_cut<DT>(w, 0, (int64_t)j * W, n, nullptr) : __ldg(at + j);
-    if (s && j + 1 <= last) b = j + 1 == last && tail ? load_cut<DT>(w, 0, (int64_t)(j + 1) * W, n, nullptr) : __ldg(at + j + 1);
+    uint4 a = __ldg(at + j), b = a;
+    if (s) {
+      if (j + 1 == last && tail) b = load_cut<DT>(w, 0, (int64_t)(j + 1) * W, n, nullptr);
+      else b = __ldg(at + j + 1);
+    }
     uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     if ((s / EW) & 2) {
 #pragma unroll
@@ -77,7 +96,7 @@ __device__ __forceinline__ void load_weights(const void* w, int dt, float offset
     unpack<DT>(make_uint4(u[0], u[1], u[2], u[3]), v);
   } else {
 #pragma unroll
-    for (int e = 0; e < W; ++e) v[e] = c0 + e >= 0 && c0 + e < n ? load_as_f32(w, dt, c0 + e) : 1.0f;
+    for (int e = 0; e < W; ++e) v[e] = load_as_f32(w, dt, c0 + e);
   }
   if (offset != 0.0f) {
 #pragma unroll

@@ -5,16 +5,9 @@
 
 namespace hlo {
 
-template <int DT, bool CUT>
-__device__ __forceinline__ void store_row_vec(const NormPlan& p, int64_t off, int c0, int n, const float (&y)[kVec<DT>], float inv) {
+template <int DT>
+__device__ __forceinline__ void store_row_vec(const NormPlan& p, int64_t at, const float (&y)[kVec<DT>], float inv) {
   constexpr int W = kVec<DT>;
-  const bool full = !CUT || (c0 >= 0 && c0 + W <= n);
-  if (!full) {
-#pragma unroll
-    for (int e = 0; e < W; ++e)
-      if (c0 + e >= 0 && c0 + e < n) store_out(p, off + c0 + e, y[e], inv);
-    return;
-  }
   if (p.quant != NQ_NONE) {
     uint32_t u[2] = {0, 0};
 #pragma unroll
@@ -25,15 +18,15 @@ __device__ __forceinline__ void store_row_vec(const NormPlan& p, int64_t off, in
       else b = f8_bits(__fmul_rn(y[e], inv));
       u[e >> 2] |= (uint32_t)b << (8 * (e & 3));
     }
-    char* a = reinterpret_cast<char*>(p.out) + off + c0;
+    char* a = reinterpret_cast<char*>(p.out) + at;
     if (W == 8) *reinterpret_cast<uint2*>(a) = make_uint2(u[0], u[1]);
     else *reinterpret_cast<uint32_t*>(a) = u[0];
   } else if (p.out_dt == DT) {
-    *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.out) + (off + c0) * (16 / W)) = pack<DT>(y);
+    *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.out) + at * (16 / W)) = pack<DT>(y);
   } else {
 #pragma unroll
     for (int q = 0; q < W / 4; ++q)
-      *(reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + off + c0) + q) =
+      *(reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at) + q) =
           make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
   }
 }
@@ -41,8 +34,9 @@ __device__ __forceinline__ void store_row_vec(const NormPlan& p, int64_t off, in
 // One read and one write of everything: blockDim.x threads hold a row, K vectors of 16 bytes each, and the
 // block blockDim.y rows. All of a thread's loads are issued before the first is used; sum is stored before
 // the row's barrier, out after it.
-// CUT: rows that start or end inside a vector (an odd length, a pitch). Vector j covers the columns
-// j W - shift ..., where shift is the row's start modulo W elements, the same for every operand.
+// CUT: rows that start or end inside a vector (an odd length, a pitch): the vectors begin at the row's first
+// 16-byte boundary, the same column in every operand, and the up to 2 W - 2 elements before and behind them
+// go to a thread each.
 template <int DT, int K, int DROP, bool CUT>
 __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_row_kernel(const __grid_constant__ NormPlan p, int weight_whole) {
   constexpr int W = kVec<DT>, EB = 16 / W;
@@ -52,27 +46,31 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_row_kernel(const __g
   if (row >= p.rows) return;  // the whole group: its barrier is its own
   int64_t off[4];
   row_offsets(p.map, row, off);
-  const int shift = CUT ? (int)(((int64_t)((uintptr_t)p.x / EB) + off[0]) & (W - 1)) : 0;
+  const RowCut cut = CUT ? row_cut<W>(p.x, EB, off[0], n) : RowCut{0, n};
+  const int edge = CUT ? cut.edge(threadIdx.x, n) : -1;
   uint4 xr[K], rr[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c0 = (int)(threadIdx.x + k * blockDim.x) * W - shift;
+    const int c0 = cut.head + (int)(threadIdx.x + k * blockDim.x) * W;
     xr[k] = rr[k] = make_uint4(0, 0, 0, 0);
-    if (c0 >= n) continue;
-    if (CUT) {
-      xr[k] = load_cut<DT>(p.x, off[0], c0, n, p.end[0]);
-      if (p.res) rr[k] = load_cut<DT>(p.res, off[1], c0, n, p.end[1]);
-    } else {
-      xr[k] = load16(reinterpret_cast<const char*>(p.x) + (off[0] + c0) * EB);
-      if (p.res) rr[k] = load16(reinterpret_cast<const char*>(p.res) + (off[1] + c0) * EB);
-    }
+    if (c0 >= cut.end) continue;
+    xr[k] = load16(reinterpret_cast<const char*>(p.x) + (off[0] + c0) * EB);
+    if (p.res) rr[k] = load16(reinterpret_cast<const char*>(p.res) + (off[1] + c0) * EB);
+  }
+  float ve = 0.0f;
+  if (CUT && edge >= 0) {
+    ve = load_plain(p.x, DT, off[0] + edge);
+    const float res = p.res ? load_plain(p.res, DT, off[1] + edge) : 0.0f;
+    if constexpr (DROP != DROP_NONE) ve = drop1(p.drop, Philox<DROP>(p.drop), (uint64_t)(row * n + edge), ve);
+    if (p.res) ve = __fadd_rn(res, ve);
+    if (p.sum) store_from_f32(p.sum, DT, off[2] + edge, ve);
   }
   const Philox<DROP> g(p.drop);
-  const bool whole_w = weight_whole && shift == 0;
-  float v[K][W], ss = 0.0f, top = 0.0f;
+  const bool whole_w = weight_whole && cut.head == 0;
+  float v[K][W], ss = ve * ve, top = 0.0f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c0 = (int)(threadIdx.x + k * blockDim.x) * W - shift;
+    const int c0 = cut.head + (int)(threadIdx.x + k * blockDim.x) * W;
     unpack<DT>(xr[k], v[k]);
     float res[W];
     unpack<DT>(rr[k], res);  // +0 without a residual
@@ -84,18 +82,17 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_row_kernel(const __g
     }
 #pragma unroll
     for (int e = 0; e < W; ++e) ss = fmaf(v[k][e], v[k][e], ss);
-    if (c0 >= n) continue;
-    if (p.sum) {
-      if (CUT) store_cut<DT>(p.sum, off[2], c0, n, v[k]);
-      else *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.sum) + (off[2] + c0) * EB) = pack<DT>(v[k]);
-    }
+    if (c0 >= cut.end) continue;
+    if (p.sum) *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.sum) + (off[2] + c0) * EB) = pack<DT>(v[k]);
     if (p.quant == NQ_ROW) {
       float w[W];
-      load_weights<DT>(p.w, p.w_dt, p.w_offset, c0, n, whole_w && (!CUT || c0 + W <= n), w);
+      load_weights<DT>(p.w, p.w_dt, p.w_offset, c0, n, whole_w, w);
 #pragma unroll
       for (int e = 0; e < W; ++e) top = ieee_max(top, fabsf(v[k][e] * w[e]));
     }
   }
+  const float we = CUT && edge >= 0 ? weight_at(p.w, p.w_dt, p.w_offset, edge) : 0.0f;
+  if (CUT && edge >= 0) top = ieee_max(top, fabsf(ve * we));
   group_sum_max<true>(ss, top, red);
   const float r = rsqrtf(__fdiv_rn(ss, (float)p.n) + p.eps);
   if (threadIdx.x == 0 && p.rstd) p.rstd[row] = r;
@@ -107,14 +104,15 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_row_kernel(const __g
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c0 = (int)(threadIdx.x + k * blockDim.x) * W - shift;
-    if (c0 >= n) continue;
+    const int c0 = cut.head + (int)(threadIdx.x + k * blockDim.x) * W;
+    if (c0 >= cut.end) continue;
     float w[W], y[W];
-    load_weights<DT>(p.w, p.w_dt, p.w_offset, c0, n, whole_w && (!CUT || c0 + W <= n), w);
+    load_weights<DT>(p.w, p.w_dt, p.w_offset, c0, n, whole_w, w);
 #pragma unroll
     for (int e = 0; e < W; ++e) y[e] = __fmul_rn(__fmul_rn(v[k][e], r), w[e]);
-    store_row_vec<DT, CUT>(p, off[3], c0, n, y, inv);
+    store_row_vec<DT>(p, off[3] + c0, y, inv);
   }
+  if (CUT && edge >= 0) store_out(p, off[3] + edge, __fmul_rn(__fmul_rn(ve, r), we), inv);
 }
 
 template <int DT, int K, int DROP>
