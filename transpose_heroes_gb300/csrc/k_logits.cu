@@ -94,14 +94,16 @@ __device__ __forceinline__ float warp_max_of(float v) {
   return r;
 }
 
-// Dynamic shared memory for slabs of `slab` tokens: their counts, a bit for each that occurs, and the list of
-// those with their values.
+// Dynamic shared memory for slabs of `slab` tokens: a bit for each that occurs; their counts, one for each token
+// of the slab (places = slab) or for each place of a table of keys; and the list of those that occur, with
+// their values.
 struct LogitsShared {
-  size_t bits, value, list, bytes;
-  __host__ __device__ LogitsShared(int slab, int count_bytes, int64_t max_length) {
+  size_t bits, key, value, list, bytes;
+  __host__ __device__ LogitsShared(int slab, bool table, int places, int count_bytes, int64_t max_length) {
     const size_t listed = (size_t)(slab < max_length ? slab : max_length);
-    bits = (size_t)slab * count_bytes;
-    value = bits + slab / 8;
+    bits = (size_t)places * count_bytes;
+    key = bits + slab / 8;
+    value = key + (table ? (size_t)places * 4 : 0);
     list = value + listed * 4;
     bytes = list + listed * count_bytes;
   }
@@ -112,13 +114,16 @@ struct LogitsShared {
 // and all its lanes would run their division. So a slab has three parts:
 //  1. mark the tokens that occur in the history and count their occurrences after the prompt, in shared memory
 //     (COUNT is uint16_t for histories below 2^16, else uint32_t; adding and or-ing whole numbers gives one
-//     result in any order). Whoever finds a token first puts it on a list.
+//     result in any order). Whoever finds a token first puts it on a list. TABLE: counts are kept for the
+//     tokens that occur alone, in a table with open addressing, so that a slab can be a whole row; else
+//     for every token of the slab.
 //  2. a thread for each listed token works out its value, from the logit itself.
 //  3. stream the slab, with the listed tokens masked out; then store their values over it.
 // The slab's first logits are requested before all this. The blocks' best tokens are written to the first
 // block's shared memory, and only that block waits for them.
-template <int DT, int U, typename COUNT>
-__global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_constant__ LogitsPlan p, int cluster, int batches) {
+template <int DT, int U, typename COUNT, bool TABLE>
+__global__ void __launch_bounds__(kThreads, 2)
+    logits_kernel(const __grid_constant__ LogitsPlan p, int cluster, int batches, int table_bits) {
   constexpr int W = kVec<DT>, EB = 16 / W;
   constexpr int CB = sizeof(COUNT), CPW = 4 / CB;  // counts a 32-bit word
   extern __shared__ __align__(16) char shared[];
@@ -131,9 +136,11 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
   const int rank = (int)(blockIdx.x - b * cluster), tid = threadIdx.x, threads = blockDim.x;
   const int vocab = (int)p.vocab, words = (vocab + 31) / 32;
   const int batch = threads * U * W, slab = batches * batch;
-  const LogitsShared parts(slab, CB, p.max_length);
+  const int places = TABLE ? 1 << table_bits : slab;
+  const LogitsShared parts(slab, TABLE, places, CB, p.max_length);
   uint32_t* const seen = reinterpret_cast<uint32_t*>(shared);
   uint32_t* const bits = reinterpret_cast<uint32_t*>(shared + parts.bits);
+  uint32_t* const key = reinterpret_cast<uint32_t*>(shared + parts.key);  // a token's number in the slab + 1, or 0
   float* const value = reinterpret_cast<float*>(shared + parts.value);
   COUNT* const list = reinterpret_cast<COUNT*>(shared + parts.list);
   const char* const x_row = reinterpret_cast<const char*>(p.x) + b * p.x_stride * EB;
@@ -147,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
     len = (int)p.max_length;
     if (p.lengths) len = max(0, min(len, p.lengths[b]));
     if (p.prompts) prompt = p.prompts[b];
-    for (int i = tid; i < slab * CB / 16 + slab / 128; i += threads) reinterpret_cast<uint4*>(shared)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < (int)(parts.value / 16); i += threads) reinterpret_cast<uint4*>(shared)[i] = make_uint4(0, 0, 0, 0);
     if (tid == 0) listed = 0;
   }
   float best_v = __int_as_float(0xFF800000);
@@ -198,17 +205,26 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
         const int token = i < len ? __ldg(h + i) : -1;
         const uint32_t at = (uint32_t)token - (uint32_t)s0;
         bool first = false;
+        uint32_t place = at;
         if (at < limit && token >= 0) {  // not another slab's token, nor one outside the vocabulary
           const uint32_t m = 1u << (at & 31);
-          first = !(atomicOr(&bits[at >> 5], m) & m);
-          if (i >= prompt) atomicAdd(&seen[at / CPW], 1u << (8 * CB * (int)(at % CPW)));
+          if (TABLE) {
+            atomicOr(&bits[at >> 5], m);
+            place = (at * 2654435761u) >> (32 - table_bits);
+            uint32_t found;  // the table has more places than the history has tokens, so one is free
+            while ((found = atomicCAS(&key[place], 0u, at + 1)) != 0 && found != at + 1) place = (place + 1) & (places - 1);
+            first = found == 0;
+          } else {
+            first = !(atomicOr(&bits[at >> 5], m) & m);
+          }
+          if (i >= prompt) atomicAdd(&seen[place / CPW], 1u << (8 * CB * (int)(place % CPW)));
         }
         const uint32_t firsts = __ballot_sync(0xffffffffu, first);
         if (firsts) {  // one place on the list for all of the warp's
-          int place = 0;
-          if (lane == 0) place = atomicAdd(&listed, __popc(firsts));
-          place = __shfl_sync(0xffffffffu, place, 0) + __popc(firsts & ((1u << lane) - 1));
-          if (first) list[place] = (COUNT)at;
+          int index = 0;
+          if (lane == 0) index = atomicAdd(&listed, __popc(firsts));
+          index = __shfl_sync(0xffffffffu, index, 0) + __popc(firsts & ((1u << lane) - 1));
+          if (first) list[index] = (COUNT)place;
         }
       }
       __syncthreads();
@@ -219,21 +235,21 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
         float top_v = __int_as_float(0xFF800000);
         int top_i = -1;
         for (int i = tid; i < n; i += threads) {
-          const int at = (int)list[i], c = s0 + at;
+          const int place = (int)list[i], c = s0 + (TABLE ? (int)key[place] - 1 : place);
+          COUNT* const count = reinterpret_cast<COUNT*>(seen) + place;
           float l = load_plain(x_row, DT, c);
-          const uint32_t s = reinterpret_cast<COUNT*>(seen)[at];
           if (bias) l = __fadd_rn(l, __ldg(bias + c));
-          l = penalised(l, (float)s, rep, freq, pres);
+          l = penalised(l, (float)*count, rep, freq, pres);
           if (mask && !((__ldg(mask + (c >> 5)) >> (c & 31)) & 1u)) l = __int_as_float(0xFF800000);
           value[i] = l;
-          reinterpret_cast<COUNT*>(seen)[at] = 0;
+          *count = 0;
           if (l > top_v || (l == top_v && c < top_i)) {
             top_v = l;
             top_i = c;
           }
         }
-        const unsigned long long key = top_i >= 0 ? choice_key(top_v, top_i) : 0;
-        best = key > best ? key : best;
+        const unsigned long long found = top_i >= 0 ? choice_key(top_v, top_i) : 0;
+        best = found > best ? found : best;
         __syncthreads();
       }
     }
@@ -334,9 +350,10 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
     if (n > 0) {
       __syncthreads();  // the slab is stored
       for (int i = tid; i < n; i += threads) {
-        const int at = (int)list[i];
+        const int place = (int)list[i], at = TABLE ? (int)key[place] - 1 : place;
         if (p.out) store_from_f32(p.out, p.out_dt, out_off + s0 + at, value[i]);
         bits[at >> 5] = 0;
+        if (TABLE) key[place] = 0;
       }
       if (tid == 0) listed = 0;
     }
@@ -365,9 +382,10 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
   if (tid == 0) p.token[b] = best ? (int32_t)~(uint32_t)best : -1;
 }
 
-template <int DT, int U, typename COUNT>
-cudaError_t run_logits(const LogitsPlan& p, int threads, int cluster, int batches, cudaStream_t s) {
-  const auto kernel = logits_kernel<DT, U, COUNT>;
+template <int DT, int U, typename COUNT, bool TABLE>
+cudaError_t run_logits(const LogitsPlan& p, int threads, int cluster, int batches, int table_bits, cudaStream_t s) {
+  const auto kernel = logits_kernel<DT, U, COUNT, TABLE>;
+  const int slab = threads * U * kVec<DT> * batches;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -376,7 +394,7 @@ cudaError_t run_logits(const LogitsPlan& p, int threads, int cluster, int batche
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(p.batch * cluster));
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = p.history ? LogitsShared(threads * U * kVec<DT> * batches, sizeof(COUNT), p.max_length).bytes : 0;
+  cfg.dynamicSmemBytes = p.history ? LogitsShared(slab, TABLE, TABLE ? 1 << table_bits : slab, sizeof(COUNT), p.max_length).bytes : 0;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
@@ -384,7 +402,7 @@ cudaError_t run_logits(const LogitsPlan& p, int threads, int cluster, int batche
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, kernel, p, cluster, batches);
+  return cudaLaunchKernelEx(&cfg, kernel, p, cluster, batches, table_bits);
 }
 
 template <int DT>
@@ -392,20 +410,29 @@ cudaError_t run_logits_type(const LogitsPlan& p, cudaStream_t s) {
   constexpr int W = kVec<DT>;
   const int64_t vectors = p.vocab / W + 2;
   const int threads = (int)std::min<int64_t>(kThreads, (vectors + 31) / 32 * 32);
-  // as many blocks a row as give every SM one and a half, but no more than the row has vectors for: 256 rows
-  // of 131072 take 70 us with one or two blocks a row, 76 us with four, 91 us with eight (a block's
-  // work on its slabs' histories does not shrink with them)
+  // as many blocks a row as give every SM one and a half, but no more than the row has vectors for
   int cluster = 1;
   while (cluster < 8 && p.batch * cluster * 2 < 3 * device_sm_count() && cluster * threads < vectors) cluster *= 2;
   // four vectors a thread where a block has that many
   const int u = vectors >= (int64_t)3 * threads * cluster ? 4 : 1;
+  const int64_t batch = (int64_t)threads * u * W, needed = (vectors * W + batch * cluster - 1) / (batch * cluster);
+  // A table where it leaves an SM two blocks; slabs of 131072 tokens then, as the work on a slab's history does not
+  // shrink with it: 256 rows of 131072 with up to 4096 entries each take 64 us, with counts for all of a
+  // slab's tokens (slabs of 64 KB of counts) 68 us
+  int table_bits = 6;
+  while ((int64_t)3 << table_bits < 4 * p.max_length && table_bits < 14) ++table_bits;
+  if (table_bits <= 13) {
+    const int batches = (int)std::max<int64_t>(1, std::min((1 << 17) / batch, needed));
+    if (u == 4) return run_logits<DT, 4, uint16_t, true>(p, threads, cluster, batches, table_bits, s);
+    return run_logits<DT, 1, uint16_t, true>(p, threads, cluster, batches, table_bits, s);
+  }
   const bool narrow = p.max_length < (1 << 16);
-  // slabs of at most 64 KB of counts, so that an SM holds two blocks
-  const int64_t room = 64 * 1024 / (threads * u * W * (narrow ? 2 : 4));
-  const int64_t needed = (vectors + (int64_t)threads * u * cluster - 1) / ((int64_t)threads * u * cluster);
-  const int batches = (int)std::max<int64_t>(1, std::min(room, needed));
-  if (u == 4) return narrow ? run_logits<DT, 4, uint16_t>(p, threads, cluster, batches, s) : run_logits<DT, 4, uint32_t>(p, threads, cluster, batches, s);
-  return narrow ? run_logits<DT, 1, uint16_t>(p, threads, cluster, batches, s) : run_logits<DT, 1, uint32_t>(p, threads, cluster, batches, s);
+  const int batches = (int)std::max<int64_t>(1, std::min(64 * 1024 / (batch * (narrow ? 2 : 4)), needed));
+  if (u == 4)
+    return narrow ? run_logits<DT, 4, uint16_t, false>(p, threads, cluster, batches, 0, s)
+                  : run_logits<DT, 4, uint32_t, false>(p, threads, cluster, batches, 0, s);
+  return narrow ? run_logits<DT, 1, uint16_t, false>(p, threads, cluster, batches, 0, s)
+                : run_logits<DT, 1, uint32_t, false>(p, threads, cluster, batches, 0, s);
 }
 
 cudaError_t launch_logits(const LogitsPlan& p, cudaStream_t s) {

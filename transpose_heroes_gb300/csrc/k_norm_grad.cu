@@ -51,6 +51,9 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(const __grid
   }
 }
 
+// Lets the next kernel of the stream be set up while this one's last blocks finish.
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---- gradient, rows held in registers ------------------------------------------------------------------------
 // Row groups walk the rows with a stride of all groups, keep dy, h and dsum of a row in registers (packed)
 // across its one reduction, and add each row's share of dweight to sums of their own: in registers, where
@@ -164,6 +167,7 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(cons
     }
   }
   if (!p.dw) return;
+  allow_next();
   if (CUT) {  // the block's groups in order, as one share
     __syncthreads();
     float* const out = p.ws + (int64_t)blockIdx.x * n;
@@ -310,6 +314,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) norm_grad_stream_ke
     }
   }
   if (!p.dw) return;
+  allow_next();
   float* const out = p.ws + (int64_t)blockIdx.x * n;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -321,13 +326,17 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) norm_grad_stream_ke
   }
 }
 
-// dw[c] = sum of the groups' shares, in a fixed order: 32 columns a block, 32 threads a column.
+// dw[c] = sum of the groups' shares, in a fixed order: 32 columns a block, 32 threads a column. It is launched before
+// the kernel that writes them has ended, and waits for that end.
 __global__ void __launch_bounds__(1024) norm_grad_join_kernel(const float* ws, float* dw, int64_t n, int64_t groups) {
   __shared__ float part[32][33];
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float acc = 0.0f;
-  if (c < n)
-    for (int64_t k = threadIdx.y; k < groups; k += 32) acc += ws[k * n + c];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c < n) {
+#pragma unroll 4
+    for (int64_t k = threadIdx.y; k < groups; k += 32) acc += __ldcg(ws + k * n + c);
+  }
   part[threadIdx.y][threadIdx.x] = acc;
   __syncthreads();
   acc = warp_sum(part[threadIdx.x][threadIdx.y]);
@@ -483,8 +492,17 @@ cudaError_t launch_norm_grad(const NormGradPlan& p, cudaStream_t s) {
     else if (p.drop.mode == DROP_HOST) norm_grad_any_kernel<DROP_HOST><<<any_grid(p.rows), kAnyThreads, 0, s>>>(p);
     else norm_grad_any_kernel<DROP_DEVICE><<<any_grid(p.rows), kAnyThreads, 0, s>>>(p);
   }
-  if (p.dw) norm_grad_join_kernel<<<(unsigned)((p.n + 31) / 32), dim3(32, 32), 0, s>>>(p.ws, p.dw, p.n, groups);
-  return cudaGetLastError();
+  if (!p.dw) return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)((p.n + 31) / 32));
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_grad_join_kernel, (const float*)p.ws, p.dw, p.n, groups);
 }
 
 }  // namespace hlo
