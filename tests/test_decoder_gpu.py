@@ -1,0 +1,141 @@
+"""The layer operators together: the small decoder of transpose_heroes_gb300.decoder serves and trains with
+them. The same model written in 64 bits with torch's own operations is the reference."""
+
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import layer_reference as ref
+import transpose_heroes_gb300 as hf
+
+pytestmark = pytest.mark.gpu
+
+PROMPT = [3, 1, 4, 1, 5, 9, 2, 6, 5, 3, 5]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from transpose_heroes_gb300 import build
+
+    build.build()
+    hf.lib()
+
+
+def model(**kw):
+    from transpose_heroes_gb300 import decoder
+
+    return decoder.Decoder(vocab=300, width=96, layers=2, heads=4, kv=2, dim=32, hidden=160, **kw)
+
+
+def reference(m, tokens, p=0.0, seed=0):
+    """(logits of every position, the parameters they depend on), in 64 bits on the CPU."""
+    D = lambda t: t.detach().double().cpu().requires_grad_(True)  # noqa: E731
+    embed, head, last = D(m.embed), D(m.head), D(m.last)
+    layers = [{k: D(v) for k, v in w.items()} for w in m.layers]
+    tokens = torch.as_tensor(tokens).cpu()
+    n, place = len(tokens), [0]
+
+    def drop(x):
+        if not p:
+            return x
+        k = torch.from_numpy(ref.keep(p, seed, place[0], x.numel()).reshape(x.shape)).double()
+        place[0] += 1
+        return x * k * ref.drop_scale(p)
+
+    norm = lambda t, w: t / (t.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * w  # noqa: E731
+    angle = torch.arange(n).double()[:, None] * torch.tensor([10000.0 ** (-2 * i / m.dim) for i in range(m.dim // 2)]).double()
+    c, s = angle.cos()[:, None], angle.sin()[:, None]
+
+    def turn(x):
+        a, b = x[..., :m.dim // 2], x[..., m.dim // 2:]
+        return torch.cat([a * c - b * s, b * c + a * s], -1)
+
+    h = drop(embed[tokens])
+    for w in layers:
+        qkv = (norm(h, w["n1"]) @ w["qkv"]).view(n, m.heads + 2 * m.kv, m.dim)
+        q, k, v = qkv.split([m.heads, m.kv, m.kv], 1)
+        k, v = turn(k).repeat_interleave(m.heads // m.kv, 1), v.repeat_interleave(m.heads // m.kv, 1)
+        a = torch.einsum("thd,shd->hts", turn(q), k) / math.sqrt(m.dim)
+        a = a.masked_fill(torch.ones(n, n).triu(1).bool(), -math.inf).softmax(-1)
+        h = h + drop(torch.einsum("hts,shd->thd", a, v).flatten(1) @ w["o"])
+        y = norm(h, w["n2"])
+        h = h + drop((torch.nn.functional.silu(y @ w["gate"]) * (y @ w["up"])) @ w["down"])
+    return norm(h, last) @ head, [embed, head, last] + [t for w in layers for t in w.values()]
+
+
+def test_prompt_and_single_tokens_agree_with_64_bits():
+    """Two layers of f32 products of up to 160 terms and a handful of operators: far inside 1e-4 of the logits'
+    size (f32 products of k terms err by at most k 2^-24, here about 1e-5)."""
+    m = model()
+    want, _ = reference(m, PROMPT)
+    scale = float(want.detach().abs().max())
+    whole = m.forward(torch.tensor(PROMPT, device="cuda"), [None] * 2, 0)
+    assert float((whole[0].cpu().double() - want[-1].detach()).abs().max()) <= 1e-4 * scale
+    cache = [None] * 2
+    for i, t in enumerate(PROMPT):
+        one = m.forward(torch.tensor([t], device="cuda"), cache, i)
+        assert float((one[0].cpu().double() - want[i].detach()).abs().max()) <= 1e-4 * scale
+
+
+def test_generation_is_the_references_greedy_choice():
+    m = model()
+    got = m.generate(PROMPT, 6, repetition=1.3, frequency=0.2, presence=0.1)
+    tokens = list(PROMPT)
+    for t in got:
+        l = reference(m, tokens)[0][-1].detach().numpy()
+        made = tokens[len(PROMPT):]
+        for v in set(tokens):
+            l[v] = l[v] / np.float32(1.3) if l[v] > 0 else l[v] * np.float32(1.3)
+        for v in set(made):
+            l[v] -= 0.2 * made.count(v) + 0.1
+        top = np.sort(l)[-2:]
+        if top[1] - top[0] > 1e-3:  # otherwise f32 may choose either
+            assert t == int(l.argmax())
+        tokens.append(t)
+
+
+def test_generation_under_a_mask():
+    m = model()
+    bits = np.zeros(10, np.uint32)
+    for v in (7, 40, 299):
+        bits[v // 32] |= np.uint32(1 << (v % 32))
+    mask = torch.from_numpy(bits.view(np.int32)).cuda()
+    assert set(m.generate(PROMPT, 8, mask=mask)) <= {7, 40, 299}
+    assert m.generate(PROMPT, 8, mask=torch.zeros_like(mask)) == []
+
+
+@pytest.mark.parametrize("p", [0.0, 0.2])
+def test_training_gradients_agree_with_64_bits(p):
+    m = model()
+    for t in m.parameters():
+        t.requires_grad_(True)
+    tokens = torch.tensor(PROMPT, device="cuda")
+    loss = m.loss(tokens, p=p, seed=5)
+    loss.backward()
+    logits, params = reference(m, PROMPT[:-1], p, 5)
+    want = torch.nn.functional.cross_entropy(logits, tokens[1:].cpu())
+    want.backward()
+    assert abs(float(loss.detach()) - float(want.detach())) <= 1e-4 * (1 + abs(float(want.detach())))
+    for got, w in zip(m.parameters(), params):
+        # back through two layers the f32 errors of a dozen products add up: still under 1e-3 of the gradient's size
+        assert float((got.grad.cpu().double() - w.grad).abs().max()) <= 1e-3 * float(w.grad.abs().max())
+
+
+def test_training_learns():
+    m = model()
+    for t in m.parameters():
+        t.requires_grad_(True)
+    opt = torch.optim.Adam(m.parameters(), lr=2e-3)
+    tokens = torch.tensor([3, 1, 4, 1, 5, 9, 2, 6] * 6, device="cuda")
+    first = float(m.loss(tokens).detach())
+    for step in range(30):
+        opt.zero_grad()
+        m.loss(tokens, p=0.1, seed=step).backward()
+        opt.step()
+    assert float(m.loss(tokens).detach()) < 0.2 * first
+    assert m.generate([3, 1, 4, 1, 5, 9, 2, 6, 3, 1], 6) == [4, 1, 5, 9, 2, 6]

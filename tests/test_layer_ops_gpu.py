@@ -136,6 +136,13 @@ def test_rms_norm(rows, n, dtype):
     check_norm(rows, n, dtype, residual=False, weight="f32", p=0.3, seed=9)
 
 
+@pytest.mark.parametrize("rows,n", [(310, 256), (310, 512), (320, 1000), (310, 1001), (310, 5120), (306, 8199)])
+def test_rms_norm_of_many_rows(rows, n):
+    """Past two rows an SM, where a thread holds several vectors."""
+    check_norm(rows, n, "bf16", p=0.1)
+    check_norm(rows, n, "f32", out="f32")
+
+
 @pytest.mark.parametrize("out", ["x", "f32", "s8", "f8", "static"])
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,n", [(1, 1), (4, 8), (3, 77), (33, 256), (5, 1001), (2, 5120), (2, 8192), (1, 33001)])
@@ -248,6 +255,16 @@ def test_rms_norm_backward_strides(rows, n, pitch, shift, dtype):
 @pytest.mark.parametrize("in_place", ["dy", "h", "dsum"])
 def test_rms_norm_backward_in_place(in_place, n):
     check_grad(9, n, "bf16", in_place=in_place, p=0.1)
+
+
+@pytest.mark.parametrize("rows,n,dtype", [(640, 64, "f32"), (613, 512, "bf16"), (640, 1024, "f16"), (700, 4096, "bf16"), (611, 4104, "f32"),
+                                          (620, 8192, "bf16"), (610, 12000, "bf16"), (609, 16384, "f16"), (2000, 1001, "bf16")])
+def test_rms_norm_backward_of_many_rows(rows, n, dtype):
+    """Rows that stream through shared memory: each number of vectors a thread, with and without dsum, weights of
+    either type, and a pitch."""
+    check_grad(rows, n, dtype, p=0.1)
+    check_grad(rows, n, dtype, dsum=False, weight="f32", w_offset=1.0, pitch=64, shift=8)
+    check_grad(rows, n, dtype, weight=None, dweight=False, in_place="h")
 
 
 def test_rms_norm_backward_is_deterministic():
@@ -496,6 +513,21 @@ def test_logits_many_occurrences_of_one_token():
     check_logits(2, 100, "f32", m=40000)
 
 
+@pytest.mark.parametrize("m", [6144, 6145, 9000, 66000])
+@pytest.mark.parametrize("batch,vocab", [(2, 40000), (3, 150001)])
+def test_logits_long_histories(batch, vocab, m):
+    """The longest history that is kept in a table, the shortest that is not, and one whose counts need 32 bits;
+    vocabularies of several slabs."""
+    check_logits(batch, vocab, "bf16", m=m, bias="row", mask="rows")
+
+
+def test_logits_of_a_full_table():
+    """As many different tokens as entries, all of them in one row's slab."""
+    g = np.random.default_rng(3)
+    hist = np.stack([g.permutation(9000)[:6144] for _ in range(4)]).astype(np.int32)
+    check_logits(4, 9000, "f32", m=6144, history=hist, token=True)
+
+
 def test_logits_ties_go_to_the_lowest_token():
     x = torch.zeros(2, 70000, device="cuda", dtype=torch.bfloat16)
     x[0, 123] = x[0, 60000] = 4.0
@@ -526,6 +558,110 @@ def test_calls_run_on_the_stream_they_are_given():
     hf.logits_process(y, token=tok, stream=s)
     s.synchronize()
     assert bool((y == 1.0).all()) and bool((tok == 0).all())
+
+
+def test_calls_are_captured_into_a_graph():
+    """Norm, gradient (two kernels), rotary and logits replayed on new inputs give what direct calls give."""
+    rows, n = 700, 1032
+    x, r, gy = (torch.from_numpy(rnd(s, rows, n)).to(torch.bfloat16).cuda() for s in (1, 2, 3))
+    y, h, dh = (torch.empty_like(x) for _ in range(3))
+    rs, dw = torch.empty(rows, device="cuda"), torch.empty(n, device="cuda")
+    ws = torch.empty(hf.rms_norm_workspace_size(rows, n), dtype=torch.uint8, device="cuda")
+    q = torch.from_numpy(rnd(4, 50, 3, 64)).float().cuda()
+    qo = torch.empty_like(q)
+    pos, turns = torch.arange(50, dtype=torch.int32, device="cuda"), torch.from_numpy(hf.rotary_turns(64)).cuda()
+    hist = torch.arange(rows * 9, dtype=torch.int32, device="cuda").view(rows, 9) % n
+    half = torch.full((rows,), 0.5, device="cuda")
+    tok = torch.empty(rows, dtype=torch.int32, device="cuda")
+
+    def calls():
+        hf.rms_norm(x, y, residual=r, sum_out=h, rstd=rs)
+        hf.rms_norm_backward(gy, h, rs, dh, dweight=dw, workspace=ws)
+        hf.rotary(q, qo, pos, turns)
+        hf.logits_process(y, history=hist, presence=half, token=tok)
+
+    calls()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    x.copy_(torch.from_numpy(rnd(9, rows, n)))
+    q.copy_(torch.from_numpy(rnd(8, 50, 3, 64)))
+    g.replay()
+    got = [t.clone() for t in (y, h, dh, rs, dw, qo, tok)]
+    for t in (y, h, dh, rs, dw, qo, tok):
+        t.zero_()
+    calls()
+    assert all(torch.equal(a, b) for a, b in zip(got, (y, h, dh, rs, dw, qo, tok)))
+
+
+# ---- offsets past 32 bits ------------------------------------------------------------------------------------
+def _room(gigabytes):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gigabytes * 1e9:
+        pytest.skip(f"needs {gigabytes} GB of device memory")
+
+
+def test_dropout_past_2_31_elements():
+    _room(16)
+    n = (1 << 31) + 4099
+    x = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    hf.dropout(x, x, hf.Dropout(0.5, 77, 6))
+    for at in (0, (1 << 31) - 64, n - 131):
+        first = at // 4 * 4
+        words = ref.philox(77, 6, np.arange(first // 4, (at + 131 + 3) // 4)).reshape(-1)[at - first:at - first + 131]
+        assert np.array_equal(host(x[at:at + 131]) == 2.0, words >= 1 << 31)
+
+
+def test_rms_norm_past_2_31_elements():
+    _room(32)
+    n = 4096
+    rows = (1 << 31) // n + 9
+    x = torch.ones(rows, n, dtype=torch.bfloat16, device="cuda")
+    last, ld = dev(rnd(1, 8, n), "bf16")
+    x[-8:] = last
+    y = torch.empty_like(x)
+    rs = torch.empty(rows, device="cuda")
+    hf.rms_norm(x, y, rstd=rs)
+    _, r, want, _, er, ey = ref.rms_norm(ld, np.ones(n))
+    close(y[-8:], want, ey, "bf16")
+    dw = torch.empty(n, device="cuda")
+    ws = torch.empty(hf.rms_norm_workspace_size(rows, n), dtype=torch.uint8, device="cuda")
+    rs.fill_(1.0)
+    hf.rms_norm_backward(x, x, rs, y, dweight=dw, workspace=ws)
+    dh, _, _, edh, _, _ = ref.rms_norm_backward(ld, ld, np.ones(8), np.ones(n))
+    close(y[-8:], dh, edh, "bf16")
+    want = (rows - 8) + (ld * ld).sum(0)
+    # ones add exactly up to 2^24; the last rows' products round
+    assert np.all(np.abs(host(dw) - want) <= want * 64 * ref.U)
+
+
+def test_rotary_past_2_31_elements():
+    _room(16)
+    tokens, heads, dim = (1 << 31) // (64 * 128) + 5, 64, 128
+    x = torch.zeros(tokens, heads, dim, dtype=torch.bfloat16, device="cuda")
+    last, ld = dev(rnd(1, 4, heads, dim), "bf16")
+    x[-4:] = last
+    turns = ref.turns_of(dim)
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    hf.rotary(x, x, pos, torch.from_numpy(turns.view(np.int64)).cuda())
+    want, err = ref.rotary(ld[None], np.arange(tokens - 4, tokens)[None], turns)
+    close(x[-4:], want[0], err[0], "bf16")
+    assert bool((x[:2] == 0).all())
+
+
+def test_logits_past_2_31_elements():
+    _room(16)
+    vocab = 131072
+    batch = (1 << 31) // vocab + 3
+    x = torch.zeros(batch, vocab, dtype=torch.bfloat16, device="cuda")
+    x[-1, 70000], x[-2, 5] = 3.0, 1.0
+    hist = torch.full((batch, 2), 5, dtype=torch.int32, device="cuda")
+    pres = torch.full((batch,), 2.0, device="cuda")
+    tok = torch.empty(batch, dtype=torch.int32, device="cuda")
+    hf.logits_process(x, x, history=hist, presence=pres, token=tok)
+    assert tok[-3:].tolist() == [0, 0, 70000] and int(tok.sum()) == 70000
+    assert float(x[-2, 5]) == -1.0 and float(x[-1, 5]) == -2.0 and float(x[-1, 70000]) == 3.0
 
 
 # ---- together ----------------------------------------------------------------------------------------------
