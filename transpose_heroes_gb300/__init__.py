@@ -464,27 +464,14 @@ def _load_call():
         raise RuntimeError(f"_hlocall.so is not built ({CALL_PATH}); run transpose_heroes_gb300.build.build()")
     import importlib.util
 
-    import torch
+    import torch  # noqa: F401  (the extension uses its libraries)
 
     spec = importlib.util.spec_from_file_location("_hlocall", CALL_PATH)
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
-    get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-    get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: _stream(None))
-    m.setup(DeviceView, get_device, get_stream, torch.float32, torch.bfloat16, torch.int8, torch.float16, torch.int32,
-            torch.float8_e4m3fn)
+    m.setup(DeviceView, HloError)
     _call = m
     return m
-
-
-def _made(name, *args):
-    """Makes the extension's call `name` and raises its refusals as HloError."""
-    try:
-        status = getattr(_call or _load_call(), name)(*args)
-    except ValueError as e:
-        raise HloError(STATUS_INVALID_ARG, str(e)) from None
-    if status:
-        _check(status)
 
 
 def rms_norm(x, out, weight=None, residual=None, sum_out=None, rstd=None, eps=1e-6, weight_offset=0.0, dropout=None,
@@ -492,9 +479,11 @@ def rms_norm(x, out, weight=None, residual=None, sum_out=None, rstd=None, eps=1e
     """hlo_rms_norm: h = residual + drop(x) (to sum_out), out = h / rms(h) * (weight + weight_offset), out in
     x's type, f32, or 8 bits with `scales` (per row) or `out_q` (static). weight_dtype names the type of a
     weight given as a raw address."""
-    q = _QuantKeep(out_q) if out_q is not None else None
-    _made("rms_norm", x, out, weight, VIEW_DTYPES[weight_dtype], residual, sum_out, rstd, eps, weight_offset, dropout,
-          scales, None if q is None else q.q, None if stream is None else _stream(stream))
+    q = None if out_q is None else _QuantKeep(out_q)
+    call = _call or _load_call()
+    status = call.rms_norm(x, out, weight, VIEW_DTYPES[weight_dtype], residual, sum_out, rstd, eps, weight_offset, dropout, scales, None if q is None else q.q, None if stream is None else _stream(stream))
+    if status:
+        _check(status)
     return out
 
 
@@ -510,15 +499,20 @@ def rms_norm_backward(dy, h, rstd, dh, weight=None, dsum=None, dx=None, dropout=
     tensor, or a raw address with workspace_bytes."""
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _made("rms_norm_backward", dy, h, rstd, dh, weight, VIEW_DTYPES[weight_dtype], dsum, dx, dropout, dweight,
-          _ptr(workspace), workspace_bytes, weight_offset, None if stream is None else _stream(stream))
+    call = _call or _load_call()
+    status = call.rms_norm_backward(dy, h, rstd, dh, weight, VIEW_DTYPES[weight_dtype], dsum, dx, dropout, dweight, _ptr(workspace), workspace_bytes, weight_offset, None if stream is None else _stream(stream))
+    if status:
+        _check(status)
     return dh
 
 
 def dropout(x, out, params, residual=None, stream=None):
     """hlo_dropout: out = residual + drop(x) for params = Dropout(p, seed, offset). The backward pass is the
     same call on the gradient."""
-    _made("dropout", x, out, params, residual, None if stream is None else _stream(stream))
+    call = _call or _load_call()
+    status = call.dropout(x, out, params, residual, None if stream is None else _stream(stream))
+    if status:
+        _check(status)
     return out
 
 
@@ -539,8 +533,10 @@ def rotary(x, out, positions, turns, k=None, k_out=None, interleaved=False, scal
     """hlo_rotary: rotates the first 2 n_pairs elements of every head of x (and of k) by position * turns; the
     rest is copied. turns: rotary_turns() on the device (int64), or a raw address with n_pairs. inverse
     turns back: the backward pass."""
-    _made("rotary", x, out, positions, turns, n_pairs, k, k_out, interleaved, scale, inverse,
-          None if stream is None else _stream(stream))
+    call = _call or _load_call()
+    status = call.rotary(x, out, positions, turns, n_pairs, k, k_out, interleaved, scale, inverse, None if stream is None else _stream(stream))
+    if status:
+        _check(status)
     return out
 
 
@@ -549,6 +545,8 @@ def logits_process(logits, out=None, bias=None, history=None, lengths=None, prom
     """hlo_logits_process: bias, repetition / frequency / presence penalties for the tokens of each row's
     history, the grammar's bit mask, and the greedy token (lowest index on ties, -1 when nothing is left).
     A bias or mask of one dimension serves every row."""
-    _made("logits_process", logits, out, bias, history, lengths, prompt_lengths, repetition, frequency, presence, mask,
-          token, None if stream is None else _stream(stream))
+    call = _call or _load_call()
+    status = call.logits_process(logits, out, bias, history, lengths, prompt_lengths, repetition, frequency, presence, mask, token, None if stream is None else _stream(stream))
+    if status:
+        _check(status)
     return out if out is not None else token

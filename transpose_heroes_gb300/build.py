@@ -69,8 +69,10 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
                 sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, len(srcs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, len(srcs) + 1)) as ex:
+        call_obj = ex.submit(_compile_call, force)
         objs = list(ex.map(compile_one, srcs))
+        call_obj = call_obj.result()
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-ldl"]
@@ -78,22 +80,41 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-    build_call(force)
+    if force or _stale(CALL, [call_obj]):
+        _link_call(call_obj)
     return LIB
 
 
-def build_call(force: bool = False) -> str:
-    """The CPython extension that marshals the calls of small layers (csrc/call.cc), linked to the library."""
-    src = os.path.join(CSRC, "call.cc")
-    if force or _stale(CALL, [src, os.path.join(INCLUDE, "hlo_fusion.h")]):
-        tmp = CALL + f".tmp{os.getpid()}"
-        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-I", INCLUDE, "-I",
-               sysconfig.get_paths()["include"], src, "-o", tmp, "-L", LIBDIR, "-l:libhlofusion.so", "-Wl,-rpath,$ORIGIN"]
+def _compile_call(force: bool) -> str:
+    """The CPython extension that marshals the layer operators' calls (csrc/call.cc), against torch's headers."""
+    src, obj = os.path.join(CSRC, "call.cc"), os.path.join(BUILD, "call.o")
+    if force or _stale(obj, [src, os.path.join(INCLUDE, "hlo_fusion.h")]):
+        import torch
+
+        torch_include = os.path.join(os.path.dirname(torch.__file__), "include")
+        cuda_include = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+        includes = [INCLUDE, sysconfig.get_paths()["include"], torch_include,
+                    os.path.join(torch_include, "torch", "csrc", "api", "include"), cuda_include]
+        abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+               *(f"-isystem{d}" if d != INCLUDE else f"-I{d}" for d in includes), "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, CALL)
-    return CALL
+    return obj
+
+
+def _link_call(obj: str) -> None:
+    import torch
+
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALL + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", LIBDIR, "-l:libhlofusion.so", "-Wl,-rpath,$ORIGIN",
+           "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{torch_lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL)
 
 
 if __name__ == "__main__":

@@ -1,21 +1,27 @@
 // _hlocall: the marshalling of the layer entry points (hlo_rms_norm, hlo_rms_norm_backward, hlo_dropout, hlo_rotary,
 // hlo_logits_process) as a CPython extension. A serving step makes hundreds of these calls on a few
-// kilobytes each, where building the descriptors through ctypes costs more than the kernel (measured on the
-// GPU's host: 11 us a call, of which the launch is 3); here the tensors' attributes are read directly.
-// Every function takes its operands by position and returns the hlo_status; nothing is kept between calls.
+// kilobytes each, where building the descriptors in Python costs more than the kernel (measured on the
+// GPU's host for one token's norm: 11 us a call through ctypes, of which the launch is about 2); here the
+// tensors' own fields are read. Every function takes its operands by position and returns the hlo_status;
+// nothing is kept between calls.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cstdarg>
 #include <cstring>
+#include <exception>
 
 #include "hlo_fusion.h"
 
 namespace {
 
-PyObject *s_data_ptr, *s_shape, *s_stride, *s_dtype, *s_ptr, *s_addr;
-PyObject* g_dtypes[6];    // torch's element types by hlo_dtype, once registered
+PyObject *s_ptr, *s_addr;
 PyObject* g_view_type;    // DeviceView
-PyObject *g_get_device, *g_get_stream;
+PyObject* g_error;        // HloError
 
 // One argument: a tensor, a DeviceView or None.
 struct Operand {
@@ -25,51 +31,65 @@ struct Operand {
   const hlo_view* view() const { return given ? &v : nullptr; }
 };
 
+// Raises HloError(HLO_ERR_INVALID_ARG, message).
+bool refuse(const char* format, ...) {
+  va_list ap;
+  va_start(ap, format);
+  PyObject* text = PyUnicode_FromFormatV(format, ap);
+  va_end(ap);
+  PyObject* e = text ? PyObject_CallFunction(g_error, "iO", (int)HLO_ERR_INVALID_ARG, text) : nullptr;
+  if (e) PyErr_SetObject(g_error, e);
+  Py_XDECREF(e);
+  Py_XDECREF(text);
+  return false;
+}
+
 bool address(PyObject* o, void** p) {
   *p = PyLong_AsVoidPtr(o);
   return *p || !PyErr_Occurred();
 }
 
-bool fill(PyObject* seq, int64_t* to, Py_ssize_t* n) {  // torch.Size and stride() are tuples
-  if (!PyTuple_Check(seq)) {
-    PyErr_SetString(PyExc_TypeError, "a tensor or a DeviceView is wanted");
-    return false;
+int32_t type_of(at::ScalarType t) {
+  switch (t) {
+    case at::kFloat: return HLO_F32;
+    case at::kBFloat16: return HLO_BF16;
+    case at::kHalf: return HLO_F16;
+    case at::kChar: return HLO_S8;
+    case at::kInt: return HLO_S32;
+    case at::kFloat8_e4m3fn: return HLO_F8E4M3FN;
+    default: return -1;
   }
-  *n = PyTuple_GET_SIZE(seq);
-  for (Py_ssize_t i = 0; i < *n && i < HLO_MAX_RANK; ++i) {
-    to[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(seq, i));
-    if (to[i] == -1 && PyErr_Occurred()) return false;
-  }
-  return true;
 }
 
 bool read(PyObject* t, Operand* o) {
   if (t == Py_None) return true;
   o->given = true;
-  if ((PyObject*)Py_TYPE(t) == g_view_type) {
-    PyObject *a = PyObject_GetAttr(t, s_addr), *p = a ? PyObject_GetAttr(t, s_ptr) : nullptr;
-    void* view = nullptr;
-    const bool ok = a && p && address(a, &view) && address(p, &o->p);
-    if (ok) std::memcpy(&o->v, view, sizeof o->v);
-    Py_XDECREF(a);
-    Py_XDECREF(p);
-    return ok;
+  if (THPVariable_Check(t)) {
+    try {
+      const at::Tensor& x = THPVariable_Unpack(t);
+      const auto sizes = x.sizes(), strides = x.strides();
+      o->v.rank = (int32_t)x.dim();  // a rank that is too high is the library's to refuse
+      o->v.dtype = type_of(x.scalar_type());
+      for (int64_t d = 0; d < x.dim() && d < HLO_MAX_RANK; ++d) {
+        o->v.dims[d] = sizes[d];
+        o->v.strides[d] = strides[d];
+      }
+      o->p = x.data_ptr();
+      return true;
+    } catch (const std::exception& e) {  // a tensor without storage or strides
+      return refuse("%s", e.what());
+    }
   }
-  PyObject *p = PyObject_CallMethodNoArgs(t, s_data_ptr), *shape = nullptr, *stride = nullptr, *dtype = nullptr;
-  bool ok = p && address(p, &o->p) && (shape = PyObject_GetAttr(t, s_shape)) && (stride = PyObject_CallMethodNoArgs(t, s_stride)) &&
-            (dtype = PyObject_GetAttr(t, s_dtype));
-  Py_ssize_t rank = 0, strides = 0;
-  ok = ok && fill(shape, o->v.dims, &rank) && fill(stride, o->v.strides, &strides);
-  if (ok) {
-    o->v.rank = (int32_t)rank;  // a rank that is too high is the library's to refuse
-    o->v.dtype = -1;
-    for (int k = 0; k < 6; ++k)
-      if (g_dtypes[k] == dtype) o->v.dtype = k;
+  if ((PyObject*)Py_TYPE(t) != g_view_type) {
+    PyErr_SetString(PyExc_TypeError, "a tensor or a DeviceView is wanted");
+    return false;
   }
+  PyObject *a = PyObject_GetAttr(t, s_addr), *p = a ? PyObject_GetAttr(t, s_ptr) : nullptr;
+  void* view = nullptr;
+  const bool ok = a && p && address(a, &view) && address(p, &o->p);
+  if (ok) std::memcpy(&o->v, view, sizeof o->v);
+  Py_XDECREF(a);
   Py_XDECREF(p);
-  Py_XDECREF(shape);
-  Py_XDECREF(stride);
-  Py_XDECREF(dtype);
   return ok;
 }
 
@@ -88,8 +108,7 @@ bool read_vector(PyObject* t, int64_t* count, int32_t* dtype, const char* what, 
     n *= o.v.dims[d];
   }
   if ((!dense && n != 0) || (*count >= 0 && n != *count) || (*dtype >= 0 && o.v.dtype != *dtype)) {
-    PyErr_Format(PyExc_ValueError, "%s: a contiguous vector of %lld elements of the right type is wanted", what, (long long)*count);
-    return false;
+    return refuse("%s: a contiguous vector of %lld elements of the right type is wanted", what, (long long)*count);
   }
   *count = n;
   *dtype = o.v.dtype;
@@ -115,15 +134,16 @@ bool read_struct(PyObject* o, T** out) {
   return ok;
 }
 
-// A stream's handle, or None for the current stream of the current device.
+// A stream's handle, or None for torch's current stream.
 bool read_stream(PyObject* o, void** stream) {
   if (o != Py_None) return address(o, stream);
-  PyObject* dev = PyObject_CallNoArgs(g_get_device);
-  PyObject* s = dev ? PyObject_CallOneArg(g_get_stream, dev) : nullptr;
-  const bool ok = s && address(s, stream);
-  Py_XDECREF(dev);
-  Py_XDECREF(s);
-  return ok;
+  try {
+    *stream = c10::cuda::getCurrentCUDAStream().stream();
+    return true;
+  } catch (const std::exception& e) {  // no device
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return false;
+  }
 }
 
 bool count_is(Py_ssize_t n, Py_ssize_t want) {
@@ -213,7 +233,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void *turns, *stream;
   if (!read_vector(a[3], &pairs, &any, "turns", &turns) || !read_stream(a[10], &stream)) return nullptr;
   if (any >= 0) {
-    PyErr_SetString(PyExc_ValueError, "rotary turns: a contiguous vector of 64-bit words is wanted");
+    refuse("rotary turns: a contiguous vector of 64-bit words is wanted");
     return nullptr;
   }
   if (a[4] != Py_None) pairs = PyLong_AsLongLong(a[4]);
@@ -255,15 +275,13 @@ PyObject* logits_process(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           out.p, static_cast<int32_t*>(token), stream));
 }
 
-// view_type, get_device, get_stream, then torch's element types in the order of hlo_dtype
+// DeviceView and HloError
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count_is(n, 9)) return nullptr;
-  PyObject** const to[9] = {&g_view_type, &g_get_device, &g_get_stream, g_dtypes, g_dtypes + 1, g_dtypes + 2, g_dtypes + 3, g_dtypes + 4,
-                            g_dtypes + 5};
-  for (int k = 0; k < 9; ++k) {
-    Py_INCREF(a[k]);
-    Py_XSETREF(*to[k], a[k]);
-  }
+  if (!count_is(n, 2)) return nullptr;
+  Py_INCREF(a[0]);
+  Py_INCREF(a[1]);
+  Py_XSETREF(g_view_type, a[0]);
+  Py_XSETREF(g_error, a[1]);
   Py_RETURN_NONE;
 }
 
@@ -279,10 +297,6 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hlocall", nullptr, -1, methods, n
 }  // namespace
 
 PyMODINIT_FUNC PyInit__hlocall() {
-  s_data_ptr = PyUnicode_InternFromString("data_ptr");
-  s_shape = PyUnicode_InternFromString("shape");
-  s_stride = PyUnicode_InternFromString("stride");
-  s_dtype = PyUnicode_InternFromString("dtype");
   s_ptr = PyUnicode_InternFromString("ptr");
   s_addr = PyUnicode_InternFromString("addr");
   return PyModule_Create(&module);
