@@ -513,10 +513,10 @@ def test_logits_many_occurrences_of_one_token():
     check_logits(2, 100, "f32", m=40000)
 
 
-@pytest.mark.parametrize("m", [6144, 6145, 9000, 66000])
+@pytest.mark.parametrize("m", [6720, 6800, 9000, 16383, 16384, 66000])
 @pytest.mark.parametrize("batch,vocab", [(2, 40000), (3, 150001)])
 def test_logits_long_histories(batch, vocab, m):
-    """The longest history that is kept in a table, the shortest that is not, and one whose counts need 32 bits;
+    """Histories about as long as a table takes (with two blocks an SM and with one), and one whose counts need 32 bits;
     vocabularies of several slabs."""
     check_logits(batch, vocab, "bf16", m=m, bias="row", mask="rows")
 
@@ -524,8 +524,10 @@ def test_logits_long_histories(batch, vocab, m):
 def test_logits_of_a_full_table():
     """As many different tokens as entries, all of them in one row's slab."""
     g = np.random.default_rng(3)
-    hist = np.stack([g.permutation(9000)[:6144] for _ in range(4)]).astype(np.int32)
-    check_logits(4, 9000, "f32", m=6144, history=hist, token=True)
+    hist = np.stack([g.permutation(9000)[:6700] for _ in range(4)]).astype(np.int32)
+    check_logits(4, 9000, "f32", m=6700, history=hist, token=True)
+    hist = np.stack([g.permutation(700)[:600] for _ in range(400)]).astype(np.int32)
+    check_logits(400, 700, "bf16", m=600, history=hist, token=True)
 
 
 def test_logits_ties_go_to_the_lowest_token():

@@ -94,20 +94,23 @@ __device__ __forceinline__ float warp_max_of(float v) {
   return r;
 }
 
-// Dynamic shared memory for slabs of `slab` tokens: a bit for each that occurs; their counts, one for each token
-// of the slab (places = slab) or for each place of a table of keys; and the list of those that occur, with
-// their values.
+// Dynamic shared memory for slabs of `slab` tokens: their counts (`places` words of `width` bytes: one for each token
+// of the slab, or the places of a table); a bit for each that occurs; and the list of those, with their values.
 struct LogitsShared {
-  size_t bits, key, value, list, bytes;
-  __host__ __device__ LogitsShared(int slab, bool table, int places, int count_bytes, int64_t max_length) {
+  size_t bits, value, list, bytes;
+  __host__ __device__ LogitsShared(int slab, int places, int width, int count_bytes, int64_t max_length) {
     const size_t listed = (size_t)(slab < max_length ? slab : max_length);
-    bits = (size_t)places * count_bytes;
-    key = bits + slab / 8;
-    value = key + (table ? (size_t)places * 4 : 0);
+    bits = (size_t)places * width;
+    value = bits + slab / 8;
     list = value + listed * 4;
     bytes = list + listed * count_bytes;
   }
 };
+
+// A place of the table: 1 + the token's number in the slab, above a count. So slabs have at most 2^17 tokens, and
+// histories fewer than 2^14 entries.
+constexpr int kCountBits = 14;
+constexpr int kTableSlab = 1 << 17;
 
 // A cluster of blocks shares a row; its blocks take slabs of `batches` times blockDim.x U vectors in turn.
 // The penalties touch a few of a slab's tokens (those of the history), but nearly every warp would meet one
@@ -119,13 +122,16 @@ struct LogitsShared {
 //     for every token of the slab.
 //  2. a thread for each listed token works out its value, from the logit itself.
 //  3. stream the slab, with the listed tokens masked out; then store their values over it.
+// ALONE: an SM has one block, which has its registers for itself and nobody to hide its waits: parts 1 and 2 take
+// four tokens a thread at a time.
 // The slab's first logits are requested before all this. The blocks' best tokens are written to the first
 // block's shared memory, and only that block waits for them.
-template <int DT, int U, typename COUNT, bool TABLE>
-__global__ void __launch_bounds__(kThreads, 2)
-    logits_kernel(const __grid_constant__ LogitsPlan p, int cluster, int batches, int table_bits) {
+template <int DT, int U, typename COUNT, bool TABLE, bool ALONE>
+__global__ void __launch_bounds__(kThreads, ALONE ? 1 : 2)
+    logits_kernel(const __grid_constant__ LogitsPlan p, int cluster, int batches, int table) {
   constexpr int W = kVec<DT>, EB = 16 / W;
   constexpr int CB = sizeof(COUNT), CPW = 4 / CB;  // counts a 32-bit word
+  constexpr int Q = ALONE ? 4 : 1;
   extern __shared__ __align__(16) char shared[];
   __shared__ unsigned long long best_of[kThreads / 32], cluster_best[8];
   __shared__ int listed;
@@ -136,11 +142,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int rank = (int)(blockIdx.x - b * cluster), tid = threadIdx.x, threads = blockDim.x;
   const int vocab = (int)p.vocab, words = (vocab + 31) / 32;
   const int batch = threads * U * W, slab = batches * batch;
-  const int places = TABLE ? 1 << table_bits : slab;
-  const LogitsShared parts(slab, TABLE, places, CB, p.max_length);
+  const LogitsShared parts(slab, TABLE ? table : slab, TABLE ? 4 : CB, CB, p.max_length);
   uint32_t* const seen = reinterpret_cast<uint32_t*>(shared);
   uint32_t* const bits = reinterpret_cast<uint32_t*>(shared + parts.bits);
-  uint32_t* const key = reinterpret_cast<uint32_t*>(shared + parts.key);  // a token's number in the slab + 1, or 0
   float* const value = reinterpret_cast<float*>(shared + parts.value);
   COUNT* const list = reinterpret_cast<COUNT*>(shared + parts.list);
   const char* const x_row = reinterpret_cast<const char*>(p.x) + b * p.x_stride * EB;
@@ -199,25 +203,26 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int32_t* const h = p.history + b * p.history_stride;
       const uint32_t limit = (uint32_t)min(slab, vocab - s0);
       const int lane = tid & 31;
-#pragma unroll 2
-      for (int i0 = tid - lane; i0 < len; i0 += threads) {
-        const int i = i0 + lane;
-        const int token = i < len ? __ldg(h + i) : -1;
+      const auto count = [&](int token, int i) {  // one entry a lane; -1 where the history has ended
         const uint32_t at = (uint32_t)token - (uint32_t)s0;
         bool first = false;
         uint32_t place = at;
         if (at < limit && token >= 0) {  // not another slab's token, nor one outside the vocabulary
           const uint32_t m = 1u << (at & 31);
+          const uint32_t made = i >= prompt;
           if (TABLE) {
             atomicOr(&bits[at >> 5], m);
-            place = (at * 2654435761u) >> (32 - table_bits);
-            uint32_t found;  // the table has more places than the history has tokens, so one is free
-            while ((found = atomicCAS(&key[place], 0u, at + 1)) != 0 && found != at + 1) place = (place + 1) & (places - 1);
+            // the table has more places than the history has entries, so one is free
+            place = __umulhi(at * 2654435761u, (uint32_t)table);
+            uint32_t found;
+            while ((found = atomicCAS(&seen[place], 0u, (at + 1) << kCountBits | made)) != 0 && found >> kCountBits != at + 1)
+              place = place + 1 == (uint32_t)table ? 0 : place + 1;
             first = found == 0;
+            if (!first && made) atomicAdd(&seen[place], 1u);
           } else {
             first = !(atomicOr(&bits[at >> 5], m) & m);
+            if (made) atomicAdd(&seen[at / CPW], 1u << (8 * CB * (int)(at % CPW)));
           }
-          if (i >= prompt) atomicAdd(&seen[place / CPW], 1u << (8 * CB * (int)(place % CPW)));
         }
         const uint32_t firsts = __ballot_sync(0xffffffffu, first);
         if (firsts) {  // one place on the list for all of the warp's
@@ -226,6 +231,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           index = __shfl_sync(0xffffffffu, index, 0) + __popc(firsts & ((1u << lane) - 1));
           if (first) list[index] = (COUNT)place;
         }
+      };
+      for (int base = tid - lane; base < len; base += Q * threads) {
+        int tokens[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) tokens[q] = base + q * threads + lane < len ? __ldg(h + base + q * threads + lane) : -1;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) count(tokens[q], base + q * threads + lane);
       }
       __syncthreads();
       n = listed;
@@ -234,18 +246,33 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float freq = p.frequency ? p.frequency[b] : 0.0f, pres = p.presence ? p.presence[b] : 0.0f;
         float top_v = __int_as_float(0xFF800000);
         int top_i = -1;
-        for (int i = tid; i < n; i += threads) {
-          const int place = (int)list[i], c = s0 + (TABLE ? (int)key[place] - 1 : place);
-          COUNT* const count = reinterpret_cast<COUNT*>(seen) + place;
-          float l = load_plain(x_row, DT, c);
-          if (bias) l = __fadd_rn(l, __ldg(bias + c));
-          l = penalised(l, (float)*count, rep, freq, pres);
-          if (mask && !((__ldg(mask + (c >> 5)) >> (c & 31)) & 1u)) l = __int_as_float(0xFF800000);
-          value[i] = l;
-          *count = 0;
-          if (l > top_v || (l == top_v && c < top_i)) {
-            top_v = l;
-            top_i = c;
+        for (int base = tid; base < n; base += Q * threads) {
+          int place[Q], c[Q];
+          float l[Q], add[Q];
+          uint32_t open[Q];
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const int i = base + q * threads;
+            if (i >= n) continue;
+            place[q] = (int)list[i];
+            c[q] = s0 + (TABLE ? (int)(seen[place[q]] >> kCountBits) - 1 : place[q]);
+            l[q] = load_plain(x_row, DT, c[q]);
+            add[q] = bias ? __ldg(bias + c[q]) : 0.0f;
+            open[q] = mask ? __ldg(mask + (c[q] >> 5)) >> (c[q] & 31) : 1u;
+          }
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const int i = base + q * threads;
+            if (i >= n) continue;
+            const uint32_t times = TABLE ? seen[place[q]] & ((1u << kCountBits) - 1) : reinterpret_cast<const COUNT*>(seen)[place[q]];
+            if (bias) l[q] = __fadd_rn(l[q], add[q]);
+            float v = penalised(l[q], (float)times, rep, freq, pres);
+            if (!(open[q] & 1u)) v = __int_as_float(0xFF800000);
+            value[i] = v;
+            if (v > top_v || (v == top_v && c[q] < top_i)) {
+              top_v = v;
+              top_i = c[q];
+            }
           }
         }
         const unsigned long long found = top_i >= 0 ? choice_key(top_v, top_i) : 0;
@@ -350,10 +377,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (n > 0) {
       __syncthreads();  // the slab is stored
       for (int i = tid; i < n; i += threads) {
-        const int place = (int)list[i], at = TABLE ? (int)key[place] - 1 : place;
+        const int place = (int)list[i], at = TABLE ? (int)(seen[place] >> kCountBits) - 1 : place;
         if (p.out) store_from_f32(p.out, p.out_dt, out_off + s0 + at, value[i]);
         bits[at >> 5] = 0;
-        if (TABLE) key[place] = 0;
+        if (TABLE) seen[place] = 0;
+        else reinterpret_cast<COUNT*>(seen)[place] = 0;
       }
       if (tid == 0) listed = 0;
     }
@@ -382,9 +410,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (tid == 0) p.token[b] = best ? (int32_t)~(uint32_t)best : -1;
 }
 
-template <int DT, int U, typename COUNT, bool TABLE>
-cudaError_t run_logits(const LogitsPlan& p, int threads, int cluster, int batches, int table_bits, cudaStream_t s) {
-  const auto kernel = logits_kernel<DT, U, COUNT, TABLE>;
+template <int DT, int U, typename COUNT, bool TABLE, bool ALONE>
+cudaError_t run_logits(const LogitsPlan& p, int threads, int cluster, int batches, int table, cudaStream_t s) {
+  const auto kernel = logits_kernel<DT, U, COUNT, TABLE, ALONE>;
   const int slab = threads * U * kVec<DT> * batches;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -394,7 +422,7 @@ cudaError_t run_logits(const LogitsPlan& p, int threads, int cluster, int batche
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(p.batch * cluster));
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = p.history ? LogitsShared(slab, TABLE, TABLE ? 1 << table_bits : slab, sizeof(COUNT), p.max_length).bytes : 0;
+  cfg.dynamicSmemBytes = p.history ? LogitsShared(slab, TABLE ? table : slab, TABLE ? 4 : (int)sizeof(COUNT), sizeof(COUNT), p.max_length).bytes : 0;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
@@ -402,37 +430,45 @@ cudaError_t run_logits(const LogitsPlan& p, int threads, int cluster, int batche
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, kernel, p, cluster, batches, table_bits);
+  return cudaLaunchKernelEx(&cfg, kernel, p, cluster, batches, table);
 }
 
-template <int DT>
-cudaError_t run_logits_type(const LogitsPlan& p, cudaStream_t s) {
+template <int DT, bool ALONE>
+cudaError_t run_logits_blocks(const LogitsPlan& p, int threads, int cluster, cudaStream_t s) {
   constexpr int W = kVec<DT>;
   const int64_t vectors = p.vocab / W + 2;
-  const int threads = (int)std::min<int64_t>(kThreads, (vectors + 31) / 32 * 32);
-  // as many blocks a row as give every SM one and a half, but no more than the row has vectors for
-  int cluster = 1;
-  while (cluster < 8 && p.batch * cluster * 2 < 3 * device_sm_count() && cluster * threads < vectors) cluster *= 2;
   // four vectors a thread where a block has that many
   const int u = vectors >= (int64_t)3 * threads * cluster ? 4 : 1;
   const int64_t batch = (int64_t)threads * u * W, needed = (vectors * W + batch * cluster - 1) / (batch * cluster);
-  // A table where it leaves an SM two blocks; slabs of 131072 tokens then, as the work on a slab's history does not
-  // shrink with it: 256 rows of 131072 with up to 4096 entries each take 64 us, with counts for all of a
-  // slab's tokens (slabs of 64 KB of counts) 68 us
-  int table_bits = 6;
-  while ((int64_t)3 << table_bits < 4 * p.max_length && table_bits < 14) ++table_bits;
-  if (table_bits <= 13) {
-    const int batches = (int)std::max<int64_t>(1, std::min((1 << 17) / batch, needed));
-    if (u == 4) return run_logits<DT, 4, uint16_t, true>(p, threads, cluster, batches, table_bits, s);
-    return run_logits<DT, 1, uint16_t, true>(p, threads, cluster, batches, table_bits, s);
+  // A table, half full at most, where it leaves an SM its blocks; slabs of 131072 tokens then, as the work on a slab's
+  // history does not shrink with it. 256 rows of 131072 with 4096 entries each take 51 us, with 6500 101 us (the
+  // shared memory is then missing from the first-level cache); with counts for all of a slab's tokens (slabs of
+  // 64 KB of counts) 70 and 110 us
+  const int table = (int)std::min<int64_t>((2 * p.max_length + 7) / 4 * 4, 1 << 20);
+  const int table_batches = (int)std::max<int64_t>(1, std::min(kTableSlab / batch, needed));
+  const size_t room = (ALONE ? 220 : 110) * 1024;
+  if (p.max_length < (1 << kCountBits) && LogitsShared((int)(table_batches * batch), table, 4, 2, p.max_length).bytes <= room) {
+    if (u == 4) return run_logits<DT, 4, uint16_t, true, ALONE>(p, threads, cluster, table_batches, table, s);
+    return run_logits<DT, 1, uint16_t, true, ALONE>(p, threads, cluster, table_batches, table, s);
   }
   const bool narrow = p.max_length < (1 << 16);
   const int batches = (int)std::max<int64_t>(1, std::min(64 * 1024 / (batch * (narrow ? 2 : 4)), needed));
   if (u == 4)
-    return narrow ? run_logits<DT, 4, uint16_t, false>(p, threads, cluster, batches, 0, s)
-                  : run_logits<DT, 4, uint32_t, false>(p, threads, cluster, batches, 0, s);
-  return narrow ? run_logits<DT, 1, uint16_t, false>(p, threads, cluster, batches, 0, s)
-                : run_logits<DT, 1, uint32_t, false>(p, threads, cluster, batches, 0, s);
+    return narrow ? run_logits<DT, 4, uint16_t, false, ALONE>(p, threads, cluster, batches, 0, s)
+                  : run_logits<DT, 4, uint32_t, false, ALONE>(p, threads, cluster, batches, 0, s);
+  return narrow ? run_logits<DT, 1, uint16_t, false, ALONE>(p, threads, cluster, batches, 0, s)
+                : run_logits<DT, 1, uint32_t, false, ALONE>(p, threads, cluster, batches, 0, s);
+}
+
+template <int DT>
+cudaError_t run_logits_type(const LogitsPlan& p, cudaStream_t s) {
+  const int64_t vectors = p.vocab / kVec<DT> + 2;
+  const int threads = (int)std::min<int64_t>(kThreads, (vectors + 31) / 32 * 32);
+  // as many blocks a row as give every SM one and a half, but no more than the row has vectors for
+  int cluster = 1;
+  while (cluster < 8 && p.batch * cluster * 2 < 3 * device_sm_count() && cluster * threads < vectors) cluster *= 2;
+  if (p.batch * cluster <= device_sm_count()) return run_logits_blocks<DT, true>(p, threads, cluster, s);
+  return run_logits_blocks<DT, false>(p, threads, cluster, s);
 }
 
 cudaError_t launch_logits(const LogitsPlan& p, cudaStream_t s) {
