@@ -412,6 +412,31 @@ def test_rotary(batch, seq, heads, kv, dim, rot, interleaved, dtype):
     check_rotary(batch, seq, heads, kv, dim, rot, dtype, interleaved, shift=1)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("batch,seq,heads,kv,dim,rot", [(2, 2700, 32, 8, 128, 64), (1, 6001, 4, 1, 64, 64), (3, 6700, 2, 1, 16, 8), (1, 5000, 9, 3, 80, 48),
+                                                        (1, 2600, 1, 1, 256, 256)])
+def test_rotary_of_many_tokens(batch, seq, heads, kv, dim, rot, dtype):
+    """Tokens that stream through shared memory, and the same from heads that do not lie together."""
+    check_rotary(batch, seq, heads, kv, dim, rot, dtype, True, packed=True, heads_major=True, scale=0.75)
+    check_rotary(batch, seq, heads, kv, dim, rot, dtype, False, packed=True, in_place=True, start=7)
+
+
+def test_rotary_of_many_tokens_with_gaps():
+    """One array of strided tokens and, heads first, another whose heads do not lie together."""
+    x, xd = dev(rnd(1, 1, 7000, 4, 64), "bf16", 8)  # a pitch of 72 elements from head to head
+    turns, pos = ref.turns_of(64), np.arange(7000, dtype=np.int32)[None]
+    td, pd = torch.from_numpy(turns.view(np.int64)).cuda(), torch.from_numpy(pos).cuda()
+    out = Band((1, 7000, 4, 64), torch.bfloat16, 8)
+    hf.rotary(x, out.t, pd, td)
+    want, err = ref.rotary(xd, pos, turns)
+    out.check()
+    close(out.t, want, err, "bf16")
+    y = torch.empty(1, 4, 7000, 64, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    y.copy_(x)
+    hf.rotary(y, y, pd, td)
+    assert torch.equal(y, out.t)
+
+
 @pytest.mark.parametrize("start", [-5, 500000, 2 ** 31 - 100])
 def test_rotary_far_positions(start):
     check_rotary(1, 40, 2, 1, 64, 64, "f32", start=start, base=500000.0)

@@ -1,6 +1,7 @@
 // Rotary positions (hlo_rotary): each pair of a head turns by 2 pi frac(position * turns / 2^64).
 #include <algorithm>
 
+#include "async_copy.cuh"
 #include "vectors.cuh"
 
 namespace hlo {
@@ -187,6 +188,135 @@ cudaError_t run_rotary(const RotaryPlan& p, const RotaryTile& tile, cudaStream_t
   return cudaGetLastError();
 }
 
+// ---- many tokens whose heads lie together --------------------------------------------------------------------
+// Persistent blocks; thread 0 keeps a ring of `stages` groups of t.tokens tokens (their heads of x, then of y)
+// coming with one bulk copy a token and array, so the loads never wait for the cosines. A group's cosines go
+// to one of two tables in shared memory before its one barrier, behind which every thread has left the group
+// before, whose stage is refilled then. Threads share the heads as in rotary_kernel.
+constexpr int kMaxStages = 4;
+
+template <int DT, bool INTER>
+__global__ void __launch_bounds__(256, 2) rotary_stream_kernel(const __grid_constant__ RotaryPlan p, const RotaryTile t, int total_tokens,
+                                                               int total_heads, int stages) {
+  constexpr int V = kVec<DT>, EB = 16 / V;
+  extern __shared__ __align__(128) char ring[];
+  __shared__ __align__(8) uint64_t full[kMaxStages];
+  const int split = (int)p.a[0].heads, tid = threadIdx.x;
+  const int x_bytes = split * p.dim * EB, token_bytes = total_heads * p.dim * EB, stage_bytes = t.tokens * token_bytes;
+  float2* const tables = reinterpret_cast<float2*>(ring + (size_t)stages * stage_bytes);
+  const int groups = (total_tokens + t.tokens - 1) / t.tokens;
+  const int mine = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;  // groups of this block
+  const auto place = [&](int token, int a, bool out) {  // bytes from the array's start
+    const uint32_t bi = p.batch > 1 ? (uint32_t)token / (uint32_t)p.seq : 0, si = (uint32_t)token - bi * (uint32_t)p.seq;
+    const int64_t* const s = out ? p.a[a].out_stride : p.a[a].in_stride;
+    return (bi * s[0] + si * s[1]) * EB;
+  };
+  const auto request = [&](int i) {
+    const int s = i % stages, first = ((int)blockIdx.x + i * (int)gridDim.x) * t.tokens, n = min(t.tokens, total_tokens - first);
+    const uint32_t bar = smem_addr(&full[s]);
+    mbar_arrive_expect_tx(bar, n * token_bytes);
+    for (int k = 0; k < n; ++k) {
+      char* const to = ring + (size_t)s * stage_bytes + k * token_bytes;
+      bulk_load(to, reinterpret_cast<const char*>(p.a[0].in) + place(first + k, 0, false), x_bytes, bar);
+      if (p.arrays > 1) bulk_load(to + x_bytes, reinterpret_cast<const char*>(p.a[1].in) + place(first + k, 1, false), token_bytes - x_bytes, bar);
+    }
+  };
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(smem_addr(&full[s]), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (tid == 0)
+    for (int i = 0; i < min(stages, mine); ++i) request(i);
+  const int part = tid / t.items, k = tid - part * t.items;
+  const int tok = part / t.slots, slot = part - tok * t.slots;
+  const bool turn = k < t.turned;
+  const int ea = (turn ? (INTER ? 2 * k * V : k * V) : 2 * p.pairs + 2 * (k - t.turned) * V) * EB;
+  const int eb = turn ? (INTER ? ea + 16 : ea + p.pairs * EB) : (2 * (k - t.turned) + 1 < t.copied ? ea + 16 : -1);
+  for (int i = 0; i < mine; ++i) {
+    const int s = i % stages, first = ((int)blockIdx.x + i * (int)gridDim.x) * t.tokens, n = min(t.tokens, total_tokens - first);
+    float2* const cs = tables + (i & 1) * t.tokens * p.pairs;
+    for (int j = tid; j < n * p.pairs; j += 256) {
+      const int tk = j / p.pairs, pair = j - tk * p.pairs;
+      const uint32_t g = (uint32_t)(first + tk), bi = p.batch > 1 ? g / (uint32_t)p.seq : 0, si = g - bi * (uint32_t)p.seq;
+      cs[j] = cos_sin(p, p.pos[bi * p.pos_stride[0] + si * p.pos_stride[1]], __ldg(reinterpret_cast<const unsigned long long*>(p.turns) + pair));
+    }
+    const bool arrived = mbar_wait(smem_addr(&full[s]), (i / stages) & 1);
+    if (!__syncthreads_and(arrived)) {  // a copy did not come: give up, when the others have come or their waits run out
+      if (tid == 0) {
+        record_fault(kFaultCopyTimeout);
+        for (int j = i; j < min(i + stages - (i > 0 ? 1 : 0), mine); ++j) mbar_wait(smem_addr(&full[j % stages]), (j / stages) & 1);
+      }
+      __syncthreads();
+      return;
+    }
+    if (tid == 0 && i > 0 && i - 1 + stages < mine) request(i - 1 + stages);
+    if (tok >= n) continue;
+    float2 w[V];
+    if (turn) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[e] = cs[tok * p.pairs + k * V + e];
+    }
+    const char* const from = ring + (size_t)s * stage_bytes + tok * token_bytes;
+    char* const x_out = reinterpret_cast<char*>(p.a[0].out) + place(first + tok, 0, true);
+    char* const y_out = reinterpret_cast<char*>(p.a[1].out) + place(first + tok, 1, true);
+#pragma unroll 2
+    for (int head = slot; head < total_heads; head += t.slots) {
+      const char* const at = from + head * p.dim * EB;
+      char* const to = head < split ? x_out + head * p.a[0].out_stride[2] * EB : y_out + (head - split) * p.a[1].out_stride[2] * EB;
+      uint4 a = *reinterpret_cast<const uint4*>(at + ea), b = eb >= 0 ? *reinterpret_cast<const uint4*>(at + eb) : a;
+      if (turn) {
+        float u[V], v[V];
+        unpack<DT>(a, u);
+        unpack<DT>(b, v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float& x = !INTER ? u[e] : 2 * e < V ? u[2 * e] : v[2 * e - V];
+          float& y = !INTER ? v[e] : 2 * e < V ? u[2 * e + 1] : v[2 * e + 1 - V];
+          const float x0 = x, y0 = y;
+          x = x0 * w[e].x - y0 * w[e].y;
+          y = y0 * w[e].x + x0 * w[e].y;
+        }
+        a = pack<DT>(u);
+        b = pack<DT>(v);
+      }
+      *reinterpret_cast<uint4*>(to + ea) = a;
+      if (eb >= 0) *reinterpret_cast<uint4*>(to + eb) = b;
+    }
+  }
+}
+
+// The ring's shape, if these arrays can use it: heads that lie together, and enough tokens for several groups a
+// block. false otherwise.
+template <int DT>
+bool run_rotary_stream(const RotaryPlan& p, const RotaryTile& tile, cudaStream_t s, cudaError_t* result) {
+  constexpr int EB = 16 / kVec<DT>;
+  int64_t heads = 0;
+  for (int k = 0; k < p.arrays; ++k) {
+    if (p.a[k].heads > 1 && p.a[k].in_stride[2] != p.dim) return false;
+    heads += p.a[k].heads;
+  }
+  RotaryTile t = tile;
+  const int parts = 256 / t.items;
+  const int64_t tokens = p.batch * p.seq, token_bytes = heads * p.dim * EB;
+  t.slots = 1;
+  while (t.slots * 2 <= parts && heads > 8 * t.slots) t.slots *= 2;  // up to eight heads a thread
+  t.tokens = (int)std::min<int64_t>(parts / t.slots, std::max<int64_t>(1, 40 * 1024 / token_bytes));
+  if (t.tokens * token_bytes > 100 * 1024 || t.tokens * (int64_t)p.pairs > 4096) return false;
+  const size_t stage = t.tokens * token_bytes, tables = (size_t)2 * t.tokens * p.pairs * sizeof(float2);
+  // two blocks an SM
+  const int stages = (int)std::min<size_t>(kMaxStages, (108 * 1024 - tables) / stage);
+  const int64_t groups = (tokens + t.tokens - 1) / t.tokens, blocks = (int64_t)device_sm_count() * 2;
+  if (stages < 2 || groups < 4 * blocks) return false;
+  const size_t smem = stages * stage + tables;
+  const auto kernel = p.interleaved ? rotary_stream_kernel<DT, true> : rotary_stream_kernel<DT, false>;
+  *result = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 108 * 1024);
+  if (*result != cudaSuccess) return true;
+  kernel<<<(unsigned)blocks, 256, smem, s>>>(p, t, (int)tokens, (int)heads, stages);
+  *result = cudaGetLastError();
+  return true;
+}
+
 // Any alignment and size: a thread per pair, then per element that is copied.
 __global__ void __launch_bounds__(256) rotary_any_kernel(RotaryPlan p, RotaryArray a, int64_t total) {
   const int per = p.dim - p.pairs;
@@ -232,6 +362,8 @@ int access_width(const RotaryPlan& p) {
 template <int DT>
 cudaError_t run_rotary_type(const RotaryPlan& p, int v, const RotaryTile& t, cudaStream_t s) {
   const int64_t heads = p.a[0].heads + (p.arrays > 1 ? p.a[1].heads : 0);
+  cudaError_t result = cudaSuccess;
+  if (v == kVec<DT> && run_rotary_stream<DT>(p, t, s, &result)) return result;
   // several heads a thread once one each fills the device twice over
   const bool many = p.batch * p.seq * heads * t.items >= (int64_t)device_sm_count() * 8 * 1024;
 #define HLO_CASE(VV) \
