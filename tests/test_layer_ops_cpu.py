@@ -253,6 +253,16 @@ def test_logits_refusals(monkeypatch):
     accepted(lambda: run(out=V(B, [3, 70], "f32"), bias=V(E, [3, 70], "f32", [0, 1])), monkeypatch)
 
 
+def test_tensors_must_be_on_the_gpu():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(4, 8)
+    refused(lambda: hf.rms_norm(x, V(B, [4, 8], "f32"), stream=0), word="on the GPU")
+    refused(lambda: hf.rms_norm(V(A, [4, 8], "f32"), V(B, [4, 8], "f32"), weight=torch.ones(8), stream=0), word="on the GPU")
+    refused(lambda: hf.rms_norm(x.to_sparse(), V(B, [4, 8], "f32"), stream=0))
+    with pytest.raises(TypeError):
+        hf.rms_norm(3, V(B, [4, 8], "f32"), stream=0)
+
+
 def test_f8_is_no_type_of_the_other_entry_points():
     a = hf.make_array([4, 5], None, "f32")
     a.dtype = 5

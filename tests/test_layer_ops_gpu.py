@@ -258,7 +258,8 @@ def test_rms_norm_backward_in_place(in_place, n):
 
 
 @pytest.mark.parametrize("rows,n,dtype", [(640, 64, "f32"), (613, 512, "bf16"), (640, 1024, "f16"), (700, 4096, "bf16"), (611, 4104, "f32"),
-                                          (620, 8192, "bf16"), (610, 12000, "bf16"), (609, 16384, "f16"), (2000, 1001, "bf16")])
+                                          (620, 8192, "bf16"), (610, 12000, "bf16"), (609, 16384, "f16"), (609, 16381, "f16"),
+                                          (311, 9000, "f32"), (310, 16384, "f32"), (5, 16383, "f32"), (2000, 1001, "bf16")])
 def test_rms_norm_backward_of_many_rows(rows, n, dtype):
     """Rows that stream through shared memory: each number of vectors a thread, with and without dsum, weights of
     either type, and a pitch."""

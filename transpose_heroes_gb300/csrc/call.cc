@@ -67,6 +67,7 @@ bool read(PyObject* t, Operand* o) {
   if (THPVariable_Check(t)) {
     try {
       const at::Tensor& x = THPVariable_Unpack(t);
+      if (!x.is_cuda()) return refuse("a tensor on the GPU is wanted");
       const auto sizes = x.sizes(), strides = x.strides();
       o->v.rank = (int32_t)x.dim();  // a rank that is too high is the library's to refuse
       o->v.dtype = type_of(x.scalar_type());

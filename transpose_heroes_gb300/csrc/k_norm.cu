@@ -51,11 +51,11 @@ cudaError_t launch_norm(const NormPlan& p, cudaStream_t s) {
   const void* const ptr[4] = {p.x, p.res, p.sum, p.out};
   const int ebs[4] = {eb, eb, eb, view_dt_bytes(p.out_dt)};
   bool cut = false;
-  const int64_t vectors = (p.n + w - 1) / w + 1;
+  const int64_t vectors = (p.n + w - 1) / w;
   if (vectors <= 512 * 8 && p.rows <= INT32_MAX && vectors_fit<4>(p.map, ptr, ebs, p.n, w, &cut)) {
     // up to four vectors a thread, as long as a warp's lanes are all used. 2^26 bf16 elements with residual: 82 us
     // with four (1024 to 16384 columns), 85 to 93 with two, 105 to 144 with one
-    const RowShape r = row_shape(p.rows, vectors - 1, 8, 24);
+    const RowShape r = row_shape(p.rows, vectors, 8, 24);
     const int whole = p.w && (uintptr_t)p.w % 16 == 0;
     if (p.dt == F32) return run_norm_f32(p, r, cut, whole, s);
     if (p.dt == BF16) return run_norm_bf16(p, r, cut, whole, s);

@@ -408,6 +408,11 @@ cudaError_t run_norm_grad(const NormGradPlan& p, const RowShape& r, bool cut, in
   HLO_CASE(4, DROP_NONE);
   HLO_CASE(4, DROP_HOST);
   HLO_CASE(4, DROP_DEVICE);
+  if constexpr (DT == F32) {  // 32 sums a thread, as with four vectors of 16 bits
+    HLO_CASE(8, DROP_NONE);
+    HLO_CASE(8, DROP_HOST);
+    HLO_CASE(8, DROP_DEVICE);
+  }
 #undef HLO_CASE
   return cudaErrorInvalidValue;
 }
@@ -468,13 +473,14 @@ cudaError_t launch_norm_grad(const NormGradPlan& p, cudaStream_t s) {
   const void* const ptr[5] = {p.dy, p.h, p.dsum, p.dh, p.dx};
   const int ebs[5] = {eb, eb, eb, eb, eb};
   bool cut = false;
-  const int64_t vectors = (p.n + w - 1) / w + 1;
+  const int64_t vectors = (p.n + w - 1) / w;
+  const int max_k = p.dt == F32 ? 8 : 4;
   int64_t groups = norm_grad_partials(p.rows, p.n);
-  if (vectors <= 512 * 4 && vectors_fit<5>(p.map, ptr, ebs, p.n, w, &cut)) {
-    const RowShape r = row_shape(p.rows, vectors - 1, 4, 64);
+  if (vectors <= 512 * max_k && vectors_fit<5>(p.map, ptr, ebs, p.n, w, &cut)) {
+    const RowShape r = row_shape(p.rows, vectors, max_k, 64);
     const int whole = p.w && (uintptr_t)p.w % 16 == 0;
     // the ring pays once its blocks have several rows each
-    const RingShape ring = ring_shape(vectors - 1, p.dsum ? 3 : 2);
+    const RingShape ring = ring_shape(vectors, p.dsum ? 3 : 2);
     const bool stream = !cut && ring.stages > 0 && p.map.n <= 1 && p.rows >= 4 * device_sm_count();
     const cudaError_t e = stream ? (p.dt == F32    ? run_norm_grad_ring<F32>(p, ring, whole, &groups, s)
                                     : p.dt == BF16 ? run_norm_grad_ring<BF16>(p, ring, whole, &groups, s)

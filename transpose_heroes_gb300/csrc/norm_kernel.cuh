@@ -57,6 +57,21 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_row_kernel(const __g
     xr[k] = load16(reinterpret_cast<const char*>(p.x) + (off[0] + c0) * EB);
     if (p.res) rr[k] = load16(reinterpret_cast<const char*>(p.res) + (off[1] + c0) * EB);
   }
+  // one vector a thread is for few rows, where latency counts: the weights are requested with the row
+  const bool whole_w = weight_whole && cut.head == 0, early_w = K == 1 && whole_w && p.w && p.w_dt == DT;
+  uint4 wr = make_uint4(0, 0, 0, 0);
+  if (early_w && cut.head + (int)threadIdx.x * W < cut.end) wr = __ldg(reinterpret_cast<const uint4*>(p.w) + threadIdx.x);
+  const auto weights = [&](int c0, float (&w)[W]) {
+    if (K == 1 && early_w) {
+      unpack<DT>(wr, w);
+      if (p.w_offset != 0.0f) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) w[e] += p.w_offset;
+      }
+    } else {
+      load_weights<DT>(p.w, p.w_dt, p.w_offset, c0, n, whole_w, w);
+    }
+  };
   float ve = 0.0f;
   if (CUT && edge >= 0) {
     ve = load_plain(p.x, DT, off[0] + edge);
@@ -66,7 +81,6 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_row_kernel(const __g
     if (p.sum) store_from_f32(p.sum, DT, off[2] + edge, ve);
   }
   const Philox<DROP> g(p.drop);
-  const bool whole_w = weight_whole && cut.head == 0;
   float v[K][W], ss = ve * ve, top = 0.0f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -86,7 +100,7 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_row_kernel(const __g
     if (p.sum) *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.sum) + (off[2] + c0) * EB) = pack<DT>(v[k]);
     if (p.quant == NQ_ROW) {
       float w[W];
-      load_weights<DT>(p.w, p.w_dt, p.w_offset, c0, n, whole_w, w);
+      weights(c0, w);
 #pragma unroll
       for (int e = 0; e < W; ++e) top = ieee_max(top, fabsf(v[k][e] * w[e]));
     }
@@ -107,7 +121,7 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_row_kernel(const __g
     const int c0 = cut.head + (int)(threadIdx.x + k * blockDim.x) * W;
     if (c0 >= cut.end) continue;
     float w[W], y[W];
-    load_weights<DT>(p.w, p.w_dt, p.w_offset, c0, n, whole_w, w);
+    weights(c0, w);
 #pragma unroll
     for (int e = 0; e < W; ++e) y[e] = __fmul_rn(__fmul_rn(v[k][e], r), w[e]);
     store_row_vec<DT>(p, off[3] + c0, y, inv);
