@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(cons
 constexpr int kMaxStages = 8;
 
 template <int DT, int K, int DROP, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1) norm_grad_stream_kernel(const __grid_constant__ NormGradPlan p, int stages, int weight_whole) {
+__global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : K == 4 ? 2 : 3) norm_grad_stream_kernel(const __grid_constant__ NormGradPlan p, int stages, int weight_whole) {
   constexpr int W = kVec<DT>, EB = 16 / W, H = W / 2;
   extern __shared__ __align__(128) char ring[];
   __shared__ __align__(8) uint64_t full[kMaxStages];
@@ -419,8 +419,7 @@ cudaError_t run_norm_grad(const NormGradPlan& p, const RowShape& r, bool cut, in
 
 template <int DT, int K, int DROP>
 cudaError_t run_norm_grad_stream(const NormGradPlan& p, int threads, int stages, size_t smem, int whole, int64_t* groups, cudaStream_t s) {
-  const auto kernel = K == 1 || (K == 2 && threads <= 256) ? norm_grad_stream_kernel<DT, K, DROP, K == 4 ? 512 : 256>
-                                                       : norm_grad_stream_kernel<DT, K, DROP, K == 1 ? 256 : 512>;
+  const auto kernel = threads <= 256 ? norm_grad_stream_kernel<DT, K, DROP, 256> : norm_grad_stream_kernel<DT, K, DROP, K == 4 ? 512 : 256>;
   int per_sm = 1;
   const cudaError_t e = resident_blocks((const void*)kernel, threads, smem, &per_sm);
   if (e != cudaSuccess) return e;
@@ -438,7 +437,7 @@ struct RingShape {
 };
 RingShape ring_shape(int64_t vectors, int arrays) {
   RingShape r = {};
-  r.k = vectors > 1024 ? 4 : vectors > 128 ? 2 : 1;
+  r.k = vectors > 512 ? 4 : vectors > 128 ? 2 : 1;
   r.threads = (int)((vectors + r.k - 1) / r.k + 31) / 32 * 32;
   const size_t stage = (size_t)vectors * 16 * arrays;
   // 768 threads an SM: 8192 x 4096 bf16 takes 52 us, with 512 threads 58 us, with 256 85 us
