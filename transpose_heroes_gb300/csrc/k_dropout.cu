@@ -27,6 +27,9 @@ __global__ void __launch_bounds__(256) dropout_any_kernel(const __grid_constant_
 // Dense operands, aligned to 16 bytes (one row): persistent blocks whose threads take vectors in turn, two
 // vectors ahead of the one they work on. A loop that is not unrolled, so that the generator's ten rounds
 // are in flight for one vector at a time and registers leave room for many warps.
+// Bound: the wide multiplies (18 for the words of four elements; that pipe is 69% busy) beside HBM: 2^27 bf16
+// elements with residual (805 MB) 134 us, 6.0 TB/s, 89% of the copy rate. Four vectors a thread at once (94
+// registers, half the warps) took 170 us, two with spills 144.
 template <int DT, int MODE, bool RES>
 __global__ void __launch_bounds__(256, 4) dropout_flat_kernel(const __grid_constant__ DropoutPlan p) {
   constexpr int W = kVec<DT>;
