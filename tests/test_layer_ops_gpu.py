@@ -623,6 +623,58 @@ def test_calls_are_captured_into_a_graph():
     assert all(torch.equal(a, b) for a, b in zip(got, (y, h, dh, rs, dw, qo, tok)))
 
 
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_that_follow_closely_see_each_others_writes(graph):
+    """Each call reads or overwrites what the one before it wrote or reads; the device is waited for after every
+    call on one side and not at all on the other."""
+    rows, heads, dim = 512, 8, 128
+    n = heads * dim
+    x0, r0 = (torch.from_numpy(rnd(s, rows, n)).float().cuda() for s in (1, 2))
+    x, r = x0.clone(), r0.clone()
+    h, y, dh = (torch.empty_like(x) for _ in range(3))
+    rs, dw = torch.empty(rows, device="cuda"), torch.empty(n, device="cuda")
+    ws = torch.empty(hf.rms_norm_workspace_size(rows, n), dtype=torch.uint8, device="cuda")
+    pos, turns = torch.arange(rows, dtype=torch.int32, device="cuda"), torch.from_numpy(hf.rotary_turns(dim)).cuda()
+    hist = torch.arange(rows * 9, dtype=torch.int32, device="cuda").view(rows, 9) % n
+    half = torch.full((rows,), 0.5, device="cuda")
+    tok = torch.empty(rows, dtype=torch.int32, device="cuda")
+    outs = (x, r, h, y, dh, rs, dw, tok)
+
+    def calls(wait):
+        for step in range(5):
+            d = hf.Dropout(0.25, 7, 1000 * step)
+            hf.rms_norm(x, y, residual=r, sum_out=r, rstd=rs, dropout=d)
+            wait()
+            hf.rotary(y.view(rows, heads, dim), x.view(rows, heads, dim), pos, turns)
+            wait()
+            hf.dropout(x, h, d, residual=r)
+            wait()
+            hf.rms_norm(h, y, rstd=rs)
+            wait()
+            hf.rms_norm_backward(y, h, rs, dh, dweight=dw, workspace=ws)
+            wait()
+            hf.rms_norm(dh, x, weight=dw)
+            wait()
+            hf.logits_process(x, y, history=hist, presence=half, token=tok)
+            wait()
+            hf.dropout(y, x, d)
+            wait()
+
+    calls(torch.cuda.synchronize)
+    want = [t.clone() for t in outs]
+    run = lambda: calls(lambda: None)
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        run = g.replay
+    for _ in range(3):
+        x.copy_(x0)
+        r.copy_(r0)
+        run()
+        assert all(torch.equal(a, b) for a, b in zip(want, outs))
+
+
 # ---- offsets past 32 bits ------------------------------------------------------------------------------------
 def _room(gigabytes):
     torch.cuda.empty_cache()

@@ -28,11 +28,12 @@ __global__ void __launch_bounds__(256) dropout_any_kernel(const __grid_constant_
 // vectors ahead of the one they work on. A loop that is not unrolled, so that the generator's ten rounds
 // are in flight for one vector at a time and registers leave room for many warps.
 // Bound: the wide multiplies (18 for the words of four elements; that pipe is 69% busy) beside HBM: 2^27 bf16
-// elements with residual (805 MB) 134 us, 6.0 TB/s, 89% of the copy rate. Four vectors a thread at once (94
+// elements with residual (805 MB) 132 us, 6.1 TB/s, 90% of the copy rate. Four vectors a thread at once (94
 // registers, half the warps) took 170 us, two with spills 144.
 template <int DT, int MODE, bool RES>
 __global__ void __launch_bounds__(256, 4) dropout_flat_kernel(const __grid_constant__ DropoutPlan p) {
   constexpr int W = kVec<DT>;
+  follow();
   const Philox<MODE> g(p.drop);
   const uint4* const x = reinterpret_cast<const uint4*>(p.x);
   const uint4* const res = reinterpret_cast<const uint4*>(p.res);
@@ -77,6 +78,7 @@ __global__ void __launch_bounds__(256, 4) dropout_flat_kernel(const __grid_const
 template <int DT, int MODE, bool RES>
 __global__ void __launch_bounds__(256) dropout_row_kernel(const __grid_constant__ DropoutPlan p) {
   constexpr int W = kVec<DT>, EB = 16 / W;
+  follow();
   const Philox<MODE> g(p.drop);
   for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
     int64_t off[3];
@@ -103,16 +105,13 @@ cudaError_t run_dropout(const DropoutPlan& p, bool flat, cudaStream_t s) {
     const auto kernel = p.res ? dropout_flat_kernel<DT, MODE, true> : dropout_flat_kernel<DT, MODE, false>;
     const int64_t cap = (int64_t)device_sm_count() * kernel_blocks_per_sm((const void*)kernel, 256, 0);
     const int64_t blocks = std::max<int64_t>(1, std::min(cap, (p.n / W + 255) / 256));
-    kernel<<<(unsigned)blocks, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_after(kernel, dim3((unsigned)blocks), dim3(256), 0, s, 1, p);
   }
   const int64_t vectors = (p.n + W - 1) / W + 1;
   const int threads = (int)std::min<int64_t>(256, (vectors + 31) / 32 * 32);
   const unsigned rows = (unsigned)std::min<int64_t>(p.rows, 65535);
   const dim3 grid((unsigned)((vectors + threads - 1) / threads), rows);
-  if (p.res) dropout_row_kernel<DT, MODE, true><<<grid, threads, 0, s>>>(p);
-  else dropout_row_kernel<DT, MODE, false><<<grid, threads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(p.res ? dropout_row_kernel<DT, MODE, true> : dropout_row_kernel<DT, MODE, false>, grid, dim3(threads), 0, s, 1, p);
 }
 
 template <int MODE>

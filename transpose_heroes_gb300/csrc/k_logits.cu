@@ -127,7 +127,7 @@ constexpr int kTableSlab = 1 << 17;
 // Bound: for a batch, the scattered accesses of the listed tokens (a wavefront each) and the waits of parts 1
 // and 2, not HBM: 256 rows of 131072 bf16 with histories of up to 4096 entries, bias and mask (141 MB, most of it in the
 // second-level cache between calls) 56 us; without a history 29 us, 4.6 TB/s, without bias and mask as well 21 us.
-// One row of 32000 with 700 entries 6.3 us.
+// One row of 32000 with 700 entries 5.3 us.
 // The slab's first logits are requested before all this. The blocks' best tokens are written to the first
 // block's shared memory, and only that block waits for them.
 template <int DT, int U, typename COUNT, bool TABLE, bool ALONE>
@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 1 : 2)
   extern __shared__ __align__(16) char shared[];
   __shared__ unsigned long long best_of[kThreads / 32], cluster_best[8];
   __shared__ int listed;
+  follow();
   const bool meet = cluster > 1 && p.token;
   // the first of the cluster's two barriers: every block has started before one writes to another
   if (meet) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 1 : 2)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int c = c0 + u * threads * W;  // a multiple of W: its bits lie in one byte
-          allowed[u] = mask ? (uint32_t)__ldg(reinterpret_cast<const uint8_t*>(mask) + (c >> 3)) >> (c & 7) : 0xFFFFFFFFu;
+          allowed[u] = mask ? (uint32_t)load_kept(reinterpret_cast<const uint8_t*>(mask) + (c >> 3)) >> (c & 7) : 0xFFFFFFFFu;
         }
         return;
       }
@@ -194,8 +195,8 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 1 : 2)
         x[u] = load_cut<DT>(p.x, b * p.x_stride, c, vocab, p.x_end);
         if (mask) {
           const int w0 = c >> 5;  // -1 for the columns before the row
-          const uint32_t lo = w0 >= 0 ? __ldg(mask + w0) : 0;
-          const uint32_t hi = (c & 31) + W > 32 && w0 + 1 < words ? __ldg(mask + w0 + 1) : 0;
+          const uint32_t lo = w0 >= 0 ? load_kept(mask + w0) : 0;
+          const uint32_t hi = (c & 31) + W > 32 && w0 + 1 < words ? load_kept(mask + w0 + 1) : 0;
           allowed[u] = __funnelshift_r(lo, hi, c & 31);
         }
       }
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 1 : 2)
       for (int base = tid - lane; base < len; base += Q * threads) {
         int tokens[Q];
 #pragma unroll
-        for (int q = 0; q < Q; ++q) tokens[q] = base + q * threads + lane < len ? __ldg(h + base + q * threads + lane) : -1;
+        for (int q = 0; q < Q; ++q) tokens[q] = base + q * threads + lane < len ? load_kept(h + base + q * threads + lane) : -1;
 #pragma unroll
         for (int q = 0; q < Q; ++q) count(tokens[q], base + q * threads + lane);
       }
@@ -261,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 1 : 2)
             place[q] = (int)list[i];
             c[q] = s0 + (TABLE ? (int)(seen[place[q]] >> kCountBits) - 1 : place[q]);
             l[q] = load_plain(x_row, DT, c[q]);
-            add[q] = bias ? __ldg(bias + c[q]) : 0.0f;
-            open[q] = mask ? __ldg(mask + (c[q] >> 5)) >> (c[q] & 31) : 1u;
+            add[q] = bias ? load_kept(bias + c[q]) : 0.0f;
+            open[q] = mask ? load_kept(mask + (c[q] >> 5)) >> (c[q] & 31) : 1u;
           }
 #pragma unroll
           for (int q = 0; q < Q; ++q) {
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 1 : 2)
         const float* const bias_at = bias + base + tid * W;
         if (bias) {
 #pragma unroll
-          for (int q = 0; q < W / 4; ++q) w[q] = __ldg(reinterpret_cast<const float4*>(bias_at) + q);
+          for (int q = 0; q < W / 4; ++q) w[q] = load_kept(reinterpret_cast<const float4*>(bias_at) + q);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 1 : 2)
             }
             if (u + 1 < U) {
 #pragma unroll
-              for (int q = 0; q < W / 4; ++q) w[q] = __ldg(reinterpret_cast<const float4*>(bias_at + (u + 1) * threads * W) + q);
+              for (int q = 0; q < W / 4; ++q) w[q] = load_kept(reinterpret_cast<const float4*>(bias_at + (u + 1) * threads * W) + q);
             }
           }
           if (mask || n > 0) masked(v, allowed[u], place);
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, ALONE ? 1 : 2)
         if (bias) {
 #pragma unroll
           for (int e = 0; e < W; ++e)
-            if (c0 + e >= 0 && c0 + e < vocab) v[e] = __fadd_rn(v[e], __ldg(bias + c0 + e));
+            if (c0 + e >= 0 && c0 + e < vocab) v[e] = __fadd_rn(v[e], load_kept(bias + c0 + e));
         }
         masked(v, allowed[u], place);
         const bool full = c0 >= 0 && c0 + W <= vocab;
@@ -418,23 +419,12 @@ template <int DT, int U, typename COUNT, bool TABLE, bool ALONE>
 cudaError_t run_logits(const LogitsPlan& p, int threads, int cluster, int batches, int table, cudaStream_t s) {
   const auto kernel = logits_kernel<DT, U, COUNT, TABLE, ALONE>;
   const int slab = threads * U * kVec<DT> * batches;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)(p.batch * cluster));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = p.history ? LogitsShared(slab, TABLE ? table : slab, TABLE ? 4 : (int)sizeof(COUNT), sizeof(COUNT), p.max_length).bytes : 0;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
-  if (cfg.dynamicSmemBytes > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+  const size_t smem = p.history ? LogitsShared(slab, TABLE ? table : slab, TABLE ? 4 : (int)sizeof(COUNT), sizeof(COUNT), p.max_length).bytes : 0;
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, kernel, p, cluster, batches, table);
+  return launch_after(kernel, dim3((unsigned)(p.batch * cluster)), dim3(threads), smem, s, cluster, p, cluster, batches, table);
 }
 
 template <int DT, bool ALONE>

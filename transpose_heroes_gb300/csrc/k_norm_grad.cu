@@ -51,9 +51,6 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(const __grid
   }
 }
 
-// Lets the next kernel of the stream be set up while this one's last blocks finish.
-__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // ---- gradient, rows held in registers ------------------------------------------------------------------------
 // Row groups walk the rows with a stride of all groups, keep dy, h and dsum of a row in registers (packed)
 // across its one reduction, and add each row's share of dweight to sums of their own: in registers, where
@@ -72,6 +69,7 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(cons
   __shared__ float red[2][64];
   extern __shared__ float cut_shared[];
   const int n = (int)p.n, places = n + n / W + 1;
+  follow();
   const int64_t group = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool idle = group >= groups;
   const Philox<DROP> g(p.drop);
@@ -170,7 +168,6 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(cons
     }
   }
   if (!p.dw) return;
-  allow_next();
   if (CUT) {  // the block's groups in order, as one share
     __syncthreads();
     float* const out = p.ws + (int64_t)blockIdx.x * n;
@@ -207,6 +204,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : K == 4 ? 2 : 3) norm_g
   extern __shared__ __align__(128) char ring[];
   __shared__ __align__(8) uint64_t full[kMaxStages];
   __shared__ float red[2][16];
+  follow();
   const int n = (int)p.n, tid = threadIdx.x, warps = blockDim.x >> 5;
   const int row_bytes = n * EB, stage_bytes = row_bytes * (p.dsum ? 3 : 2);
   const int mine = (int)((p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);  // rows of this block
@@ -235,7 +233,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : K == 4 ? 2 : 3) norm_g
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c0 = (int)(tid + k * blockDim.x) * W;
-    wr[k] = packed && c0 < n ? __ldg(reinterpret_cast<const uint4*>(p.w) + c0 / W) : make_uint4(0, 0, 0, 0);
+    wr[k] = packed && c0 < n ? load_kept(reinterpret_cast<const uint4*>(p.w) + c0 / W) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int e = 0; e < H; ++e) acc[k][e] = make_float2(0.0f, 0.0f);
   }
@@ -319,7 +317,6 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : K == 4 ? 2 : 3) norm_g
     }
   }
   if (!p.dw) return;
-  allow_next();
   float* const out = p.ws + (int64_t)blockIdx.x * n;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -332,13 +329,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : K == 4 ? 2 : 3) norm_g
 }
 
 // dw[c] = sum of the groups' shares, in a fixed order: 32 columns a block, 32 threads a column (a thread a column took
-// 9 us for 500 shares of 4096 columns, this takes 5). It is launched before
-// the kernel that writes them has ended, and waits for that end.
+// 9 us for 500 shares of 4096 columns, this takes 5).
 __global__ void __launch_bounds__(1024) norm_grad_join_kernel(const float* ws, float* dw, int64_t n, int64_t groups) {
   __shared__ float part[32][33];
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float acc = 0.0f;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  follow();
   if (c < n) {
 #pragma unroll 4
     for (int64_t k = threadIdx.y; k < groups; k += 32) acc += __ldcg(ws + k * n + c);
@@ -395,9 +391,8 @@ cudaError_t run_norm_grad_row(const NormGradPlan& p, const RowShape& r, int whol
   const int64_t most = std::min(norm_grad_partials(p.rows, p.n), (int64_t)device_sm_count() * per_sm * r.ty);
   const int64_t rows_each = (p.rows + most - 1) / most, count = (p.rows + rows_each - 1) / rows_each;
   const int64_t blocks = (count + r.ty - 1) / r.ty;
-  kernel<<<(unsigned)blocks, dim3(r.tx, r.ty), smem, s>>>(p, whole, count);
   *groups = CUT ? blocks : count;
-  return cudaGetLastError();
+  return launch_after(kernel, dim3((unsigned)blocks), dim3(r.tx, r.ty), smem, s, 1, p, whole, count);
 }
 
 template <int DT>
@@ -432,8 +427,7 @@ cudaError_t run_norm_grad_stream(const NormGradPlan& p, int threads, int stages,
   const int64_t most = std::min(norm_grad_partials(p.rows, p.n), (int64_t)device_sm_count() * per_sm);
   const int64_t rows_each = (p.rows + most - 1) / most;
   *groups = (p.rows + rows_each - 1) / rows_each;
-  kernel<<<(unsigned)*groups, threads, smem, s>>>(p, stages, whole);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3((unsigned)*groups), dim3(threads), smem, s, 1, p, stages, whole);
 }
 
 // The ring's shape for rows of `vectors` vectors; 0 stages: the rows do not fit.
@@ -504,16 +498,7 @@ cudaError_t launch_norm_grad(const NormGradPlan& p, cudaStream_t s) {
     else norm_grad_any_kernel<DROP_DEVICE><<<any_grid(p.rows), kAnyThreads, 0, s>>>(p);
   }
   if (!p.dw) return cudaGetLastError();
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)((p.n + 31) / 32));
-  cfg.blockDim = dim3(32, 32);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_grad_join_kernel, (const float*)p.ws, p.dw, p.n, groups);
+  return launch_after(norm_grad_join_kernel, dim3((unsigned)((p.n + 31) / 32)), dim3(32, 32), 0, s, 1, (const float*)p.ws, p.dw, p.n, groups);
 }
 
 }  // namespace hlo

@@ -85,11 +85,12 @@ struct RotaryTile {
 // two halves of V pairs (half layout), V adjacent pairs (interleaved), or 2 V copied elements; a thread's
 // item and token stay, so the places of its elements and its cosines are found once for U heads. The
 // loads of the first U heads are issued before the cosines are computed. Bound: latency for a few tokens (32 tokens
-// of 32 + 8 heads: 4.2 us a call, the launch); HBM and the phases of a block for many (see below).
+// of 32 + 8 heads: 4.1 us a call, the launch); HBM and the phases of a block for many (see below).
 template <int DT, int V, int U, bool INTER>
 __global__ void __launch_bounds__(256, 3) rotary_kernel(const __grid_constant__ RotaryPlan p, const RotaryTile t, int total_tokens,
                                                      int total_heads) {
   extern __shared__ float2 cs[];
+  follow();
   const int token0 = blockIdx.x * t.tokens;
   const int tokens = min(t.tokens, total_tokens - token0);
   const int head_end = min(total_heads, (int)(blockIdx.y + 1) * t.heads);
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(256, 3) rotary_kernel(const __grid_constant__ 
       for (int i = threadIdx.x; i < tokens * p.pairs; i += 256) {
         const int tk = i / p.pairs, pair = i - tk * p.pairs;
         const uint32_t g = (uint32_t)(token0 + tk), bi = p.batch > 1 ? g / (uint32_t)p.seq : 0, si = g - bi * (uint32_t)p.seq;
-        cs[i] = cos_sin(p, p.pos[bi * p.pos_stride[0] + si * p.pos_stride[1]], __ldg(reinterpret_cast<const unsigned long long*>(p.turns) + pair));
+        cs[i] = cos_sin(p, p.pos[bi * p.pos_stride[0] + si * p.pos_stride[1]], load_kept(reinterpret_cast<const unsigned long long*>(p.turns) + pair));
       }
       __syncthreads();
       if (!busy) return;
@@ -184,9 +185,8 @@ cudaError_t run_rotary(const RotaryPlan& p, const RotaryTile& tile, cudaStream_t
   t.heads = std::min(heads, t.slots * U);
   const int gx = (tokens + t.tokens - 1) / t.tokens, gy = (heads + t.heads - 1) / t.heads;
   const size_t smem = (size_t)t.tokens * p.pairs * sizeof(float2);
-  if (p.interleaved) rotary_kernel<DT, V, U, true><<<dim3(gx, gy), 256, smem, s>>>(p, t, tokens, heads);
-  else rotary_kernel<DT, V, U, false><<<dim3(gx, gy), 256, smem, s>>>(p, t, tokens, heads);
-  return cudaGetLastError();
+  return launch_after(p.interleaved ? rotary_kernel<DT, V, U, true> : rotary_kernel<DT, V, U, false>, dim3(gx, gy), dim3(256), smem, s, 1, p, t,
+                      tokens, heads);
 }
 
 // ---- many tokens whose heads lie together --------------------------------------------------------------------
@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(256, 2) rotary_stream_kernel(const __grid_cons
   constexpr int V = kVec<DT>, EB = 16 / V;
   extern __shared__ __align__(128) char ring[];
   __shared__ __align__(8) uint64_t full[kMaxStages];
+  follow();
   const int split = (int)p.a[0].heads, tid = threadIdx.x;
   const int x_bytes = split * p.dim * EB, token_bytes = total_heads * p.dim * EB, stage_bytes = t.tokens * token_bytes;
   float2* const tables = reinterpret_cast<float2*>(ring + (size_t)stages * stage_bytes);
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(256, 2) rotary_stream_kernel(const __grid_cons
     for (int j = tid; j < n * p.pairs; j += 256) {
       const int tk = j / p.pairs, pair = j - tk * p.pairs;
       const uint32_t g = (uint32_t)(first + tk), bi = p.batch > 1 ? g / (uint32_t)p.seq : 0, si = g - bi * (uint32_t)p.seq;
-      cs[j] = cos_sin(p, p.pos[bi * p.pos_stride[0] + si * p.pos_stride[1]], __ldg(reinterpret_cast<const unsigned long long*>(p.turns) + pair));
+      cs[j] = cos_sin(p, p.pos[bi * p.pos_stride[0] + si * p.pos_stride[1]], load_kept(reinterpret_cast<const unsigned long long*>(p.turns) + pair));
     }
     const bool arrived = mbar_wait(smem_addr(&full[s]), (i / stages) & 1);
     if (!__syncthreads_and(arrived)) {  // a copy did not come: give up, when the others have come or their waits run out
@@ -315,8 +316,7 @@ bool run_rotary_stream(const RotaryPlan& p, const RotaryTile& tile, cudaStream_t
   const auto kernel = p.interleaved ? rotary_stream_kernel<DT, true> : rotary_stream_kernel<DT, false>;
   *result = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 108 * 1024);
   if (*result != cudaSuccess) return true;
-  kernel<<<(unsigned)blocks, 256, smem, s>>>(p, t, (int)tokens, (int)heads, stages);
-  *result = cudaGetLastError();
+  *result = launch_after(kernel, dim3((unsigned)blocks), dim3(256), smem, s, 1, p, t, (int)tokens, (int)heads, stages);
   return true;
 }
 

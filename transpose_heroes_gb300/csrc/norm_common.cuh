@@ -62,11 +62,11 @@ __device__ __forceinline__ void load_weights(const void* w, int dt, float offset
 #pragma unroll
     for (int e = 0; e < W; ++e) v[e] = 1.0f;
   } else if (whole && dt == DT) {
-    unpack<DT>(__ldg(reinterpret_cast<const uint4*>(w) + c0 / W), v);
+    unpack<DT>(load_kept(reinterpret_cast<const uint4*>(w) + c0 / W), v);
   } else if (whole) {
 #pragma unroll
     for (int q = 0; q < W / 4; ++q) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(w) + c0) + q);
+      const float4 f = load_kept(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(w) + c0) + q);
       v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
     }
   } else if (dt == DT && (uintptr_t)w % 16 == 0) {
@@ -75,10 +75,10 @@ __device__ __forceinline__ void load_weights(const void* w, int dt, float offset
     const int j = c0 / W, s = c0 - j * W, last = (n - 1) / W;
     const uint4* const at = reinterpret_cast<const uint4*>(w);
     const bool tail = n % W != 0;  // the last vector would end behind the weights
-    uint4 a = __ldg(at + j), b = a;
+    uint4 a = load_kept(at + j), b = a;
     if (s) {
       if (j + 1 == last && tail) b = load_cut<DT>(w, 0, (int64_t)(j + 1) * W, n, nullptr);
-      else b = __ldg(at + j + 1);
+      else b = load_kept(at + j + 1);
     }
     uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     if ((s / EW) & 2) {

@@ -38,15 +38,16 @@ __device__ __forceinline__ void store_row_vec(const NormPlan& p, int64_t at, con
 // 16-byte boundary, the same column in every operand, and the up to 2 W - 2 elements before and behind them
 // go to a thread each.
 // Bound: HBM. A row is read and written once, so the time is that of its bytes: 16384 x 8192 bf16 with
-// residual (1074 MB) 159 us, 6.75 TB/s, the rate of a plain copy; cut rows, 32768 x 1001 bf16, 53 us (5.0 TB/s:
+// residual (1074 MB) 157 us, 6.84 TB/s, the rate of a plain copy; cut rows, 32768 x 1001 bf16, 53 us (5.0 TB/s:
 // the weights are shifted into place, and the ends are accesses of their own). With dropout the generator adds five
-// wide multiplies an element: 8192 x 4096 (268 MB) 52 us, 5.2 TB/s, the issue slots and the multiplier each
-// half busy. One token of 8192: 4.1 us a call, which is the launch.
+// wide multiplies an element: 8192 x 4096 (268 MB) 50 us, 5.4 TB/s, the issue slots and the multiplier each
+// half busy. One token of 8192: 3.3 us a call, which is the launch.
 template <int DT, int K, int DROP, bool CUT>
 __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_row_kernel(const __grid_constant__ NormPlan p, int weight_whole) {
   constexpr int W = kVec<DT>, EB = 16 / W;
   __shared__ float red[64];
   const int n = (int)p.n;
+  follow();
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= p.rows) return;  // the whole group: its barrier is its own
   int64_t off[4];
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_row_kernel(const __g
   // one vector a thread is for few rows, where latency counts: the weights are requested with the row
   const bool whole_w = weight_whole && cut.head == 0, early_w = K == 1 && whole_w && p.w && p.w_dt == DT;
   uint4 wr = make_uint4(0, 0, 0, 0);
-  if (early_w && cut.head + (int)threadIdx.x * W < cut.end) wr = __ldg(reinterpret_cast<const uint4*>(p.w) + threadIdx.x);
+  if (early_w && cut.head + (int)threadIdx.x * W < cut.end) wr = load_kept(reinterpret_cast<const uint4*>(p.w) + threadIdx.x);
   const auto weights = [&](int c0, float (&w)[W]) {
     if (K == 1 && early_w) {
       unpack<DT>(wr, w);
@@ -138,9 +139,7 @@ template <int DT, int K, int DROP>
 cudaError_t run_norm_row(const NormPlan& p, const RowShape& r, bool cut, int whole, cudaStream_t s) {
   const dim3 block(r.tx, r.ty);
   const unsigned grid = (unsigned)((p.rows + r.ty - 1) / r.ty);
-  if (cut) norm_row_kernel<DT, K, DROP, true><<<grid, block, 0, s>>>(p, whole);
-  else norm_row_kernel<DT, K, DROP, false><<<grid, block, 0, s>>>(p, whole);
-  return cudaGetLastError();
+  return launch_after(cut ? norm_row_kernel<DT, K, DROP, true> : norm_row_kernel<DT, K, DROP, false>, grid, block, 0, s, 1, p, whole);
 }
 
 template <int DT>

@@ -33,8 +33,8 @@ struct Philox {
     if constexpr (MODE == DROP_DEVICE) {
       uint64_t seed = d.seed, offset = d.offset;
       if (d.state) {
-        seed = __ldg(reinterpret_cast<const unsigned long long*>(d.state));
-        offset += __ldg(reinterpret_cast<const unsigned long long*>(d.state) + 1);
+        seed = reinterpret_cast<const unsigned long long*>(d.state)[0];
+        offset += reinterpret_cast<const unsigned long long*>(d.state)[1];
       }
       k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32), o0 = (uint32_t)offset, o1 = (uint32_t)(offset >> 32);
     }

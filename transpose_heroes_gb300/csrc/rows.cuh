@@ -9,7 +9,41 @@
 
 namespace hlo {
 
-// Plain loads: an output may be the input, so the read-only path is not allowed.
+// Kernels of one stream that follow one another closely: a kernel launched by launch_after() may be set up, and its
+// blocks placed, while the one before it ends. Every block of it calls follow() first: it lets the next kernel
+// do the same, and waits until everything queued before this kernel has ended and its writes are seen. Back to
+// back, 256 rows' norms (5120 bf16 to 8 bits) take 4.0 us a call in place of 6.1, and the gradient of 2049 x 1001
+// f32 12.9 in place of 14.4.
+__device__ __forceinline__ void follow() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Plain loads, also of weights, tables and histories: the read-only path (__ldg) asks that nobody writes the data
+// while the kernel runs, and here the kernel before may still be writing them when this one is set up. An output
+// may also be the input.
+template <typename T>
+__device__ __forceinline__ T load_kept(const T* p) {
+  return *p;
+}
 __device__ __forceinline__ float load_plain(const void* p, int dt, int64_t i) {
   switch (dt) {
     case F32: return reinterpret_cast<const float*>(p)[i];
