@@ -59,10 +59,11 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(const __grid
 // its group's barrier of that row, so two rows never add to one at once. The groups' sums go to the
 // workspace, and norm_grad_join_kernel adds them in order.
 //
-// CUT rows are taken apart as in norm_row_kernel; their weights lie in shared memory too, in the same places.
+// CUT rows are taken apart as in norm_row_kernel; their weights lie in shared memory too, in the same places. (A column a thread, for
+// sums and weights in registers at any alignment, took 120 us in place of 79: one element an access.)
 // Bound: the loads wait for the row's reduction, so an SM has few bytes in flight; this form serves cut rows and
-// few rows. 2049 x 1001 f32 (33 MB, in the second-level cache) 14 us with dweight, 16384 x 1001 f32 (262 MB) 52 us,
-// 5.1 TB/s; 32768 x 1001 bf16 84 us, the column sums in shared memory costing as much as the row itself.
+// few rows. 2049 x 1001 f32 (33 MB, in the second-level cache) 12 us with dweight, 16384 x 1001 f32 (262 MB) 50 us,
+// 5.3 TB/s; 32768 x 1001 bf16 79 us, the column sums in shared memory costing as much as the row itself.
 template <int DT, int K, int DROP, bool CUT>
 __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(const __grid_constant__ NormGradPlan p, int weight_whole, int64_t groups) {
   constexpr int W = kVec<DT>, EB = 16 / W;
@@ -77,7 +78,13 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(cons
   float* const ws = cut_shared;
   float* const cols = cut_shared + (1 + (int)threadIdx.y) * places;
   if (CUT) {
-    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < n; c += blockDim.x * blockDim.y) ws[c + c / W] = weight_at(p.w, p.w_dt, p.w_offset, c);
+    const int t0 = threadIdx.y * blockDim.x + threadIdx.x, step = blockDim.x * blockDim.y;
+    if (p.w && p.w_dt == DT) {  // without the choices of weight_at the loads go out eight at a time: 333 x 8191 bf16 11 us in place of 16
+#pragma unroll 8
+      for (int c = t0; c < n; c += step) ws[c + c / W] = load_plain(p.w, DT, c) + p.w_offset;
+    } else {
+      for (int c = t0; c < n; c += step) ws[c + c / W] = weight_at(p.w, p.w_dt, p.w_offset, c);
+    }
     if (p.dw)
       for (int c = threadIdx.x; c < places; c += blockDim.x) cols[c] = 0.0f;
     __syncthreads();
@@ -329,15 +336,28 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : K == 4 ? 2 : 3) norm_g
 }
 
 // dw[c] = sum of the groups' shares, in a fixed order: 32 columns a block, 32 threads a column (a thread a column took
-// 9 us for 500 shares of 4096 columns, this takes 5).
+// 9 us for 500 shares of 4096 columns, this takes 5). Blocks of 8 or 16 columns, for more blocks, are no faster.
 __global__ void __launch_bounds__(1024) norm_grad_join_kernel(const float* ws, float* dw, int64_t n, int64_t groups) {
   __shared__ float part[32][33];
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float acc = 0.0f;
   follow();
   if (c < n) {
-#pragma unroll 4
-    for (int64_t k = threadIdx.y; k < groups; k += 32) acc += __ldcg(ws + k * n + c);
+    const float* at = ws + threadIdx.y * n + c;
+    const int64_t step = 32 * n;
+    int64_t k = threadIdx.y;
+    for (; k + 96 < groups; k += 128, at += 4 * step) {
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __ldcg(at + j * step);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc += v[j];
+    }
+    float v[3];  // the last ones go out together too
+#pragma unroll
+    for (int j = 0; j < 3; ++j) v[j] = k + 32 * j < groups ? __ldcg(at + j * step) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) acc += v[j];
   }
   part[threadIdx.y][threadIdx.x] = acc;
   __syncthreads();
