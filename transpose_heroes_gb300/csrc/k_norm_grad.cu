@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(cons
   __shared__ float red[2][64];
   extern __shared__ float cut_shared[];
   const int n = (int)p.n, places = n + n / W + 1;
-  follow();
+  wait_for_last();
   const int64_t group = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool idle = group >= groups;
   const Philox<DROP> g(p.drop);
@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(cons
       if constexpr (DROP != DROP_NONE) store_from_f32(p.dx, DT, off[4] + edge, drop1(p.drop, g, (uint64_t)(row * n + edge), de));
     }
   }
+  allow_next();
   if (!p.dw) return;
   if (CUT) {  // the block's groups in order, as one share
     __syncthreads();
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : K == 4 ? 2 : 3) norm_g
   extern __shared__ __align__(128) char ring[];
   __shared__ __align__(8) uint64_t full[kMaxStages];
   __shared__ float red[2][16];
-  follow();
+  wait_for_last();
   const int n = (int)p.n, tid = threadIdx.x, warps = blockDim.x >> 5;
   const int row_bytes = n * EB, stage_bytes = row_bytes * (p.dsum ? 3 : 2);
   const int mine = (int)((p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);  // rows of this block
@@ -323,6 +324,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : K == 4 ? 2 : 3) norm_g
       }
     }
   }
+  allow_next();
   if (!p.dw) return;
   float* const out = p.ws + (int64_t)blockIdx.x * n;
 #pragma unroll
@@ -337,15 +339,15 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : K == 4 ? 2 : 3) norm_g
 
 // dw[c] = sum of the groups' shares, in a fixed order: 32 columns a block, 32 threads a column (a thread a column took
 // 9 us for 500 shares of 4096 columns, this takes 5). Blocks of 8 or 16 columns, for more blocks, are no faster.
-__global__ void __launch_bounds__(1024) norm_grad_join_kernel(const float* ws, float* dw, int64_t n, int64_t groups) {
+__global__ void __launch_bounds__(1024) norm_grad_join_kernel(const float* ws, float* dw, int64_t n, int groups) {
   __shared__ float part[32][33];
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float acc = 0.0f;
   follow();
   if (c < n) {
-    const float* at = ws + threadIdx.y * n + c;
+    const float* at = ws + (int64_t)threadIdx.y * n + c;
     const int64_t step = 32 * n;
-    int64_t k = threadIdx.y;
+    int k = threadIdx.y;
     for (; k + 96 < groups; k += 128, at += 4 * step) {
       float v[4];
 #pragma unroll
@@ -518,7 +520,7 @@ cudaError_t launch_norm_grad(const NormGradPlan& p, cudaStream_t s) {
     else norm_grad_any_kernel<DROP_DEVICE><<<any_grid(p.rows), kAnyThreads, 0, s>>>(p);
   }
   if (!p.dw) return cudaGetLastError();
-  return launch_after(norm_grad_join_kernel, dim3((unsigned)((p.n + 31) / 32)), dim3(32, 32), 0, s, 1, (const float*)p.ws, p.dw, p.n, groups);
+  return launch_after(norm_grad_join_kernel, dim3((unsigned)((p.n + 31) / 32)), dim3(32, 32), 0, s, 1, (const float*)p.ws, p.dw, p.n, (int)groups);
 }
 
 }  // namespace hlo
