@@ -206,6 +206,39 @@ def test_rms_norm_special_rows(n, out):
         assert bool(y[0].isnan().all()) and bool(y[4:].isfinite().all())
 
 
+@pytest.mark.parametrize("out", ["s8", "f8"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,n", [(6, 40), (6, 1001), (400, 1000), (6, 4096), (6, 40001)])
+def test_rms_norm_8_bit_rows_are_the_definitions_quotients(rows, n, dtype, out):
+    """Exactly: scales[row] = max|y| / 127 or / 448 and codes y / scale, both one f32 division of the y that the same call
+    gives in f32. Rows of subnormal values (whose scale has no reciprocal in f32), of zeros between them, and rows
+    whose h * weight underflows or overflows where y does not."""
+    a = rnd(1, rows, n)
+    a[0] = 0
+    a[0, 1:4] = 1e-40, -5e-41, 1e-41
+    a[1] *= 1e-38
+    a[2] *= 1e-21
+    a[3] *= 1e18
+    x = torch.from_numpy(a).to(DT[dtype]).cuda()
+    top, odt = (127.0, torch.int8) if out == "s8" else (448.0, torch.float8_e4m3fn)
+    for wide, eps in ((1.0, 1e-6), (1e-21, 1e-44), (1e25, 0.0), (1e-35, 1e-6)):
+        w = torch.from_numpy(np.float32(wide * (1 + rnd(2, n, std=0.1)))).cuda()
+        y, q, scales = torch.empty(rows, n, device="cuda"), torch.empty(rows, n, dtype=odt, device="cuda"), torch.empty(rows, device="cuda")
+        hf.rms_norm(x, y, weight=w, eps=eps)
+        hf.rms_norm(x, q, weight=w, eps=eps, scales=scales)
+        yh, codes = y.cpu().numpy(), q.cpu()
+        with np.errstate(invalid="ignore", divide="ignore", over="ignore", under="ignore"):
+            want = np.abs(yh).max(1) / np.float32(top)  # NaN where the row has one
+            want[want == 0] = 1
+            t = torch.from_numpy(yh / want[:, None])
+        assert np.array_equal(scales.cpu().numpy(), want, equal_nan=True)
+        if out == "s8":
+            assert torch.equal(codes, t.nan_to_num(0.0).round().clamp(-128, 127).to(torch.int8))
+        else:
+            t = t.to(torch.float8_e4m3fn).float()
+            assert bool(((codes.float() == t) | (codes.float().isnan() & t.isnan())).all())
+
+
 # ---- gradient ----------------------------------------------------------------------------------------------
 def check_grad(rows, n, dtype, dsum=True, weight="x", p=0.0, pitch=0, shift=0, in_place=None, dweight=True, seed=0, w_offset=0.0):
     h, hd = dev(rnd(seed + 1, rows, n, std=2.0), dtype, pitch, shift)

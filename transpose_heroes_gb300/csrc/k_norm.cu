@@ -4,8 +4,8 @@
 //  norm_row_kernel -- rows of up to 32768 elements (16384 in f32) whose operands are aligned alike: the row
 //                     stays in registers, one read and one write of everything.
 //  norm_any_kernel -- any length and alignment: a block per row, threads take elements in turn, and the row
-//                     is read twice (the second time from L2). A thread reads and writes the same elements
-//                     in both passes, so outputs may replace inputs in place.
+//                     is read twice (three times for 8 bits with scales; from L2 but for the first time). A thread reads and writes the same elements
+//                     in every pass, so outputs may replace inputs in place.
 #include "norm_common.cuh"
 
 namespace hlo {
@@ -22,25 +22,28 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const __grid_cons
       if constexpr (DROP != DROP_NONE) v = drop1(p.drop, g, (uint64_t)(row * p.n + c), v);
       return p.res ? __fadd_rn(load_plain(p.res, p.dt, off[1] + c), v) : v;
     };
+    const auto y_at = [&](int64_t c, float h, float r) { return __fmul_rn(__fmul_rn(h, r), weight_at(p.w, p.w_dt, p.w_offset, c)); };
     float ss = 0.0f, top = 0.0f;
     for (int64_t c = threadIdx.x; c < p.n; c += kAnyThreads) {
       const float h = h_at(c);
       ss = fmaf(h, h, ss);
-      if (p.quant == NQ_ROW) top = ieee_max(top, fabsf(h * weight_at(p.w, p.w_dt, p.w_offset, c)));
     }
     block_sum_max(ss, top, red);
     const float r = rsqrtf(__fdiv_rn(ss, (float)p.n) + p.eps);
     if (threadIdx.x == 0 && p.rstd) p.rstd[row] = r;
-    float inv = 0.0f;
+    float scale = 0.0f;
     if (p.quant == NQ_ROW) {
-      const float s = row_scale(r * top, p.out_dt);
-      inv = __fdiv_rn(1.0f, s);
-      if (threadIdx.x == 0) p.scales[row] = s;
+      float none = 0.0f;
+      for (int64_t c = threadIdx.x; c < p.n; c += kAnyThreads) top = ieee_max(top, fabsf(y_at(c, h_at(c), r)));
+      __syncthreads();  // red is read
+      block_sum_max(none, top, red);
+      scale = row_scale(top, p.out_dt);
+      if (threadIdx.x == 0) p.scales[row] = scale;
     }
     for (int64_t c = threadIdx.x; c < p.n; c += kAnyThreads) {
       const float h = h_at(c);
       if (p.sum) store_from_f32(p.sum, p.dt, off[2] + c, h);
-      store_out(p, off[3] + c, __fmul_rn(__fmul_rn(h, r), weight_at(p.w, p.w_dt, p.w_offset, c)), inv);
+      store_out(p, off[3] + c, y_at(c, h, r), scale);
     }
     __syncthreads();  // red is used again by the next row
   }

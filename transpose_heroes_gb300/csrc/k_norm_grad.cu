@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(cons
       hr[k] = load16(reinterpret_cast<const char*>(p.h) + (off[1] + c0) * EB);
       if (p.dsum) sr[k] = load16(reinterpret_cast<const char*>(p.dsum) + (off[2] + c0) * EB);
     }
-    float dot = 0.0f, none = 0.0f, ye = 0.0f, he = 0.0f, de = 0.0f, we = 0.0f;
+    float dot = 0.0f, ye = 0.0f, he = 0.0f, de = 0.0f, we = 0.0f;
     if (CUT && edge >= 0) {
       ye = load_plain(p.dy, DT, off[0] + edge);
       he = load_plain(p.h, DT, off[1] + edge) * r;
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(cons
 #pragma unroll
       for (int e = 0; e < W; ++e) dot = fmaf(y[e] * w[e], h[e] * r, dot);
     }
-    group_sum_max<false>(dot, none, red[phase]);
+    group_sum(dot, red[phase]);
     if (CUT && blockDim.x == 32) __syncwarp();
     const float mean = __fdiv_rn(dot, (float)p.n);
 #pragma unroll

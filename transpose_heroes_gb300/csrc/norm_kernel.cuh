@@ -5,19 +5,26 @@
 
 namespace hlo {
 
+// W codes with the row's scale; inv = RN(1 / scale).
 template <int DT>
-__device__ __forceinline__ void store_row_vec(const NormPlan& p, int64_t at, const float (&y)[kVec<DT>], float inv) {
+__device__ __forceinline__ void store_row_codes(const NormPlan& p, int64_t at, const float (&y)[kVec<DT>], float scale, float inv) {
   constexpr int W = kVec<DT>;
-  if (p.quant != NQ_NONE) {
+  char* a = reinterpret_cast<char*>(p.out) + at;
+  const uint32_t u = codes(make_float4(y[0], y[1], y[2], y[3]), scale, inv, p.out_dt == F8);
+  if constexpr (W == 8)
+    *reinterpret_cast<uint2*>(a) = make_uint2(u, codes(make_float4(y[4], y[5], y[6], y[7]), scale, inv, p.out_dt == F8));
+  else
+    *reinterpret_cast<uint32_t*>(a) = u;
+}
+
+template <int DT>
+__device__ __forceinline__ void store_row_vec(const NormPlan& p, int64_t at, const float (&y)[kVec<DT>]) {
+  constexpr int W = kVec<DT>;
+  if (p.quant == NQ_STATIC) {
     uint32_t u[2] = {0, 0};
 #pragma unroll
-    for (int e = 0; e < W; ++e) {
-      uint8_t b;
-      if (p.quant == NQ_STATIC) b = (uint8_t)quant_code(y[e], p.q.scale, p.q.inv_scale, p.q.zp, p.q.smin, p.q.smax);
-      else if (p.out_dt == S8) b = (uint8_t)s8_code(y[e], inv);
-      else b = f8_bits(__fmul_rn(y[e], inv));
-      u[e >> 2] |= (uint32_t)b << (8 * (e & 3));
-    }
+    for (int e = 0; e < W; ++e)
+      u[e >> 2] |= (uint32_t)(uint8_t)quant_code(y[e], p.q.scale, p.q.inv_scale, p.q.zp, p.q.smin, p.q.smax) << (8 * (e & 3));
     char* a = reinterpret_cast<char*>(p.out) + at;
     if (W == 8) *reinterpret_cast<uint2*>(a) = make_uint2(u[0], u[1]);
     else *reinterpret_cast<uint32_t*>(a) = u[0];
@@ -38,14 +45,16 @@ __device__ __forceinline__ void store_row_vec(const NormPlan& p, int64_t at, con
 // 16-byte boundary, the same column in every operand, and the up to 2 W - 2 elements before and behind them
 // go to a thread each.
 // Bound: HBM. A row is read and written once, so the time is that of its bytes: 16384 x 8192 bf16 with
-// residual (1074 MB) 157 us, 6.84 TB/s, the rate of a plain copy; cut rows, 32768 x 1001 bf16, 53 us (5.0 TB/s:
-// the weights are shifted into place, and the ends are accesses of their own). With dropout the generator adds five
+// residual (1074 MB) 157 us, 6.84 TB/s, the rate of a plain copy, and 146 us to f8 with scales
+// (940 MB, 6.4 TB/s); cut rows, 32768 x 1001 bf16, 53 us (5.0 TB/s: the weights are shifted into place, and the ends are
+// accesses of their own). With dropout the generator adds five
 // wide multiplies an element: 8192 x 4096 (268 MB) 50 us, 5.4 TB/s, the issue slots and the multiplier each
 // half busy. One token of 8192: 3.3 us a call, which is the launch.
 template <int DT, int K, int DROP, bool CUT>
 __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_row_kernel(const __grid_constant__ NormPlan p, int weight_whole) {
   constexpr int W = kVec<DT>, EB = 16 / W;
   __shared__ float red[64];
+  __shared__ uint32_t tops[32];
   const int n = (int)p.n;
   follow();
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -87,7 +96,7 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_row_kernel(const __g
     if (p.sum) store_from_f32(p.sum, DT, off[2] + edge, ve);
   }
   const Philox<DROP> g(p.drop);
-  float v[K][W], ss = ve * ve, top = 0.0f;
+  float v[K][W], ss = ve * ve;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c0 = cut.head + (int)(threadIdx.x + k * blockDim.x) * W;
@@ -104,35 +113,47 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_row_kernel(const __g
     for (int e = 0; e < W; ++e) ss = fmaf(v[k][e], v[k][e], ss);
     if (c0 >= cut.end) continue;
     if (p.sum) *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.sum) + (off[2] + c0) * EB) = pack<DT>(v[k]);
-    if (p.quant == NQ_ROW) {
+  }
+  group_sum(ss, red);
+  const float r = rsqrtf(__fdiv_rn(ss, (float)p.n) + p.eps);
+  if (threadIdx.x == 0 && p.rstd) p.rstd[row] = r;
+  if (CUT && edge >= 0) ve = __fmul_rn(__fmul_rn(ve, r), weight_at(p.w, p.w_dt, p.w_offset, edge));
+  float scale = 0.0f;
+  if (p.quant == NQ_ROW) {  // v becomes y; the scale is that of the largest |y|, a second reduction
+    uint32_t top = magnitude(ve);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c0 = cut.head + (int)(threadIdx.x + k * blockDim.x) * W;
+      if (c0 >= cut.end) continue;
       float w[W];
       weights(c0, w);
 #pragma unroll
-      for (int e = 0; e < W; ++e) top = ieee_max(top, fabsf(v[k][e] * w[e]));
+      for (int e = 0; e < W; ++e) {
+        v[k][e] = __fmul_rn(__fmul_rn(v[k][e], r), w[e]);
+        top = max(top, magnitude(v[k][e]));
+      }
+    }
+    scale = row_scale(group_max(top, tops), p.out_dt);
+    const float inv = __fdiv_rn(1.0f, scale);
+    if (threadIdx.x == 0) p.scales[row] = scale;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c0 = cut.head + (int)(threadIdx.x + k * blockDim.x) * W;
+      if (c0 < cut.end) store_row_codes<DT>(p, off[3] + c0, v[k], scale, inv);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c0 = cut.head + (int)(threadIdx.x + k * blockDim.x) * W;
+      if (c0 >= cut.end) continue;
+      float w[W], y[W];
+      weights(c0, w);
+#pragma unroll
+      for (int e = 0; e < W; ++e) y[e] = __fmul_rn(__fmul_rn(v[k][e], r), w[e]);
+      store_row_vec<DT>(p, off[3] + c0, y);
     }
   }
-  const float we = CUT && edge >= 0 ? weight_at(p.w, p.w_dt, p.w_offset, edge) : 0.0f;
-  if (CUT && edge >= 0) top = ieee_max(top, fabsf(ve * we));
-  group_sum_max<true>(ss, top, red);
-  const float r = rsqrtf(__fdiv_rn(ss, (float)p.n) + p.eps);
-  if (threadIdx.x == 0 && p.rstd) p.rstd[row] = r;
-  float inv = 0.0f;
-  if (p.quant == NQ_ROW) {
-    const float s = row_scale(r * top, p.out_dt);
-    inv = __fdiv_rn(1.0f, s);
-    if (threadIdx.x == 0) p.scales[row] = s;
-  }
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int c0 = cut.head + (int)(threadIdx.x + k * blockDim.x) * W;
-    if (c0 >= cut.end) continue;
-    float w[W], y[W];
-    weights(c0, w);
-#pragma unroll
-    for (int e = 0; e < W; ++e) y[e] = __fmul_rn(__fmul_rn(v[k][e], r), w[e]);
-    store_row_vec<DT>(p, off[3] + c0, y, inv);
-  }
-  if (CUT && edge >= 0) store_out(p, off[3] + edge, __fmul_rn(__fmul_rn(ve, r), we), inv);
+  if (CUT && edge >= 0) store_out(p, off[3] + edge, ve, scale);
 }
 
 template <int DT, int K, int DROP>

@@ -84,20 +84,58 @@ __device__ __forceinline__ void block_sum_max(float& s, float& m, float* red) {
   m = warp_max(m);
 }
 
-__device__ __forceinline__ uint8_t f8_bits(float v) {
-  return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+// y / scale in 8 bits, by the definition's own division.
+__device__ __forceinline__ uint8_t f8_code(float y, float scale) {
+  return (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(y, scale), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ int8_t s8_code(float y, float scale) {
+  const int q = __float2int_rn(__fdiv_rn(y, scale));  // NaN -> 0
+  return (int8_t)max(-128, min(127, q));
 }
 
-// The scale of an 8-bit row whose largest magnitude is m.
+// The scale of an 8-bit row whose largest |y| is m.
 __device__ __forceinline__ float row_scale(float m, int out_dt) {
   const float s = __fdiv_rn(m, out_dt == S8 ? 127.0f : 448.0f);
   return s == 0.0f ? 1.0f : s;
 }
 
-// y / scale in 8 bits: the quotient is y * inv with inv = RN(1 / scale), within 1.5 f32 ulps of it.
-__device__ __forceinline__ int8_t s8_code(float y, float inv) {
-  const int q = __float2int_rn(__fmul_rn(y, inv));  // NaN -> 0
-  return (int8_t)max(-128, min(127, q));
+// Four of them, y[i] in byte i.
+static __device__ __noinline__ uint32_t codes_divided(float4 y, float scale, int f8) {
+  const float v[4] = {y.x, y.y, y.z, y.w};
+  uint32_t u = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u |= (uint32_t)(f8 ? f8_code(v[i], scale) : (uint8_t)s8_code(v[i], scale)) << (8 * i);
+  return u;
+}
+
+// The same without divisions. With inv = RN(1 / scale) finite and not 0, q = y inv is within 2^-23 relative of y / scale
+// and the f32 quotient within 2^-24; so the quotient lies between q (1 - 2^-21) and q (1 + 2^-21), and where both ends
+// round to one code, so does it. Where one of the four does not, or the scale is a NaN, infinite or below 2^-128, they
+// are divided. 16384 x 8192 bf16 to f8 with residual: 146 us, 172 where every element is divided.
+__device__ __forceinline__ uint32_t codes(float4 y, float scale, float inv, int f8) {
+  const float2 q0 = __fmul2_rn(make_float2(y.x, y.y), make_float2(inv, inv));
+  const float2 q1 = __fmul2_rn(make_float2(y.z, y.w), make_float2(inv, inv));
+  const float2 lo = make_float2(1.0f - 0x1p-21f, 1.0f - 0x1p-21f), hi = make_float2(1.0f + 0x1p-21f, 1.0f + 0x1p-21f);
+  uint32_t a, open;
+  if (f8) {
+    const auto both = [](float2 u, float2 v) {
+      return (uint32_t)__nv_cvt_float2_to_fp8x2(u, __NV_SATFINITE, __NV_E4M3) |
+             (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3) << 16;
+    };
+    a = both(__fmul2_rn(q0, lo), __fmul2_rn(q1, lo));
+    open = a ^ both(__fmul2_rn(q0, hi), __fmul2_rn(q1, hi));
+  } else {  // |q| < 127.5, and adding the magic number rounds to an integer, ties to even, into the low bits
+    const float2 m = make_float2(kMagic, kMagic);
+    const float2 a0 = __ffma2_rn(q0, lo, m), a1 = __ffma2_rn(q1, lo, m), b0 = __ffma2_rn(q0, hi, m), b1 = __ffma2_rn(q1, hi, m);
+    const auto bytes = [](float2 u, float2 v) {
+      return __byte_perm(__byte_perm(__float_as_uint(u.x), __float_as_uint(u.y), 0x0040),
+                         __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x0040), 0x5410);
+    };
+    a = bytes(a0, a1);
+    open = a ^ bytes(b0, b1);
+  }
+  if (open || !(inv > 0.0f && inv <= 3.4028235e38f)) a = codes_divided(y, scale, f8);
+  return a;
 }
 
 }  // namespace hlo
