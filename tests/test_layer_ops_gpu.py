@@ -605,6 +605,21 @@ def test_logits_of_an_empty_vocabulary():
     assert tok.tolist() == [-1, -1, -1]
 
 
+def test_an_error_is_reported_once():
+    """Whatever a call answers, the next one (a kernel whose launch is checked by CUDA's last error) answers for itself, and so does
+    torch."""
+    x = torch.zeros(1, 131072, dtype=torch.bfloat16, device="cuda")
+    try:
+        hf.logits_process(x, history=torch.zeros(1, 32768, dtype=torch.int32, device="cuda"),
+                          token=torch.empty(1, dtype=torch.int32, device="cuda"))
+    except hf.HloError:
+        pass
+    a = torch.ones(65, device="cuda")
+    hf.dropout(a[:64], a[1:].clone(), hf.Dropout(0.5, 1, 2))
+    hf.dropout(a[1:], torch.empty(64, device="cuda"), hf.Dropout(0.5, 1, 2))
+    torch.cuda.synchronize()
+
+
 # ---- streams -----------------------------------------------------------------------------------------------
 def test_calls_run_on_the_stream_they_are_given():
     """Work queued before on that stream is seen; nothing waits for the default stream."""

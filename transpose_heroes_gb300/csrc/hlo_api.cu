@@ -443,7 +443,10 @@ hlo_status api_fail(hlo_status s, const char* fmt, ...) {
   return s;
 }
 hlo_status api_ok() { return ok(); }
-hlo_status api_cuda_status(cudaError_t e, const char* what) { return cuda_status(e, what); }
+hlo_status api_cuda_status(cudaError_t e, const char* what) {
+  if (e != cudaSuccess) cudaGetLastError();  // reported here: not left for the next call's launch check
+  return cuda_status(e, what);
+}
 bool api_injected(const char* site) { return injected(site); }
 hlo_status api_check_quant(const hlo_quant* q, const hlo_array& a, const char* what, QuantParams* out) {
   return check_quant(q, a, what, out);
