@@ -580,6 +580,35 @@ def test_logits_long_histories(batch, vocab, m):
     check_logits(batch, vocab, "bf16", m=m, bias="row", mask="rows")
 
 
+@pytest.mark.parametrize("m", [27000, 28000, 32768, 50000, 65535])
+@pytest.mark.parametrize("batch,vocab,dtype", [(1, 131072, "bf16"), (1, 200003, "f16"), (64, 65536, "bf16"), (64, 128256, "f32"), (256, 32000, "bf16"),
+                                               (256, 50257, "bf16")])
+def test_logits_of_wide_history_buffers(batch, vocab, m, dtype):
+    """Buffers of 27000 to 65535 entries, whose lists are as large as the counts, over several batches of tokens a block: exact, by
+    counting with numpy."""
+    g = np.random.default_rng(m + vocab)
+    x, xd = dev(rnd(1, batch, vocab, std=3.0), dtype)
+    hist = (g.random((batch, m)) ** 3 * vocab).astype(np.int32)
+    lens = g.integers(0, m + 1, batch).astype(np.int32)
+    lens[0] = m
+    prompts = (lens // 2).astype(np.int32)
+    rep, fr, pr = (g.uniform(lo, hi, batch).astype(np.float32) for lo, hi in ((0.8, 1.5), (0.0, 0.5), (-0.2, 0.5)))
+    out, tok = torch.empty_like(x), torch.empty(batch, dtype=torch.int32, device="cuda")
+    c = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    hf.logits_process(x, out, history=c(hist), lengths=c(lens), prompt_lengths=c(prompts), repetition=c(rep), frequency=c(fr),
+                      presence=c(pr), token=tok)
+    want = xd.astype(np.float32)
+    for i in range(batch):
+        seen = np.bincount(hist[i, :lens[i]], minlength=vocab) > 0
+        count = np.bincount(hist[i, prompts[i]:lens[i]], minlength=vocab)
+        l = want[i]
+        l = np.where(seen, np.where(l > 0, l / rep[i], l * rep[i]), l)
+        l = np.where(seen, l - fr[i] * count.astype(np.float32), l)
+        want[i] = np.where(count > 0, l - pr[i], l)
+    assert torch.equal(out.cpu(), torch.from_numpy(want).to(DT[dtype]))
+    assert np.array_equal(tok.cpu().numpy(), want.argmax(1))
+
+
 def test_logits_of_a_full_table():
     """As many different tokens as entries, all of them in one row's slab."""
     g = np.random.default_rng(3)

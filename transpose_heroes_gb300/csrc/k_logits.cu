@@ -107,6 +107,9 @@ struct LogitsShared {
   }
 };
 
+// The dynamic shared memory that a block can have beside the kernel's own few hundred bytes (227 KB in all).
+constexpr size_t kMostShared = 226 * 1024;
+
 // A place of the table: 1 + the token's number in the slab, above a count. So slabs have at most 2^17 tokens, and
 // histories fewer than 2^14 entries.
 constexpr int kCountBits = 14;
@@ -446,7 +449,11 @@ cudaError_t run_logits_blocks(const LogitsPlan& p, int threads, int cluster, cud
     return run_logits<DT, 1, uint16_t, true, ALONE>(p, threads, cluster, table_batches, table, s);
   }
   const bool narrow = p.max_length < (1 << 16);
-  const int batches = (int)std::max<int64_t>(1, std::min(64 * 1024 / (batch * (narrow ? 2 : 4)), needed));
+  // as many tokens a slab as 64 KB of counts take, and as their list leaves room for: one batch always has (16384 tokens
+  // at most, which are 194 KB with counts of 32 bits)
+  int batches = (int)std::max<int64_t>(1, std::min(64 * 1024 / (batch * (narrow ? 2 : 4)), needed));
+  const auto bytes = [&](int n) { return LogitsShared((int)(n * batch), (int)(n * batch), narrow ? 2 : 4, narrow ? 2 : 4, p.max_length).bytes; };
+  while (batches > 1 && bytes(batches) > kMostShared) --batches;
   if (u == 4)
     return narrow ? run_logits<DT, 4, uint16_t, false, ALONE>(p, threads, cluster, batches, 0, s)
                   : run_logits<DT, 4, uint32_t, false, ALONE>(p, threads, cluster, batches, 0, s);
