@@ -609,6 +609,34 @@ def test_logits_of_wide_history_buffers(batch, vocab, m, dtype):
     assert np.array_equal(tok.cpu().numpy(), want.argmax(1))
 
 
+def test_logits_from_two_threads_with_histories_of_two_widths():
+    """Calls of one kernel that need different amounts of shared memory, from two host threads at once, each on a stream of
+    its own: none is refused, and the tokens are right."""
+    import threading
+
+    found = []
+
+    def calls(m):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            x = torch.zeros(4, 32000, dtype=torch.bfloat16, device="cuda")
+            x[:, 77], x[:, 9] = 2.0, 1.0
+            hist = torch.full((4, m), 77, dtype=torch.int32, device="cuda")
+            pres = torch.full((4,), 1.5, device="cuda")
+            tok = torch.zeros(4, dtype=torch.int32, device="cuda")
+            try:
+                for _ in range(5000):
+                    hf.logits_process(x, history=hist, presence=pres, token=tok)
+                found.append(tok.tolist())
+            except hf.HloError as e:
+                found.append(str(e))
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=calls, args=(m,)) for m in (8000, 16000)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert found == [[9] * 4] * 2
+
+
 def test_logits_of_a_full_table():
     """As many different tokens as entries, all of them in one row's slab."""
     g = np.random.default_rng(3)

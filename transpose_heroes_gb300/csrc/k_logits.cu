@@ -423,8 +423,8 @@ cudaError_t run_logits(const LogitsPlan& p, int threads, int cluster, int batche
   const auto kernel = logits_kernel<DT, U, COUNT, TABLE, ALONE>;
   const int slab = threads * U * kVec<DT> * batches;
   const size_t smem = p.history ? LogitsShared(slab, TABLE ? table : slab, TABLE ? 4 : (int)sizeof(COUNT), sizeof(COUNT), p.max_length).bytes : 0;
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 40 * 1024) {  // always to the most, never this call's: threads share the attribute, and a smaller call would lower it
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostShared);
     if (e != cudaSuccess) return e;
   }
   return launch_after(kernel, dim3((unsigned)(p.batch * cluster)), dim3(threads), smem, s, cluster, p, cluster, batches, table);
