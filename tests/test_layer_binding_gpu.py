@@ -1,0 +1,57 @@
+"""What the Python binding of the layer operators refuses of tensors on the GPU. The injected fault answers in place of every
+launch, so nothing that should have been refused reaches the device."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import transpose_heroes_gb300 as hf
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from transpose_heroes_gb300 import build
+
+    build.build()
+    hf.lib()
+
+
+@pytest.fixture(autouse=True)
+def no_launch(monkeypatch):
+    monkeypatch.setenv("HLOFUSION_FAULT", "all")
+
+
+def refused(call, word=""):
+    with pytest.raises(hf.HloError) as e:
+        call()
+    assert e.value.status == 1 and word in str(e.value), str(e.value)
+
+
+def accepted(call):
+    with pytest.raises(hf.HloError) as e:
+        call()
+    assert e.value.status == 3 and "injected fault" in str(e.value), str(e.value)
+
+
+def zeros(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype, device="cuda")
+
+
+OTHER = [torch.float64, torch.int64, torch.uint8, torch.int16, torch.bool]
+
+
+@pytest.mark.parametrize("dtype", OTHER)
+def test_weights_of_another_type(dtype):
+    """Neither the input's type nor f32: never read as one of them."""
+    w = zeros(8, dtype=dtype)
+    x, y = zeros(4, 8), zeros(4, 8)
+    refused(lambda: hf.rms_norm(x, y, weight=w), "weight")
+    refused(lambda: hf.rms_norm(x, y, weight=w, weight_dtype="bf16"), "weight")
+    refused(lambda: hf.rms_norm_backward(x, y, zeros(4), zeros(4, 8), weight=w), "weight")
+    refused(lambda: hf.rms_norm(x, y, weight=zeros(8, dtype=torch.bfloat16)), "weight type")
+    accepted(lambda: hf.rms_norm(x, y, weight=zeros(8)))
+    accepted(lambda: hf.rms_norm(zeros(4, 8, dtype=torch.bfloat16), zeros(4, 8, dtype=torch.bfloat16), weight=zeros(8)))

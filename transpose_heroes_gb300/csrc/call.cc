@@ -95,8 +95,8 @@ bool read(PyObject* t, Operand* o) {
 }
 
 // A contiguous vector of `count` elements (count < 0: any number, stored), an address, or None. *dtype: the wanted type,
-// or -1 and then set.
-bool read_vector(PyObject* t, int64_t* count, int32_t* dtype, const char* what, void** p) {
+// or -1 and then set to that of the tensor, which has to be one of the library's.
+bool read_vector(PyObject* t, int64_t* count, int32_t* dtype, const char* what, void** p, bool other = false) {
   *p = nullptr;
   if (t == Py_None) return true;
   if (PyLong_Check(t)) return address(t, p);
@@ -111,6 +111,7 @@ bool read_vector(PyObject* t, int64_t* count, int32_t* dtype, const char* what, 
   if ((!dense && n != 0) || (*count >= 0 && n != *count) || (*dtype >= 0 && o.v.dtype != *dtype)) {
     return refuse("%s: a contiguous vector of %lld elements of the right type is wanted", what, (long long)*count);
   }
+  if (o.v.dtype < 0 && !other) return refuse("%s: element type not supported", what);
   *count = n;
   *dtype = o.v.dtype;
   *p = o.p;
@@ -232,7 +233,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int64_t pairs = -1;
   int32_t any = -1;
   void *turns, *stream;
-  if (!read_vector(a[3], &pairs, &any, "turns", &turns) || !read_stream(a[10], &stream)) return nullptr;
+  if (!read_vector(a[3], &pairs, &any, "turns", &turns, true) || !read_stream(a[10], &stream)) return nullptr;
   if (any >= 0) {
     refuse("rotary turns: a contiguous vector of 64-bit words is wanted");
     return nullptr;
