@@ -55,3 +55,13 @@ def test_weights_of_another_type(dtype):
     refused(lambda: hf.rms_norm(x, y, weight=zeros(8, dtype=torch.bfloat16)), "weight type")
     accepted(lambda: hf.rms_norm(x, y, weight=zeros(8)))
     accepted(lambda: hf.rms_norm(zeros(4, 8, dtype=torch.bfloat16), zeros(4, 8, dtype=torch.bfloat16), weight=zeros(8)))
+
+
+@pytest.mark.parametrize("dtype", [torch.float64, torch.float32, torch.int32, torch.uint8, torch.int16, torch.bool])
+def test_turns_of_another_type(dtype):
+    """Only 64-bit whole numbers are angles; narrower elements would be read past their end."""
+    q, pos = zeros(3, 2, 8), zeros(3, dtype=torch.int32)
+    refused(lambda: hf.rotary(q, q, pos, zeros(4, dtype=dtype)), "turns")
+    refused(lambda: hf.rotary(q, q, pos, zeros(4, dtype=dtype), n_pairs=4), "turns")
+    refused(lambda: hf.rotary(q, q, pos, zeros(8, dtype=torch.int64)[::2]), "turns")
+    accepted(lambda: hf.rotary(q, q, pos, zeros(4, dtype=torch.int64)))

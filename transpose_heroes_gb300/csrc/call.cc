@@ -28,6 +28,7 @@ struct Operand {
   hlo_view v;
   void* p = nullptr;
   bool given = false;
+  bool words = false;  // a tensor of 64-bit whole numbers, which no view of the library has
   const hlo_view* view() const { return given ? &v : nullptr; }
 };
 
@@ -71,6 +72,7 @@ bool read(PyObject* t, Operand* o) {
       const auto sizes = x.sizes(), strides = x.strides();
       o->v.rank = (int32_t)x.dim();  // a rank that is too high is the library's to refuse
       o->v.dtype = type_of(x.scalar_type());
+      o->words = x.scalar_type() == at::kLong || x.scalar_type() == at::kUInt64;
       for (int64_t d = 0; d < x.dim() && d < HLO_MAX_RANK; ++d) {
         o->v.dims[d] = sizes[d];
         o->v.strides[d] = strides[d];
@@ -95,8 +97,9 @@ bool read(PyObject* t, Operand* o) {
 }
 
 // A contiguous vector of `count` elements (count < 0: any number, stored), an address, or None. *dtype: the wanted type,
-// or -1 and then set to that of the tensor, which has to be one of the library's.
-bool read_vector(PyObject* t, int64_t* count, int32_t* dtype, const char* what, void** p, bool other = false) {
+// -1 and then set to that of the tensor, which has to be one of the library's, or kWords for 64-bit whole numbers.
+constexpr int32_t kWords = -2;
+bool read_vector(PyObject* t, int64_t* count, int32_t* dtype, const char* what, void** p) {
   *p = nullptr;
   if (t == Py_None) return true;
   if (PyLong_Check(t)) return address(t, p);
@@ -108,10 +111,11 @@ bool read_vector(PyObject* t, int64_t* count, int32_t* dtype, const char* what, 
     dense = o.v.dims[d] == 1 || o.v.strides[d] == n;
     n *= o.v.dims[d];
   }
-  if ((!dense && n != 0) || (*count >= 0 && n != *count) || (*dtype >= 0 && o.v.dtype != *dtype)) {
+  if ((!dense && n != 0) || (*count >= 0 && n != *count) || (*dtype >= 0 && o.v.dtype != *dtype) || (*dtype == kWords) != o.words) {
+    if (*count < 0) return refuse("%s: a contiguous vector of the right type is wanted", what);
     return refuse("%s: a contiguous vector of %lld elements of the right type is wanted", what, (long long)*count);
   }
-  if (o.v.dtype < 0 && !other) return refuse("%s: element type not supported", what);
+  if (o.v.dtype < 0 && !o.words) return refuse("%s: element type not supported", what);
   *count = n;
   *dtype = o.v.dtype;
   *p = o.p;
@@ -231,13 +235,9 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Operand x, out, pos, k, kout;
   if (!read(a[0], &x) || !read(a[1], &out) || !read(a[2], &pos) || !read(a[5], &k) || !read(a[6], &kout)) return nullptr;
   int64_t pairs = -1;
-  int32_t any = -1;
+  int32_t words = kWords;
   void *turns, *stream;
-  if (!read_vector(a[3], &pairs, &any, "turns", &turns, true) || !read_stream(a[10], &stream)) return nullptr;
-  if (any >= 0) {
-    refuse("rotary turns: a contiguous vector of 64-bit words is wanted");
-    return nullptr;
-  }
+  if (!read_vector(a[3], &pairs, &words, "turns", &turns) || !read_stream(a[10], &stream)) return nullptr;
   if (a[4] != Py_None) pairs = PyLong_AsLongLong(a[4]);
   const double scale = PyFloat_AsDouble(a[8]);
   const int inter = PyObject_IsTrue(a[7]), inverse = PyObject_IsTrue(a[9]);
