@@ -65,3 +65,14 @@ def test_turns_of_another_type(dtype):
     refused(lambda: hf.rotary(q, q, pos, zeros(4, dtype=dtype), n_pairs=4), "turns")
     refused(lambda: hf.rotary(q, q, pos, zeros(8, dtype=torch.int64)[::2]), "turns")
     accepted(lambda: hf.rotary(q, q, pos, zeros(4, dtype=torch.int64)))
+
+
+def test_more_pairs_than_turns():
+    q, pos, turns = zeros(3, 2, 8), zeros(3, dtype=torch.int32), zeros(2, dtype=torch.int64)
+    refused(lambda: hf.rotary(q, q, pos, turns, n_pairs=4), "turns has 2")
+    refused(lambda: hf.rotary(q, q, pos, turns, n_pairs=3), "turns has 2")
+    refused(lambda: hf.rotary(q, q, pos, turns, n_pairs=-(1 << 32)), "pairs")  # not 0 of them
+    refused(lambda: hf.rotary(q, q, pos, turns, n_pairs=-1), "pairs")
+    for n in (None, 2, 1):
+        accepted(lambda: hf.rotary(q, q, pos, turns, n_pairs=n))
+    accepted(lambda: hf.rotary(q, q, pos, zeros(4, dtype=torch.int64).data_ptr(), n_pairs=4))

@@ -229,7 +229,7 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
   CALL(hlo_dropout(x.view(), x.p, res.view(), res.p, drop, out.view(), out.p, stream));
 }
 
-// x, out, positions, turns, n_pairs (None: turns' count), k, k_out, interleaved, scale, inverse, stream
+// x, out, positions, turns, n_pairs (None: turns' count, the most that is taken), k, k_out, interleaved, scale, inverse, stream
 PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count_is(n, 11)) return nullptr;
   Operand x, out, pos, k, kout;
@@ -238,11 +238,20 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int32_t words = kWords;
   void *turns, *stream;
   if (!read_vector(a[3], &pairs, &words, "turns", &turns) || !read_stream(a[10], &stream)) return nullptr;
-  if (a[4] != Py_None) pairs = PyLong_AsLongLong(a[4]);
+  if (a[4] != Py_None) {
+    const int64_t wanted = PyLong_AsLongLong(a[4]);
+    if (PyErr_Occurred()) return nullptr;
+    if (pairs >= 0 && wanted > pairs) {  // an address has no count
+      refuse("rotary: %lld pairs, but turns has %lld", (long long)wanted, (long long)pairs);
+      return nullptr;
+    }
+    pairs = wanted;
+  }
   const double scale = PyFloat_AsDouble(a[8]);
   const int inter = PyObject_IsTrue(a[7]), inverse = PyObject_IsTrue(a[9]);
   if (PyErr_Occurred()) return nullptr;
   if (pairs > INT32_MAX) pairs = INT32_MAX;
+  if (pairs < -1) pairs = -1;  // refused
   CALL(hlo_rotary(x.view(), x.p, out.view(), out.p, k.view(), k.p, kout.view(), kout.p, pos.view(), static_cast<int32_t*>(pos.p),
                   static_cast<uint64_t*>(turns), (int32_t)pairs, inter, inverse, scale, stream));
 }
