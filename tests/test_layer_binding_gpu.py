@@ -76,3 +76,23 @@ def test_more_pairs_than_turns():
     for n in (None, 2, 1):
         accepted(lambda: hf.rotary(q, q, pos, turns, n_pairs=n))
     accepted(lambda: hf.rotary(q, q, pos, zeros(4, dtype=torch.int64).data_ptr(), n_pairs=4))
+
+
+def test_workspaces():
+    x, dh, rstd, dw = zeros(4, 8), zeros(4, 8), zeros(4), zeros(8)
+    n = hf.rms_norm_workspace_size(4, 8)
+    run = lambda ws, **kw: hf.rms_norm_backward(x, x, rstd, dh, dweight=dw, workspace=ws, **kw)  # noqa: E731
+    refused(lambda: run(torch.zeros(n, dtype=torch.uint8)), "on the GPU")
+    refused(lambda: run(zeros(1, dtype=torch.uint8).expand(n)), "contiguous")
+    refused(lambda: run(zeros(2 * n, dtype=torch.uint8)[::2]), "contiguous")
+    refused(lambda: run(zeros(8, dtype=torch.uint8), workspace_bytes=n), "the tensor has 8")
+    with pytest.raises(hf.HloError) as e:
+        run(zeros(n - 1, dtype=torch.uint8))
+    assert e.value.status == 4
+    with pytest.raises(TypeError):
+        run("scratch")
+    accepted(lambda: run(zeros(n, dtype=torch.uint8)))
+    accepted(lambda: run(zeros(n, dtype=torch.uint8), workspace_bytes=n))
+    accepted(lambda: run(zeros((n + 7) // 8, dtype=torch.float64)))
+    ws = zeros(n, dtype=torch.uint8)
+    accepted(lambda: run(ws.data_ptr(), workspace_bytes=n))

@@ -496,11 +496,9 @@ def rms_norm_backward(dy, h, rstd, dh, weight=None, dsum=None, dx=None, dropout=
                       weight_offset=0.0, weight_dtype="f32", workspace_bytes=None, stream=None):
     """hlo_rms_norm_backward: dh (the gradient of h), dx = drop(dh) with dropout, and dweight, from dy, the
     forward pass's sum h and rstd, and dsum (what reaches h by other ways). The workspace is a contiguous
-    tensor, or a raw address with workspace_bytes."""
-    if workspace_bytes is None:
-        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    tensor on the GPU, or a raw address with workspace_bytes."""
     call = _call or _load_call()
-    status = call.rms_norm_backward(dy, h, rstd, dh, weight, VIEW_DTYPES[weight_dtype], dsum, dx, dropout, dweight, _ptr(workspace), workspace_bytes, weight_offset, None if stream is None else _stream(stream))
+    status = call.rms_norm_backward(dy, h, rstd, dh, weight, VIEW_DTYPES[weight_dtype], dsum, dx, dropout, dweight, workspace, workspace_bytes, weight_offset, None if stream is None else _stream(stream))
     if status:
         _check(status)
     return dh

@@ -126,6 +126,30 @@ bool read_vector(PyObject* t, int64_t count, int32_t dtype, const char* what, vo
   return read_vector(t, &count, &dtype, what, p);
 }
 
+// Scratch memory: a contiguous tensor of any type, whose size counts (or fewer bytes of it), or an address with its size.
+bool read_scratch(PyObject* t, PyObject* size, void** p, size_t* bytes) {
+  *p = nullptr;
+  *bytes = 0;
+  if (size != Py_None) {
+    *bytes = PyLong_AsSize_t(size);
+    if (PyErr_Occurred()) return false;
+  }
+  if (t == Py_None) return true;
+  if (PyLong_Check(t)) return address(t, p);
+  if (!THPVariable_Check(t)) {
+    PyErr_SetString(PyExc_TypeError, "a tensor or an address is wanted");
+    return false;
+  }
+  Operand o;
+  if (!read(t, &o)) return false;
+  const at::Tensor& x = THPVariable_Unpack(t);
+  if (!x.is_contiguous()) return refuse("workspace: a contiguous tensor is wanted");
+  if (size != Py_None && *bytes > x.nbytes()) return refuse("workspace: %zu bytes, but the tensor has %zu", *bytes, (size_t)x.nbytes());
+  if (size == Py_None) *bytes = x.nbytes();
+  *p = o.p;
+  return true;
+}
+
 // The ctypes structure behind `o` (or NULL for None); its memory outlives the call, since the caller holds it.
 template <typename T>
 bool read_struct(PyObject* o, T** out) {
@@ -206,13 +230,13 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t width = cols;
   int32_t wdt = -1;
   void *w, *rstd, *dw, *ws, *stream;
+  size_t bytes;
   hlo_dropout_params* drop;
   if (!read_vector(a[4], &cols, &wdt, "weight", &w) || !read_vector(a[2], rows, HLO_F32, "rstd", &rstd) ||
-      !read_vector(a[9], width, HLO_F32, "dweight", &dw) || !read_struct(a[8], &drop) || !address(a[10], &ws) ||
+      !read_vector(a[9], width, HLO_F32, "dweight", &dw) || !read_struct(a[8], &drop) || !read_scratch(a[10], a[11], &ws, &bytes) ||
       !read_stream(a[13], &stream))
     return nullptr;
   if (wdt < 0) wdt = (int32_t)PyLong_AsLong(a[5]);
-  const size_t bytes = PyLong_AsSize_t(a[11]);
   const double off = PyFloat_AsDouble(a[12]);
   if (PyErr_Occurred()) return nullptr;
   CALL(hlo_rms_norm_backward(dy.view(), dy.p, h.view(), h.p, static_cast<float*>(rstd), w, wdt, off, ds.view(), ds.p, drop, dh.view(),
