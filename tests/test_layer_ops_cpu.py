@@ -263,6 +263,15 @@ def test_tensors_must_be_on_the_gpu():
         hf.rms_norm(3, V(B, [4, 8], "f32"), stream=0)
 
 
+def test_a_dropout_state_is_two_64_bit_words_on_the_gpu():
+    torch = pytest.importorskip("torch")
+    for state in (torch.zeros(2), torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int64), torch.zeros(3, dtype=torch.int64),
+                  torch.zeros(4, dtype=torch.int64)[::2]):
+        refused(lambda: hf.Dropout(0.5, 1, 2, state), word="64-bit")
+    refused(lambda: hf.Dropout(0.5, 1, 2, torch.zeros(2, dtype=torch.int64)), word="on the GPU")
+    assert hf.Dropout(0.5, 1, 2, S).state == S
+
+
 def test_f8_is_no_type_of_the_other_entry_points():
     a = hf.make_array([4, 5], None, "f32")
     a.dtype = 5

@@ -76,12 +76,17 @@ class View(ctypes.Structure):
 class Dropout(ctypes.Structure):
     """hlo_dropout_params: element i is dropped with probability p, by the counter-based generator's word
     for (seed, offset, i). `state` (a device tensor of two int64, or None) holds a seed that replaces
-    `seed` and an offset that `offset` is added to, read when the kernel runs."""
+    `seed` and an offset that `offset` is added to, read when the kernel runs; an address is taken as it is."""
 
     _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
                 ("state", ctypes.c_void_p)]
 
     def __init__(self, p: float, seed: int = 0, offset: int = 0, state=None):
+        if state is not None and not isinstance(state, int):
+            if str(state.dtype) not in ("torch.int64", "torch.uint64") or state.numel() != 2 or not state.is_contiguous():
+                raise HloError(STATUS_INVALID_ARG, "dropout: state must be two contiguous 64-bit whole numbers")
+            if not state.is_cuda:
+                raise HloError(STATUS_INVALID_ARG, "dropout: state must be a tensor on the GPU")
         super().__init__(p, seed, offset, _ptr(state))
         self.keep = state
 
