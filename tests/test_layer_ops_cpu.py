@@ -272,6 +272,16 @@ def test_a_dropout_state_is_two_64_bit_words_on_the_gpu():
     assert hf.Dropout(0.5, 1, 2, S).state == S
 
 
+def test_parameters_are_of_their_own_type():
+    """Not any buffer of the same size."""
+    x, y = V(A, [4, 8], "f32"), V(B, [4, 8], "f32")
+    for d in (np.zeros(4), bytes(32), 0.5, (ctypes.c_double * 4)()):
+        with pytest.raises(TypeError):
+            hf.dropout(x, y, d, stream=0)
+        with pytest.raises(TypeError):
+            hf.rms_norm(x, y, dropout=d, stream=0)
+
+
 def test_f8_is_no_type_of_the_other_entry_points():
     a = hf.make_array([4, 5], None, "f32")
     a.dtype = 5

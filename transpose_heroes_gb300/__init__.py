@@ -474,7 +474,7 @@ def _load_call():
     spec = importlib.util.spec_from_file_location("_hlocall", CALL_PATH)
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
-    m.setup(DeviceView, HloError)
+    m.setup(DeviceView, HloError, Dropout, Quant)
     _call = m
     return m
 

@@ -22,6 +22,8 @@ namespace {
 PyObject *s_ptr, *s_addr;
 PyObject* g_view_type;    // DeviceView
 PyObject* g_error;        // HloError
+PyObject* g_dropout_type; // Dropout
+PyObject* g_quant_type;   // Quant
 
 // One argument: a tensor, a DeviceView or None.
 struct Operand {
@@ -150,11 +152,16 @@ bool read_scratch(PyObject* t, PyObject* size, void** p, size_t* bytes) {
   return true;
 }
 
-// The ctypes structure behind `o` (or NULL for None); its memory outlives the call, since the caller holds it.
+// The ctypes structure of that type behind `o` (or NULL for None); its memory outlives the call, since the caller holds it.
 template <typename T>
-bool read_struct(PyObject* o, T** out) {
+bool read_struct(PyObject* o, PyObject* type, T** out) {
   *out = nullptr;
   if (o == Py_None) return true;
+  const int is = PyObject_IsInstance(o, type);
+  if (is <= 0) {
+    if (is == 0) PyErr_Format(PyExc_TypeError, "a %s is wanted", reinterpret_cast<PyTypeObject*>(type)->tp_name);
+    return false;
+  }
   Py_buffer b;
   if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE) != 0) return false;
   const bool ok = b.len == (Py_ssize_t)sizeof(T);
@@ -210,7 +217,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   hlo_dropout_params* drop;
   hlo_quant* q;
   if (!read_vector(a[2], &cols, &wdt, "weight", &w) || !read_vector(a[6], rows, HLO_F32, "rstd", &rstd) ||
-      !read_vector(a[10], rows, HLO_F32, "scales", &scales) || !read_struct(a[9], &drop) || !read_struct(a[11], &q) ||
+      !read_vector(a[10], rows, HLO_F32, "scales", &scales) || !read_struct(a[9], g_dropout_type, &drop) || !read_struct(a[11], g_quant_type, &q) ||
       !read_stream(a[12], &stream))
     return nullptr;
   if (wdt < 0) wdt = (int32_t)PyLong_AsLong(a[3]);
@@ -233,7 +240,7 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   size_t bytes;
   hlo_dropout_params* drop;
   if (!read_vector(a[4], &cols, &wdt, "weight", &w) || !read_vector(a[2], rows, HLO_F32, "rstd", &rstd) ||
-      !read_vector(a[9], width, HLO_F32, "dweight", &dw) || !read_struct(a[8], &drop) || !read_scratch(a[10], a[11], &ws, &bytes) ||
+      !read_vector(a[9], width, HLO_F32, "dweight", &dw) || !read_struct(a[8], g_dropout_type, &drop) || !read_scratch(a[10], a[11], &ws, &bytes) ||
       !read_stream(a[13], &stream))
     return nullptr;
   if (wdt < 0) wdt = (int32_t)PyLong_AsLong(a[5]);
@@ -249,7 +256,7 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Operand x, out, res;
   hlo_dropout_params* drop;
   void* stream;
-  if (!read(a[0], &x) || !read(a[1], &out) || !read(a[3], &res) || !read_struct(a[2], &drop) || !read_stream(a[4], &stream)) return nullptr;
+  if (!read(a[0], &x) || !read(a[1], &out) || !read(a[3], &res) || !read_struct(a[2], g_dropout_type, &drop) || !read_stream(a[4], &stream)) return nullptr;
   CALL(hlo_dropout(x.view(), x.p, res.view(), res.p, drop, out.view(), out.p, stream));
 }
 
@@ -310,13 +317,14 @@ PyObject* logits_process(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           out.p, static_cast<int32_t*>(token), stream));
 }
 
-// DeviceView and HloError
+// DeviceView, HloError, Dropout and Quant
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count_is(n, 2)) return nullptr;
-  Py_INCREF(a[0]);
-  Py_INCREF(a[1]);
+  if (!count_is(n, 4)) return nullptr;
+  for (int i = 0; i < 4; ++i) Py_INCREF(a[i]);
   Py_XSETREF(g_view_type, a[0]);
   Py_XSETREF(g_error, a[1]);
+  Py_XSETREF(g_dropout_type, a[2]);
+  Py_XSETREF(g_quant_type, a[3]);
   Py_RETURN_NONE;
 }
 
