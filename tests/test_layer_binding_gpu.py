@@ -96,3 +96,20 @@ def test_workspaces():
     accepted(lambda: run(zeros((n + 7) // 8, dtype=torch.float64)))
     ws = zeros(n, dtype=torch.uint8)
     accepted(lambda: run(ws.data_ptr(), workspace_bytes=n))
+
+
+def test_tensors_of_another_device():
+    """With one GPU in the machine, tensors without memory that say they are on the next one."""
+
+    class Elsewhere(torch.Tensor):
+        __torch_dispatch__ = classmethod(lambda cls, *a, **kw: NotImplemented)
+
+    other = f"cuda:{torch.cuda.current_device() + 1}"
+    x, w, scratch = (torch.Tensor._make_wrapper_subclass(Elsewhere, shape, dtype=t, device=other)
+                     for shape, t in (((4, 8), torch.float32), ((8,), torch.float32), ((1 << 20,), torch.uint8)))
+    a, b = zeros(4, 8), zeros(4, 8)
+    for call in (lambda: hf.rms_norm(x, b), lambda: hf.rms_norm(a, x), lambda: hf.rms_norm(a, b, weight=w),
+                 lambda: hf.dropout(a, b, hf.Dropout(0.5), residual=x), lambda: hf.logits_process(a, x),
+                 lambda: hf.rms_norm_backward(a, a, zeros(4), b, dweight=zeros(8), workspace=scratch)):
+        refused(call, f"on {other}")
+    accepted(lambda: hf.rms_norm(a, b))

@@ -435,7 +435,7 @@ def quant_fusion(inp, dims, in_q, out_m2m, out, out_dtype="s8", out_q=None, in_m
 # ---- the fusions between a decoder's matrix products ---------------------------------------------------------
 # Their operands are views: torch tensors (dims, strides and element type are the tensor's own) or
 # DeviceViews of raw device pointers. Vectors (a weight, scales, lengths, ...) are contiguous tensors, or
-# raw addresses. A serving step makes hundreds of these calls, so their arguments are marshalled by a
+# raw addresses. Tensors lie on the current device. A serving step makes hundreds of these calls, so their arguments are marshalled by a
 # CPython extension (csrc/call.cc) in place of ctypes.
 class DeviceView:
     """A view of device memory at `ptr` (an address or a tensor that carries the bits)."""

@@ -25,6 +25,8 @@ PyObject* g_error;        // HloError
 PyObject* g_dropout_type; // Dropout
 PyObject* g_quant_type;   // Quant
 
+int g_device;  // the current device once a call has read a tensor, -1 before; under the interpreter's lock, as all reading is
+
 // One argument: a tensor, a DeviceView or None.
 struct Operand {
   hlo_view v;
@@ -71,6 +73,9 @@ bool read(PyObject* t, Operand* o) {
     try {
       const at::Tensor& x = THPVariable_Unpack(t);
       if (!x.is_cuda()) return refuse("a tensor on the GPU is wanted");
+      if (g_device < 0) g_device = c10::cuda::current_device();
+      if (x.get_device() != g_device)
+        return refuse("a tensor is on cuda:%d, and the current device is cuda:%d", (int)x.get_device(), (int)g_device);
       const auto sizes = x.sizes(), strides = x.strides();
       o->v.rank = (int32_t)x.dim();  // a rank that is too high is the library's to refuse
       o->v.dtype = type_of(x.scalar_type());
@@ -183,7 +188,9 @@ bool read_stream(PyObject* o, void** stream) {
   }
 }
 
+// The first step of every call.
 bool count_is(Py_ssize_t n, Py_ssize_t want) {
+  g_device = -1;
   if (n == want) return true;
   PyErr_Format(PyExc_TypeError, "%zd arguments, %zd are wanted", n, want);
   return false;
