@@ -113,3 +113,11 @@ def test_tensors_of_another_device():
                  lambda: hf.rms_norm_backward(a, a, zeros(4), b, dweight=zeros(8), workspace=scratch)):
         refused(call, f"on {other}")
     accepted(lambda: hf.rms_norm(a, b))
+
+
+def test_lazily_negated_tensors():
+    """A view whose values are the negatives of its memory's."""
+    x = torch._neg_view(zeros(4, 8))
+    refused(lambda: hf.rms_norm(x, zeros(4, 8)), "negates")
+    refused(lambda: hf.rms_norm(zeros(4, 8), x), "negates")
+    accepted(lambda: hf.rms_norm(x.resolve_neg(), zeros(4, 8)))

@@ -76,6 +76,7 @@ bool read(PyObject* t, Operand* o) {
       if (g_device < 0) g_device = c10::cuda::current_device();
       if (x.get_device() != g_device)
         return refuse("a tensor is on cuda:%d, and the current device is cuda:%d", (int)x.get_device(), (int)g_device);
+      if (x.is_neg()) return refuse("a tensor that negates its memory's values when it is read");
       const auto sizes = x.sizes(), strides = x.strides();
       o->v.rank = (int32_t)x.dim();  // a rank that is too high is the library's to refuse
       o->v.dtype = type_of(x.scalar_type());
