@@ -282,6 +282,12 @@ def test_parameters_are_of_their_own_type():
             hf.rms_norm(x, y, dropout=d, stream=0)
 
 
+def test_a_views_tensor_must_be_on_the_gpu():
+    torch = pytest.importorskip("torch")
+    refused(lambda: V(torch.zeros(4, 8), [4, 8], "f32"), word="on the GPU")
+    assert V(A, [4, 8], "f32").ptr == A and V(None, [0, 8], "f32").ptr == 0
+
+
 def test_f8_is_no_type_of_the_other_entry_points():
     a = hf.make_array([4, 5], None, "f32")
     a.dtype = 5

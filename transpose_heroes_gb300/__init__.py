@@ -454,6 +454,8 @@ class DeviceView:
         self.view = View(len(dims), VIEW_DTYPES[dtype])
         for i, (d, s) in enumerate(zip(dims, strides)):
             self.view.dims[i], self.view.strides[i] = d, int(s)
+        if ptr is not None and not isinstance(ptr, int) and not ptr.is_cuda:
+            raise HloError(STATUS_INVALID_ARG, "a view needs a tensor on the GPU, or an address")
         self.ptr, self.addr, self.keep = _ptr(ptr), ctypes.addressof(self.view), ptr
 
 
