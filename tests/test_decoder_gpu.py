@@ -139,3 +139,42 @@ def test_training_learns():
         opt.step()
     assert float(m.loss(tokens).detach()) < 0.2 * first
     assert m.generate([3, 1, 4, 1, 5, 9, 2, 6, 3, 1], 6) == [4, 1, 5, 9, 2, 6]
+
+
+# ---- the differentiable forms ------------------------------------------------------------------------------
+def _layouts(shape):
+    """The same values dense, transposed, and with a gap after every element."""
+    a = torch.randn(*shape, generator=torch.Generator().manual_seed(3)).cuda()
+    gaps = torch.zeros(*shape[:-1], 2 * shape[-1], device="cuda")[..., ::2]
+    gaps.copy_(a)
+    return [a, a.transpose(0, -1).contiguous().transpose(0, -1), gaps]
+
+
+FORMS = {
+    "drop": lambda D, x: D.drop(x, hf.Dropout(0.5, 3, 4)),
+    "rotate": lambda D, x: D.rotate(x, torch.arange(5, dtype=torch.int32, device="cuda"), torch.from_numpy(hf.rotary_turns(8)).cuda()),
+    "norm": lambda D, x: D.rms_norm_residual(x, torch.arange(1.0, 17.0, device="cuda")[::2])[0],
+    "residual": lambda D, x: D.rms_norm_residual(torch.ones(5, 3, 8, device="cuda"), torch.ones(8, device="cuda"), x)[0],
+}
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("reduce", ["sum", "mean", "transposed", "column"])
+def test_differentiable_forms_take_any_strides(form, reduce):
+    """Inputs and gradients that are transposed, strided or expanded (of sum and mean) give what dense ones give."""
+    from transpose_heroes_gb300 import decoder as D
+
+    weigh = torch.randn(8, 3, 5, generator=torch.Generator().manual_seed(4)).cuda()
+    results = []
+    for x in _layouts((5, 3, 8)):
+        for dense in (True, False):
+            x = x.detach().requires_grad_(True)
+            y = FORMS[form](D, x)
+            if dense:  # the gradient passes through a dense copy
+                y = y * torch.ones_like(y)
+            loss = {"sum": lambda: y.sum(), "mean": lambda: y.mean(), "transposed": lambda: (y.transpose(0, 2) * weigh).sum(),
+                    "column": lambda: y[..., 2].sum()}[reduce]()
+            loss.backward()
+            results.append((y.detach(), x.grad))
+    for y, g in results[1:]:
+        assert torch.equal(y, results[0][0]) and torch.equal(g, results[0][1])

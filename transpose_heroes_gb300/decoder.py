@@ -19,10 +19,15 @@ from . import dropout as _dropout
 from . import logits_process, rms_norm, rms_norm_backward, rms_norm_workspace_size, rotary, rotary_turns
 
 
+def _rows(t):
+    """t, copied only where the elements of a row do not lie together (a transposed or expanded tensor)."""
+    return t if t is None or t.dim() == 0 or t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
+
+
 class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, dropout, eps):
-        x = x.contiguous()
+        x, residual, weight = x.contiguous(), _rows(residual), weight.contiguous()
         y, h = torch.empty_like(x), torch.empty_like(x)
         rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         rms_norm(x, y, weight=weight, residual=residual, sum_out=h, rstd=rstd, eps=eps, dropout=dropout)
@@ -52,7 +57,7 @@ class _Rotate(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, positions, turns, interleaved, scale):
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        rotary(x, out, positions, turns, interleaved=interleaved, scale=scale)
+        rotary(_rows(x), out, positions, turns, interleaved=interleaved, scale=scale)
         ctx.save_for_backward(positions, turns)
         ctx.how = interleaved, scale
         return out
@@ -61,7 +66,7 @@ class _Rotate(torch.autograd.Function):
     def backward(ctx, g):
         positions, turns = ctx.saved_tensors
         out = torch.empty(g.shape, dtype=g.dtype, device=g.device)
-        rotary(g.contiguous(), out, positions, turns, interleaved=ctx.how[0], scale=ctx.how[1], inverse=True)
+        rotary(_rows(g), out, positions, turns, interleaved=ctx.how[0], scale=ctx.how[1], inverse=True)
         return out, None, None, None, None
 
 
@@ -74,11 +79,11 @@ class _Drop(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, params):
         ctx.params = params
-        return _dropout(x, torch.empty(x.shape, dtype=x.dtype, device=x.device), params)
+        return _dropout(_rows(x), torch.empty(x.shape, dtype=x.dtype, device=x.device), params)
 
     @staticmethod
     def backward(ctx, g):
-        return _dropout(g, torch.empty(g.shape, dtype=g.dtype, device=g.device), ctx.params), None
+        return _dropout(_rows(g), torch.empty(g.shape, dtype=g.dtype, device=g.device), ctx.params), None
 
 
 def drop(x, params):
