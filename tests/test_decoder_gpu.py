@@ -178,3 +178,16 @@ def test_differentiable_forms_take_any_strides(form, reduce):
             results.append((y.detach(), x.grad))
     for y, g in results[1:]:
         assert torch.equal(y, results[0][0]) and torch.equal(g, results[0][1])
+
+
+def test_a_norm_without_weight_or_with_a_fixed_one():
+    """No weight, and one that wants no gradient, leave the gradient of x what it is."""
+    from transpose_heroes_gb300 import decoder as D
+
+    base = torch.randn(5, 8, generator=torch.Generator().manual_seed(3)).cuda()
+    grads = []
+    for weight in (torch.ones(8, device="cuda", requires_grad=True), torch.ones(8, device="cuda"), None):
+        x = base.clone().requires_grad_(True)
+        D.rms_norm_residual(x, weight)[0].pow(3).sum().backward()
+        grads.append(x.grad)
+    assert torch.equal(grads[0], grads[1]) and torch.equal(grads[0], grads[2])

@@ -27,7 +27,7 @@ def _rows(t):
 class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, dropout, eps):
-        x, residual, weight = x.contiguous(), _rows(residual), weight.contiguous()
+        x, residual, weight = x.contiguous(), _rows(residual), None if weight is None else weight.contiguous()
         y, h = torch.empty_like(x), torch.empty_like(x)
         rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
         rms_norm(x, y, weight=weight, residual=residual, sum_out=h, rstd=rstd, eps=eps, dropout=dropout)
@@ -41,15 +41,17 @@ class _RmsNorm(torch.autograd.Function):
         n = h.shape[-1]
         dh = torch.empty_like(h)
         dx = torch.empty_like(h) if ctx.dropout is not None else None
-        dw = torch.empty(n, dtype=torch.float32, device=h.device)
-        ws = torch.empty(rms_norm_workspace_size(h.numel() // n, n), dtype=torch.uint8, device=h.device)
+        dw = ws = None
+        if ctx.needs_input_grad[1]:
+            dw = torch.empty(n, dtype=torch.float32, device=h.device)
+            ws = torch.empty(rms_norm_workspace_size(h.numel() // n, n), dtype=torch.uint8, device=h.device)
         rms_norm_backward(dy.contiguous(), h, rstd, dh, weight=weight, dsum=dsum.contiguous(), dx=dx, dropout=ctx.dropout,
                           dweight=dw, workspace=ws)
-        return dx if dx is not None else dh, dw.to(weight.dtype), dh if ctx.joined else None, None, None
+        return dx if dx is not None else dh, None if dw is None else dw.to(weight.dtype), dh if ctx.joined else None, None, None
 
 
 def rms_norm_residual(x, weight, residual=None, dropout=None, eps=1e-6):
-    """(y, h): h = residual + drop(x), y = h / rms(h) * weight; differentiable in x, weight and residual."""
+    """(y, h): h = residual + drop(x), y = h / rms(h) * weight (None: ones); differentiable in x, weight and residual."""
     return _RmsNorm.apply(x, weight, residual, dropout, eps)
 
 
