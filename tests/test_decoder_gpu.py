@@ -191,3 +191,14 @@ def test_a_norm_without_weight_or_with_a_fixed_one():
         D.rms_norm_residual(x, weight)[0].pow(3).sum().backward()
         grads.append(x.grad)
     assert torch.equal(grads[0], grads[1]) and torch.equal(grads[0], grads[2])
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_second_derivatives_raise(form):
+    """Not silently left out, where another path carries the graph on."""
+    from transpose_heroes_gb300 import decoder as D
+
+    x = torch.randn(5, 3, 8, generator=torch.Generator().manual_seed(3)).cuda().requires_grad_(True)
+    g, = torch.autograd.grad(FORMS[form](D, x).pow(2).sum() + x.pow(3).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()

@@ -6,6 +6,8 @@ with them (matrix products and attention itself are plain torch).
     rms_norm_residual(x, weight, residual, dropout)   y, h: h = residual + drop(x), y = rms_norm(h) * weight
     rotate(x, positions, turns)                       rotary positions
     drop(x, params)                                   dropout whose mask is never stored
+
+Their gradients are not differentiable again: a second derivative through them raises.
 """
 
 from __future__ import annotations
@@ -13,6 +15,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import Dropout
 from . import dropout as _dropout
@@ -36,6 +39,7 @@ class _RmsNorm(torch.autograd.Function):
         return y, h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dsum):
         h, weight, rstd = ctx.saved_tensors
         n = h.shape[-1]
@@ -65,6 +69,7 @@ class _Rotate(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         positions, turns = ctx.saved_tensors
         out = torch.empty(g.shape, dtype=g.dtype, device=g.device)
@@ -84,6 +89,7 @@ class _Drop(torch.autograd.Function):
         return _dropout(_rows(x), torch.empty(x.shape, dtype=x.dtype, device=x.device), params)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         return _dropout(_rows(g), torch.empty(g.shape, dtype=g.dtype, device=g.device), ctx.params), None
 
