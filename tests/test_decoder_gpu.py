@@ -202,3 +202,36 @@ def test_second_derivatives_raise(form):
     g, = torch.autograd.grad(FORMS[form](D, x).pow(2).sum() + x.pow(3).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         g.sum().backward()
+
+
+def test_overwriting_a_saved_tensor_is_noticed():
+    """The sum h that the norm keeps for its backward pass is the caller's residual stream: a call that writes over it moves its
+    version, as torch's own operations do, and the backward pass raises in place of using the new values."""
+    from transpose_heroes_gb300 import decoder as D
+
+    x = torch.randn(5, 8, device="cuda", requires_grad=True)
+    y, h = D.rms_norm_residual(x, torch.ones(8, device="cuda"))
+    with torch.no_grad():
+        hf.dropout(h, h, hf.Dropout(0.5, 1, 2))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
+def test_every_output_moves_its_version():
+    new = lambda *s, t=torch.float32: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+    x, out, s, r = new(4, 8), new(4, 8), new(4, 8), new(4)
+    q, scales, ws, dw, dx = new(4, 8, t=torch.int8), new(4), new(1 << 16, t=torch.uint8), new(8), new(4, 8)
+    hf.rms_norm(x, out, sum_out=s, rstd=r)
+    hf.rms_norm(x, q, scales=scales)
+    hf.rms_norm_backward(x, s, r, out, dx=dx, dropout=hf.Dropout(0.5), dweight=dw, workspace=ws)
+    a, b, tok, l = new(3, 2, 8), new(3, 1, 8), new(4, t=torch.int32), new(4, 8)
+    turns = new(4, t=torch.int64)
+    hf.rotary(a, a, new(3, t=torch.int32), turns, k=b, k_out=b)
+    hf.logits_process(x, l, token=tok)
+    hf.dropout(x, l, hf.Dropout(0.5))
+    assert [t._version for t in (x, out, s, r, q, scales, ws, dw, dx, a, b, tok, l, turns)] == [0, 2, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 2, 0]
+    with torch.inference_mode():  # tensors that have no versions
+        hf.dropout(x, torch.empty_like(x), hf.Dropout(0.5))
+    with pytest.raises(hf.HloError):
+        hf.dropout(x, x[:, 1:], hf.Dropout(0.5))  # refused: nothing was written
+    assert x._version == 0

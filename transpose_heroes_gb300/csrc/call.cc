@@ -14,6 +14,7 @@
 #include <cstdarg>
 #include <cstring>
 #include <exception>
+#include <initializer_list>
 
 #include "hlo_fusion.h"
 
@@ -204,14 +205,25 @@ int64_t rows_of(const hlo_view& v) {
 }
 int64_t last_of(const hlo_view& v) { return v.rank > 0 && v.rank <= HLO_MAX_RANK ? v.dims[v.rank - 1] : 0; }
 
-PyObject* status(hlo_status s) { return PyLong_FromLong((long)s); }
+// The status; after a call that ran, its output tensors' versions have moved on, so that autograd notices a saved tensor
+// that was overwritten.
+PyObject* status(hlo_status s, std::initializer_list<PyObject*> outputs) {
+  if (s == HLO_OK) {
+    for (PyObject* t : outputs) {
+      if (!THPVariable_Check(t)) continue;
+      const at::Tensor& x = THPVariable_Unpack(t);
+      if (!x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
+    }
+  }
+  return PyLong_FromLong((long)s);
+}
 
-#define CALL(expr)                             \
+#define CALL(expr, ...)                        \
   hlo_status st;                               \
   Py_BEGIN_ALLOW_THREADS;                      \
   st = (expr);                                 \
   Py_END_ALLOW_THREADS;                        \
-  return status(st)
+  return status(st, {__VA_ARGS__})
 
 // x, out, weight, weight_dtype, residual, sum, rstd, eps, weight_offset, dropout, scales, out_q, stream
 PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -232,7 +244,8 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const double eps = PyFloat_AsDouble(a[7]), off = PyFloat_AsDouble(a[8]);
   if (PyErr_Occurred()) return nullptr;
   CALL(hlo_rms_norm(x.view(), x.p, res.view(), res.p, drop, w, wdt, off, eps, sum.view(), sum.p, out.view(), out.p,
-                    static_cast<float*>(scales), q, static_cast<float*>(rstd), stream));
+                    static_cast<float*>(scales), q, static_cast<float*>(rstd), stream),
+       a[1], a[5], a[6], a[10]);
 }
 
 // dy, h, rstd, dh, weight, weight_dtype, dsum, dx, dropout, dweight, workspace, workspace_bytes, weight_offset, stream
@@ -255,7 +268,8 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const double off = PyFloat_AsDouble(a[12]);
   if (PyErr_Occurred()) return nullptr;
   CALL(hlo_rms_norm_backward(dy.view(), dy.p, h.view(), h.p, static_cast<float*>(rstd), w, wdt, off, ds.view(), ds.p, drop, dh.view(),
-                             dh.p, dx.view(), dx.p, static_cast<float*>(dw), ws, bytes, stream));
+                             dh.p, dx.view(), dx.p, static_cast<float*>(dw), ws, bytes, stream),
+       a[3], a[7], a[9], a[10]);
 }
 
 // x, out, dropout, residual, stream
@@ -265,7 +279,7 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
   hlo_dropout_params* drop;
   void* stream;
   if (!read(a[0], &x) || !read(a[1], &out) || !read(a[3], &res) || !read_struct(a[2], g_dropout_type, &drop) || !read_stream(a[4], &stream)) return nullptr;
-  CALL(hlo_dropout(x.view(), x.p, res.view(), res.p, drop, out.view(), out.p, stream));
+  CALL(hlo_dropout(x.view(), x.p, res.view(), res.p, drop, out.view(), out.p, stream), a[1]);
 }
 
 // x, out, positions, turns, n_pairs (None: turns' count, the most that is taken), k, k_out, interleaved, scale, inverse, stream
@@ -292,7 +306,8 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (pairs > INT32_MAX) pairs = INT32_MAX;
   if (pairs < -1) pairs = -1;  // refused
   CALL(hlo_rotary(x.view(), x.p, out.view(), out.p, k.view(), k.p, kout.view(), kout.p, pos.view(), static_cast<int32_t*>(pos.p),
-                  static_cast<uint64_t*>(turns), (int32_t)pairs, inter, inverse, scale, stream));
+                  static_cast<uint64_t*>(turns), (int32_t)pairs, inter, inverse, scale, stream),
+       a[1], a[6]);
 }
 
 // A row of n dimensions serves every row of the batch.
@@ -322,7 +337,8 @@ PyObject* logits_process(PyObject*, PyObject* const* a, Py_ssize_t n) {
   CALL(hlo_logits_process(x.view(), x.p, bias.view(), static_cast<float*>(bias.p), hist.view(), static_cast<int32_t*>(hist.p),
                           static_cast<int32_t*>(len), static_cast<int32_t*>(prompt), static_cast<float*>(rep),
                           static_cast<float*>(freq), static_cast<float*>(pres), mask.view(), static_cast<int32_t*>(mask.p), out.view(),
-                          out.p, static_cast<int32_t*>(token), stream));
+                          out.p, static_cast<int32_t*>(token), stream),
+       a[1], a[10]);
 }
 
 // DeviceView, HloError, Dropout and Quant
