@@ -288,6 +288,31 @@ def test_a_views_tensor_must_be_on_the_gpu():
     assert V(A, [4, 8], "f32").ptr == A and V(None, [0, 8], "f32").ptr == 0
 
 
+def test_the_library_builds_without_torch(monkeypatch, tmp_path):
+    """nvcc is enough for it; the extension is left out."""
+    import sys
+
+    monkeypatch.setitem(sys.modules, "torch", None)  # as if it were not installed
+    monkeypatch.setattr(hbuild, "CALL", str(tmp_path / "_hlocall.so"))
+    assert hbuild.build() == hbuild.LIB
+    assert not list(tmp_path.iterdir())
+
+
+def test_an_extension_of_another_torch_is_not_loaded(monkeypatch, tmp_path):
+    """... and is not up to date."""
+    pytest.importorskip("torch")
+    import shutil
+
+    call = str(tmp_path / "_hlocall.so")
+    shutil.copy(hbuild.CALL, call)
+    (tmp_path / "_hlocall.so.abi").write_text("torch 1.0, another")
+    monkeypatch.setattr(hf, "CALL_PATH", call)
+    monkeypatch.setattr(hf, "_call", None)
+    with pytest.raises(RuntimeError, match="built for torch 1.0"):
+        hf.dropout(V(A, [4], "f32"), V(B, [4], "f32"), hf.Dropout(0.5), stream=0)
+    assert hbuild.built_for(call) != hbuild.call_abi() == hbuild.built_for()
+
+
 def test_f8_is_no_type_of_the_other_entry_points():
     a = hf.make_array([4, 5], None, "f32")
     a.dtype = 5

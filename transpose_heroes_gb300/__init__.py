@@ -473,6 +473,12 @@ def _load_call():
 
     import torch  # noqa: F401  (the extension uses its libraries)
 
+    from . import build
+
+    if build.built_for(CALL_PATH) != build.call_abi():
+        raise RuntimeError(f"_hlocall.so was built for {build.built_for(CALL_PATH) or 'an unknown torch'}, and this is "
+                           f"{build.call_abi()}; run transpose_heroes_gb300.build.build()")
+
     spec = importlib.util.spec_from_file_location("_hlocall", CALL_PATH)
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)

@@ -1,8 +1,9 @@
-"""Build libhlofusion.so in-tree for sm_103a (nvcc only; no torch extension machinery).
+"""Build libhlofusion.so in-tree for sm_103a (nvcc alone).
 
 Every translation unit under csrc/ is compiled in parallel to an object file, then linked into
 transpose_heroes_gb300/_lib/libhlofusion.so with the CUDA runtime linked statically. csrc/call.cc becomes
-_lib/_hlocall.so, a CPython extension on top of it.
+_lib/_hlocall.so, a CPython extension on top of it, compiled by the host compiler against the torch that is installed; without a
+torch for CUDA it is left out, and the layer operators raise when they are called from Python.
 """
 
 from __future__ import annotations
@@ -80,15 +81,35 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-    if force or _stale(CALL, [call_obj]):
+    if call_obj and (force or _stale(CALL, [call_obj]) or built_for() != call_abi()):
         _link_call(call_obj)
     return LIB
 
 
-def _compile_call(force: bool) -> str:
-    """The CPython extension that marshals the layer operators' calls (csrc/call.cc), against torch's headers."""
+def call_abi() -> str:
+    """What _hlocall.so is compiled for: the versions of torch and of Python's extensions. Empty without a torch for CUDA."""
+    try:
+        import torch
+    except ImportError:
+        return ""
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}" if torch.version.cuda else ""
+
+
+def built_for(call: str | None = None) -> str:
+    """call_abi() of when the extension was built."""
+    path = (call or CALL) + ".abi"
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read()
+
+
+def _compile_call(force: bool) -> str | None:
+    """The CPython extension that marshals the layer operators' calls (csrc/call.cc), against torch's headers; None without them."""
     src, obj = os.path.join(CSRC, "call.cc"), os.path.join(BUILD, "call.o")
-    if force or _stale(obj, [src, os.path.join(INCLUDE, "hlo_fusion.h")]):
+    if not call_abi():
+        return None
+    if force or _stale(obj, [src, os.path.join(INCLUDE, "hlo_fusion.h")]) or built_for() != call_abi():
         import torch
 
         torch_include = os.path.join(os.path.dirname(torch.__file__), "include")
@@ -115,6 +136,8 @@ def _link_call(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALL)
+    with open(CALL + ".abi", "w") as f:
+        f.write(call_abi())
 
 
 if __name__ == "__main__":
