@@ -313,8 +313,6 @@ hlo_status hlo_rms_norm(const hlo_view* x, const void* x_ptr, const hlo_view* re
   p.eps = (float)eps;
   const hlo_view* const views[4] = {x, residual, sum, out};
   p.map = merge_rows<4>(views, x->rank - 1);
-  p.end[0] = end_of(x, x_ptr);
-  p.end[1] = end_of(residual, residual_ptr);
   INJECT("hlo_rms_norm");
   return api_cuda_status(launch_norm(p, as_stream(stream)), "rms_norm launch");
 }
@@ -402,7 +400,6 @@ hlo_status hlo_rms_norm_backward(const hlo_view* dy, const void* dy_ptr, const h
   p.w_offset = (float)weight_offset;
   const hlo_view* const views[5] = {dy, h, dsum, dh, dx};
   p.map = merge_rows<5>(views, h->rank - 1);
-  for (int k = 0; k < 3; ++k) p.end[k] = end_of(all[k].v, all[k].p);
   return api_cuda_status(launch_norm_grad(p, as_stream(stream)), "rms_norm_backward launch");
 }
 

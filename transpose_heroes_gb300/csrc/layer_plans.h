@@ -63,7 +63,6 @@ struct NormPlan {
   QuantParams q;      // NQ_STATIC
   DropPlan drop;
   Rows<4> map;        // x, residual, sum, out
-  const char* end[2]; // of x and residual
 };
 cudaError_t launch_norm(const NormPlan& p, cudaStream_t s);
 
@@ -82,7 +81,6 @@ struct NormGradPlan {
   float w_offset;
   DropPlan drop;
   Rows<5> map;        // dy, h, dsum, dh, dx
-  const char* end[3]; // of dy, h and dsum
 };
 // Row groups whose shares of dweight are summed apart (each one row of n f32 in the workspace).
 int64_t norm_grad_partials(int64_t rows, int64_t n);
