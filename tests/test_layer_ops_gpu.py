@@ -375,6 +375,24 @@ def test_dropout_extremes_and_specials():
     assert bool((x[~k] == 0).all()) and bool((x.isnan() == (k & (torch.arange(256, device="cuda") % 4 == 0))).all())
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,pitch,shift", [(4096, 0, 0), (1001, 0, 0), (72, 3, 1), (40000, 0, 0), (5, 0, 1)])
+def test_dropped_elements_of_a_negative_zero_residual(n, pitch, shift, dtype):
+    """-0 + 0 is +0, whatever the alignment, in dropout and in the norm's sum; -0 + -0 (a kept element) stays -0."""
+    d, rows = hf.Dropout(0.5, 9, 1), 3
+    x, _ = dev(np.full((rows, n), -0.0), dtype, pitch, shift)
+    r, _ = dev(np.full((rows, n), -0.0), dtype, pitch, shift)
+    kept = torch.from_numpy(ref.keep(0.5, 9, 1, rows * n).reshape(rows, n)).cuda()
+    out, odd = torch.empty(rows, n, dtype=DT[dtype], device="cuda"), torch.empty(rows, n + 1, dtype=DT[dtype], device="cuda")[:, 1:]
+    h, y = Band((rows, n), DT[dtype], pitch, shift).t, torch.empty(rows, n, dtype=DT[dtype], device="cuda")
+    for o in (out, odd, Band((rows, n), DT[dtype], pitch, shift).t):
+        hf.dropout(x, o, d, residual=r)
+        assert bool((o == 0).all()) and torch.equal(o.signbit(), kept)
+    for o in (y, Band((rows, n), DT[dtype], pitch, shift).t):
+        hf.rms_norm(x, o, residual=r, sum_out=h, dropout=d)
+        assert bool((h == 0).all()) and torch.equal(h.signbit(), kept)
+
+
 def test_dropout_mask_does_not_depend_on_the_shape_and_is_the_norms_mask():
     d = hf.Dropout(0.3, 42, 5)
     x = torch.ones(6, 1001, device="cuda")

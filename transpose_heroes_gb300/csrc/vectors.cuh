@@ -154,17 +154,19 @@ __device__ __forceinline__ void drop_vec(const DropPlan& d, const Philox<MODE>& 
   for (int e = 0; e < W; ++e) v[e] = dropped(d, w[e], v[e]);
 }
 
-// v = r + drop(v): the addition happens or not (a residual of -0 stays -0 where v is dropped), which costs less than
-// a select and an addition.
+// v = r + drop(v): r + 0 where v is dropped (+0 for an r of -0), the addition of v where it is kept. Two predicated results
+// cost less than a select and an addition.
 template <int MODE, bool WHOLE, int W>
 __device__ __forceinline__ void drop_add_vec(const DropPlan& d, const Philox<MODE>& g, int64_t i, float (&v)[W], const float (&r)[W]) {
   uint32_t w[W + 4];
   drop_words<MODE, WHOLE, W>(d, g, i, w);
 #pragma unroll
-  for (int e = 0; e < W; ++e) {
-    const float t = __fmul_rn(v[e], d.scale);
-    v[e] = r[e];
-    if (kept(d, w[e])) v[e] = __fadd_rn(r[e], t);
+  for (int e = 0; e < W; e += 2) {
+    const float2 t = __fmul2_rn(make_float2(v[e], v[e + 1]), make_float2(d.scale, d.scale));
+    const float2 s = __fadd2_rn(make_float2(r[e], r[e + 1]), make_float2(0.0f, 0.0f));
+    v[e] = s.x, v[e + 1] = s.y;
+    if (kept(d, w[e])) v[e] = __fadd_rn(r[e], t.x);
+    if (kept(d, w[e + 1])) v[e + 1] = __fadd_rn(r[e + 1], t.y);
   }
 }
 
