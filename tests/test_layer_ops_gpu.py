@@ -853,6 +853,21 @@ def test_rotary_past_2_31_elements():
     assert bool((x[:2] == 0).all())
 
 
+def test_rotary_of_the_most_tokens_that_32_bits_count():
+    """Rounded up to whole blocks, they are more than 2^31."""
+    _room(40)
+    tokens, dim = (1 << 31) - 1, 8
+    x = torch.zeros(tokens, 1, dim, dtype=torch.bfloat16, device="cuda")
+    last, ld = dev(rnd(1, 300, 1, dim), "bf16")
+    x[:300], x[-300:] = last, last
+    turns = ref.turns_of(dim)
+    pos = torch.full((1, 1), 1000, dtype=torch.int32, device="cuda").expand(tokens, 1)  # repeated over the batch
+    hf.rotary(x[:, None], x[:, None], pos, torch.from_numpy(turns.view(np.int64)).cuda())
+    want, err = ref.rotary(ld[None], np.full((1, 300), 1000), turns)
+    close(x[:300], want[0], err[0], "bf16")
+    close(x[-300:], want[0], err[0], "bf16")
+
+
 def test_logits_past_2_31_elements():
     _room(16)
     vocab = 131072

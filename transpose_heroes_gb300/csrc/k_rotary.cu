@@ -390,7 +390,8 @@ cudaError_t launch_rotary(const RotaryPlan& p, cudaStream_t s) {
   t.items = t.turned + (t.copied + 1) / 2;
   if (t.items == 0) return cudaSuccess;  // nothing turns, and nothing has to be copied
   const int64_t heads = std::max(p.a[0].heads, p.arrays > 1 ? p.a[1].heads : 0);
-  if (t.items <= 256 && p.pairs <= 4096 && p.batch <= INT32_MAX / p.seq && heads <= 32767) {
+  // tokens are counted in 32 bits, rounded up to whole blocks of at most 256
+  if (t.items <= 256 && p.pairs <= 4096 && p.batch <= (INT32_MAX - 256) / p.seq && heads <= 32767) {
     if (p.dt == F32) return run_rotary_type<F32>(p, v, t, s);
     if (p.dt == BF16) return run_rotary_type<BF16>(p, v, t, s);
     return run_rotary_type<F16>(p, v, t, s);
