@@ -313,6 +313,20 @@ def test_an_extension_of_another_torch_is_not_loaded(monkeypatch, tmp_path):
     assert hbuild.built_for(call) != hbuild.call_abi() == hbuild.built_for()
 
 
+def test_side_outputs_over_the_generators_state(monkeypatch):
+    x, y, s8, h = V(A, [4, 8], "f32"), V(B, [4, 8], "f32"), V(B, [4, 8], "s8"), V(C, [4, 8], "f32")
+    at = lambda p: hf.Dropout(0.5, 1, 2, state=p)  # noqa: E731
+    refused(lambda: hf.rms_norm(x, y, rstd=S, dropout=at(S + 8), stream=0), word="state")
+    refused(lambda: hf.rms_norm(x, s8, scales=S + 8, dropout=at(S), stream=0), word="state")
+    need = hf.rms_norm_workspace_size(4, 8)
+    run = lambda d, w, p: hf.rms_norm_backward(x, h, S, y, dx=V(E, [4, 8], "f32"), dropout=at(p), dweight=d, workspace=w,  # noqa: E731
+                                               workspace_bytes=need, stream=0)
+    refused(lambda: run(S + 4096, S + 8192, S + 4096 + 24), word="state")
+    refused(lambda: run(S + 4096, S + 8192, S + 8192), word="state")
+    accepted(lambda: run(S + 4096, S + 8192, S + 16), monkeypatch)
+    accepted(lambda: hf.rms_norm(x, y, rstd=S, dropout=at(S + 16), stream=0), monkeypatch)
+
+
 def test_f8_is_no_type_of_the_other_entry_points():
     a = hf.make_array([4, 5], None, "f32")
     a.dtype = 5

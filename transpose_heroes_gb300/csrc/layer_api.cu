@@ -294,6 +294,8 @@ hlo_status hlo_rms_norm(const hlo_view* x, const void* x_ptr, const hlo_view* re
       if (i.v) TRY(check_side(i, f, rows * 4, "scales or rstd"));
     if (weight_ptr && ranges_overlap(f, rows * 4, weight_ptr, n * dt_bytes(weight_dtype)))
       return api_fail(HLO_ERR_INVALID_ARG, "rms_norm: scales or rstd overlaps the weight");
+    if (dropout && ranges_overlap(f, rows * 4, dropout->state, 16))
+      return api_fail(HLO_ERR_INVALID_ARG, "rms_norm: scales or rstd overlaps the generator's state");
   }
   if (ranges_overlap(scales, rows * 4, rstd, rows * 4)) return api_fail(HLO_ERR_INVALID_ARG, "rms_norm: scales overlaps rstd");
   if (rows == 0) return api_ok();
@@ -379,6 +381,8 @@ hlo_status hlo_rms_norm_backward(const hlo_view* dy, const void* dy_ptr, const h
       (weight_ptr && (ranges_overlap(dweight, n * 4, weight_ptr, n * dt_bytes(weight_dtype)) ||
                       ranges_overlap(workspace, need, weight_ptr, n * dt_bytes(weight_dtype)))))
     return api_fail(HLO_ERR_INVALID_ARG, "rms_norm_backward: dweight or the workspace overlaps another buffer");
+  if (dropout && (ranges_overlap(dweight, n * 4, dropout->state, 16) || ranges_overlap(workspace, need, dropout->state, 16)))
+    return api_fail(HLO_ERR_INVALID_ARG, "rms_norm_backward: dweight or the workspace overlaps the generator's state");
   INJECT("hlo_rms_norm_backward");
   if (rows == 0) {  // a sum over no rows
     if (!dweight) return api_ok();
