@@ -711,6 +711,33 @@ def test_calls_run_on_the_stream_they_are_given():
     assert bool((y == 1.0).all()) and bool((tok == 0).all())
 
 
+def test_calls_after_another_streams_event():
+    """A call that may be set up while the one before it on its stream ends still waits for an event of another stream between
+    them, and that stream's next calls for this one's. Powers of two, whose norms are exact."""
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    rows, n = 512, 1024
+    d = hf.Dropout(0.0, 1, 1)
+    x, y, z, w = (torch.zeros(rows, n, device="cuda") for _ in range(4))
+    for step in [2.0 ** (k % 6) for k in range(20)]:
+        torch.cuda.synchronize()
+        with torch.cuda.stream(b):
+            torch.cuda._sleep(200_000)
+            z.fill_(step)
+            hf.dropout(z, x, d)
+            wrote = b.record_event()
+        with torch.cuda.stream(a):
+            hf.dropout(w, w, d)  # short, and done long before the event
+            a.wait_event(wrote)
+            hf.dropout(x, y, d, residual=x)
+            hf.rms_norm(y, w, eps=0.0)
+            read = a.record_event()
+        with torch.cuda.stream(b):
+            b.wait_event(read)
+            hf.dropout(w, x, d, residual=y)
+        torch.cuda.synchronize()
+        assert bool((y == 2.0 * step).all()) and bool((w == 1.0).all()) and bool((x == 2.0 * step + 1.0).all())
+
+
 def test_calls_are_captured_into_a_graph():
     """Norm, gradient (two kernels), rotary and logits replayed on new inputs give what direct calls give."""
     rows, n = 700, 1032
