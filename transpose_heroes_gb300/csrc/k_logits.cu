@@ -128,8 +128,9 @@ constexpr int kTableSlab = 1 << 17;
 // ALONE: an SM has one block, which has its registers for itself and nobody to hide its waits: parts 1 and 2 take
 // four tokens a thread at a time.
 // Bound: for a batch, the scattered accesses of the listed tokens (a wavefront each) and the waits of parts 1
-// and 2, not HBM: 256 rows of 131072 bf16 with histories of up to 4096 entries, bias and mask (141 MB, most of it in the
-// second-level cache between calls) 56 us; without a history 29 us, 4.6 TB/s, without bias and mask as well 21 us.
+// and 2, not HBM: 256 rows of 131072 bf16 with histories of up to 4096 entries, bias and mask (141 MB) 60 us, or 56
+// where most of it is in the second-level cache; without a history 34 us, without bias as well 25.5, 5.4 TB/s, without the
+// mask 24.
 // One row of 32000 with 700 entries 5.3 us.
 // The slab's first logits are requested before all this. The blocks' best tokens are written to the first
 // block's shared memory, and only that block waits for them.
@@ -438,9 +439,9 @@ cudaError_t run_logits_blocks(const LogitsPlan& p, int threads, int cluster, cud
   const int u = vectors >= (int64_t)3 * threads * cluster ? 4 : 1;
   const int64_t batch = (int64_t)threads * u * W, needed = (vectors * W + batch * cluster - 1) / (batch * cluster);
   // A table, half full at most, where it leaves an SM its blocks; slabs of 131072 tokens then, as the work on a slab's
-  // history does not shrink with it. 256 rows of 131072 with 4096 entries each take 51 us, with 6500 101 us (the
-  // shared memory is then missing from the first-level cache); with counts for all of a slab's tokens (slabs of
-  // 64 KB of counts) 70 and 110 us
+  // history does not shrink with it. 256 rows of 131072 with 4096 entries each take 50 us, with 6500 85 us (with bias and mask 62
+  // and 134: the shared memory is then missing from the first-level cache); with counts for all of a slab's tokens (slabs
+  // of 64 KB of counts) 61 and 97 (75 and 133)
   const int table = (int)std::min<int64_t>((2 * p.max_length + 7) / 4 * 4, 1 << 20);
   const int table_batches = (int)std::max<int64_t>(1, std::min(kTableSlab / batch, needed));
   const size_t room = (ALONE ? 220 : 110) * 1024;

@@ -60,10 +60,10 @@ __global__ void __launch_bounds__(kAnyThreads) norm_grad_any_kernel(const __grid
 // workspace, and norm_grad_join_kernel adds them in order.
 //
 // CUT rows are taken apart as in norm_row_kernel; their weights lie in shared memory too, in the same places. (A column a thread, for
-// sums and weights in registers at any alignment, took 120 us in place of 79: one element an access.)
+// sums and weights in registers at any alignment, took 120 us in place of 80: one element an access.)
 // Bound: the loads wait for the row's reduction, so an SM has few bytes in flight; this form serves cut rows and
-// few rows. 2049 x 1001 f32 (33 MB, in the second-level cache) 12 us with dweight, 16384 x 1001 f32 (262 MB) 50 us,
-// 5.3 TB/s; 32768 x 1001 bf16 79 us, the column sums in shared memory costing as much as the row itself.
+// few rows. 2049 x 1001 f32 (33 MB, in the second-level cache) 12 us with dweight, 16384 x 1001 f32 (262 MB) 52 us,
+// 5.1 TB/s; 32768 x 1001 bf16 80 us, the column sums in shared memory costing as much as the row itself.
 template <int DT, int K, int DROP, bool CUT>
 __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(const __grid_constant__ NormGradPlan p, int weight_whole, int64_t groups) {
   constexpr int W = kVec<DT>, EB = 16 / W;
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(cons
   float* const cols = cut_shared + (1 + (int)threadIdx.y) * places;
   if (CUT) {
     const int t0 = threadIdx.y * blockDim.x + threadIdx.x, step = blockDim.x * blockDim.y;
-    if (p.w && p.w_dt == DT) {  // without the choices of weight_at the loads go out eight at a time: 333 x 8191 bf16 11 us in place of 16
+    if (p.w && p.w_dt == DT) {  // without the choices of weight_at the loads go out eight at a time: 333 x 8191 bf16 10 us in place of 16
 #pragma unroll 8
       for (int c = t0; c < n; c += step) ws[c + c / W] = load_plain(p.w, DT, c) + p.w_offset;
     } else {
@@ -202,8 +202,9 @@ __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_grad_row_kernel(cons
 // dsum) coming with bulk copies, so the loads never wait for the row's reduction. K vectors a thread.
 // One barrier a row: it joins the warps' dot products, and behind it every thread has left the row
 // before, whose stage is refilled then. Sums are formed with packed f32x2 instructions.
-// Bound: HBM without dropout (8192 x 4096 bf16, 268 MB: 44 us for this kernel, 6.0 TB/s; 50 us with the join),
-// the generator with it (336 MB in 69 us, 4.8 TB/s: multiplier 57%, ALU 45%, issue 60% busy).
+// Bound: HBM without dropout (8192 x 4096 bf16, 268 MB: 46 us alone, 47.5 a call with the join, 5.7 TB/s),
+// the row's phases with it, as the masks are drawn by all warps after the row's barrier (336 MB in 70 us, 4.8 TB/s: multiplier
+// 57%, ALU 45%, issue 57% busy).
 constexpr int kMaxStages = 8;
 
 template <int DT, int K, int DROP, int MAXT>
@@ -462,7 +463,7 @@ RingShape ring_shape(int64_t vectors, int arrays) {
   r.k = vectors > 512 ? 4 : vectors > 128 ? 2 : 1;
   r.threads = (int)((vectors + r.k - 1) / r.k + 31) / 32 * 32;
   const size_t stage = (size_t)vectors * 16 * arrays;
-  // 768 threads an SM: 8192 x 4096 bf16 takes 52 us, with 512 threads 58 us, with 256 85 us
+  // 768 threads an SM: 8192 x 4096 bf16 took 52 us when this was chosen (47.5 now), with 512 threads 58 us, with 256 85 us
   const int blocks = std::max(1, std::min(16, 768 / r.threads));
   const size_t room = (size_t)220 * 1024 / blocks - 1024;
   r.stages = (int)std::min<size_t>(kMaxStages, room / stage);

@@ -85,7 +85,7 @@ struct RotaryTile {
 // two halves of V pairs (half layout), V adjacent pairs (interleaved), or 2 V copied elements; a thread's
 // item and token stay, so the places of its elements and its cosines are found once for U heads. The
 // loads of the first U heads are issued before the cosines are computed. Bound: latency for a few tokens (32 tokens
-// of 32 + 8 heads: 4.1 us a call, the launch); HBM and the phases of a block for many (see below).
+// of 32 + 8 heads: 4 us a call, the launch); HBM and the phases of a block for many (see below).
 template <int DT, int V, int U, bool INTER>
 __global__ void __launch_bounds__(256, 3) rotary_kernel(const __grid_constant__ RotaryPlan p, const RotaryTile t, int total_tokens,
                                                      int total_heads) {
@@ -194,7 +194,7 @@ cudaError_t run_rotary(const RotaryPlan& p, const RotaryTile& tile, cudaStream_t
 // coming with one bulk copy a token and array, so the loads never wait for the cosines. A group's cosines go
 // to one of two tables in shared memory before its one barrier, behind which every thread has left the group
 // before, whose stage is refilled then. Threads share the heads as in rotary_kernel.
-// Bound: HBM. 2 x 16384 tokens of 32 + 8 heads of 128 bf16 (671 MB): 108 us, 6.2 TB/s, 92% of the copy rate;
+// Bound: HBM. 2 x 16384 tokens of 32 + 8 heads of 128 bf16 (671 MB): 106 us, 6.3 TB/s, 93% of the copy rate;
 // rotary_kernel takes 117 us, as its blocks' loads, cosines and stores follow one another.
 constexpr int kMaxStages = 4;
 

@@ -45,11 +45,11 @@ __device__ __forceinline__ void store_row_vec(const NormPlan& p, int64_t at, con
 // 16-byte boundary, the same column in every operand, and the up to 2 W - 2 elements before and behind them
 // go to a thread each.
 // Bound: HBM. A row is read and written once, so the time is that of its bytes: 16384 x 8192 bf16 with
-// residual (1074 MB) 157 us, 6.84 TB/s, the rate of a plain copy, and 146 us to f8 with scales
-// (940 MB, 6.4 TB/s); cut rows, 32768 x 1001 bf16, 53 us (5.0 TB/s: the weights are shifted into place, and the ends are
+// residual (1074 MB) 157 us, 6.84 TB/s, the rate of a plain copy, and 147 us to f8 with scales
+// (940 MB, 6.4 TB/s); cut rows, 32768 x 1001 bf16, 52 us (5.1 TB/s: the weights are shifted into place, and the ends are
 // accesses of their own). With dropout the generator adds five
-// wide multiplies an element: 8192 x 4096 (268 MB) 50 us, 5.4 TB/s, the issue slots and the multiplier each
-// half busy. One token of 8192: 3.3 us a call, which is the launch.
+// wide multiplies an element: 8192 x 4096 (268 MB) 48 us, 5.6 TB/s, the issue slots, the multiplier and the
+// ALU each over half busy. One token of 8192: 3.1 to 3.7 us a call, which is the launch (2.3 in a captured graph).
 template <int DT, int K, int DROP, bool CUT>
 __global__ void __launch_bounds__(K == 1 ? 1024 : 512) norm_row_kernel(const __grid_constant__ NormPlan p, int weight_whole) {
   constexpr int W = kVec<DT>, EB = 16 / W;
