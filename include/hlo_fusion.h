@@ -582,6 +582,99 @@ hlo_status hlo_logits_process(const hlo_view* logits, const void* logits_ptr, co
                               void* out_ptr, int32_t* token, void* stream);
 
 /* ------------------------------------------------------------------------------------------------
+ * A decoder's paged cache of keys and values: appending to it (with the rotary positions on the way), the attention
+ * that reads it, and the acceptance of a drafted branch. The conventions of the layer operators above hold.
+ *
+ * hlo_cache -- the cache of one layer, and which of its pages belong to which sequence:
+ *   k, k_ptr, v, v_ptr     [pages, page_size, kv, dim], the same dims and element type (f32 / bf16 / f16 /
+ *                          f8E4M3FN) with strides of their own (pages whose heads come first are a transposed view);
+ *                          for hlo_tree_accept also [layers, pages, page_size, kv, dim]. page_size is any number >= 1.
+ *                          pages * page_size may exceed 2^31; max_pages * page_size must not reach it.
+ *   k_scale, v_scale       an f8E4M3FN code stands for code * scale (finite, > 0). 1 for the other types
+ *   table, table_ptr       s32 [batch, max_pages]: entry i of sequence b lies in page table[b][i / page_size], at place
+ *                          i % page_size. A page outside 0 .. pages - 1 is not there: nothing is written to it, its
+ *                          entries are seen by nobody. So are entries from max_pages * page_size on. Sequences may share
+ *                          pages that are only read (a common prompt); a page that a call writes belongs to one sequence
+ *   lengths                s32[batch]: entries before the new tokens, clamped to 0 .. max_pages * page_size. New token t of
+ *                          sequence b is entry lengths[b] + t. No call changes the lengths
+ * The new tokens of a call are [batch, seq]; counts (s32[batch], clamped to 0 .. seq, or NULL: seq) says how many of them
+ * each sequence has. Rows of outputs behind them are left as they were, and nothing of them is read but the rows' memory.
+ * ---------------------------------------------------------------------------------------------- */
+typedef struct {
+  hlo_view k, v;
+  void *k_ptr, *v_ptr;
+  double k_scale, v_scale;
+  hlo_view table;
+  const int32_t* table_ptr;
+  const int32_t* lengths;
+} hlo_cache;
+
+/* ------------------------------------------------------------------------------------------------
+ * hlo_cache_append -- for every new token t < counts[b]:
+ *   K[entry lengths[b] + t] = code(rot(k[b, t])),  V[entry lengths[b] + t] = code(v[b, t]),  q_out[b, t] = rot(q[b, t])
+ * rot is hlo_rotary's rotation (scale, pairs and angles as there; not inverse) by positions[b, t], or by the entry's
+ * number without positions. code rounds to the cache's type, to nearest even; in f8E4M3FN it is x / scale, rounded and
+ * saturated at 448 (a NaN stays a NaN).
+ *   k, k_ptr, v, v_ptr       [batch, seq, kv, dim], f32 / bf16 / f16; the cache's type, or the cache is f8E4M3FN
+ *   q, ... q_out_ptr         both NULL, or [batch, seq, heads, dim] of k's type; q_out may be exactly q
+ *   positions, positions_ptr NULL, or s32 [batch, seq]
+ *   turns, n_pairs           as in hlo_rotary; n_pairs 0 rotates nothing (q_out is then q * 1)
+ * Entries outside the cache or in pages that are not there are dropped (q_out is written all the same).
+ * ---------------------------------------------------------------------------------------------- */
+hlo_status hlo_cache_append(const hlo_cache* cache, const hlo_view* k, const void* k_ptr, const hlo_view* v, const void* v_ptr,
+                            const hlo_view* q, const void* q_ptr, const hlo_view* q_out, void* q_out_ptr,
+                            const int32_t* counts, const hlo_view* positions, const int32_t* positions_ptr,
+                            const uint64_t* turns, int32_t n_pairs, int32_t interleaved, double scale, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * hlo_cache_attention -- attention of the new tokens over the cache (which holds their own entries already). Query head
+ * h reads key head h / (heads / kv). For token t < counts[b]:
+ *   s[i] = scale * q[b, t, h] . K[i]        over the entries i that t sees: i < lengths[b], and entry lengths[b] + u of the
+ *                                           new tokens u < counts[b] where bit u of mask[b, t] is set (without mask: u <= t)
+ *   out[b, t, h] = sum_i softmax(s)[i] V[i],  lse[b, t, h] = ln sum_i exp(s[i])
+ * A token that sees nothing gets 0, and -inf. Keys and values (NaN and infinities included) that a token does not see
+ * leave its row as it is; an infinite or NaN element of a value that it sees makes its element of out infinite or NaN.
+ * s, the softmax's sums and out's sums are f32. With 16-bit q the weights are rounded to 16 bits (q's type; f16 over an
+ * f8E4M3FN cache) before they multiply the values: the error, half a step of a weight, is random over the entries.
+ *   q, q_ptr, out, out_ptr   [batch, seq, heads, dim], f32 / bf16 / f16, one type: the cache's, or the cache is
+ *                            f8E4M3FN; heads is a multiple of kv, dim <= 256. out may be exactly q
+ *   mask, mask_ptr           NULL, or s32 [batch, seq, ceil(seq / 32)]: bit u % 32 of word u / 32 lets t see new token u
+ *                            (stride 0 repeats one tree); bits of u >= counts[b] do not matter
+ *   scale                    finite, > 0
+ *   lse                      NULL, or f32 [batch, seq, heads], contiguous
+ *   workspace                at least hlo_cache_attention_workspace_size bytes, 16-byte aligned; contents on entry do not
+ *                            matter; not shared by calls that overlap in time. The size depends on the device's number
+ *                            of SMs (that of the current device), and not on lengths
+ * hlo_tree_mask writes, to HOST memory, the mask [n, ceil(n / 32)] and the depths [n] (NULL: not wanted) of a tree: node c
+ * sees itself and the nodes between it and its root. parents[c] is in -1 (a root) .. c - 1.
+ * ---------------------------------------------------------------------------------------------- */
+hlo_status hlo_cache_attention(const hlo_cache* cache, const hlo_view* q, const void* q_ptr, const int32_t* counts,
+                               const hlo_view* mask, const int32_t* mask_ptr, double scale, const hlo_view* out, void* out_ptr,
+                               float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+size_t hlo_cache_attention_workspace_size(int64_t batch, int64_t seq, int64_t heads, int64_t kv, int64_t dim);
+
+hlo_status hlo_tree_mask(const int32_t* parents, int32_t n, uint32_t* mask, int32_t* depths);
+
+/* ------------------------------------------------------------------------------------------------
+ * hlo_tree_accept -- which of a tree's drafted tokens the model itself would have chosen. Node 0 is the last known token;
+ * from node c the walk goes to the first child d (c < d < counts[b], parents[b, d] = c) with tokens[b, d] = picks[b, c], and
+ * ends where there is none or picks[b, c] < 0:
+ *   path[b, :]   the nodes walked, node 0 first; -1 behind them      (s32 [batch, seq])
+ *   accepted[b]  their number (0 where counts[b] = 0)                (s32[batch])
+ *   next[b]      picks[b, last node of the path], the token after them; -1 where accepted[b] = 0
+ * and, with a cache, entry lengths[b] + path[b, i] moves to lengths[b] + i (K and V, all layers), so that the sequence
+ * goes on from length lengths[b] + accepted[b]. Entries to or from pages that are not there stay.
+ *   tokens, parents, picks   s32 [batch, seq] views; stride 0 over the batch repeats one row. picks: each node's greedy token
+ *                            (hlo_logits_process); tokens[b, 0] and parents[b, 0] do not matter
+ *   cache                    NULL, or as above; its scales do not matter
+ *   seq                      at most 4096
+ * ---------------------------------------------------------------------------------------------- */
+hlo_status hlo_tree_accept(const hlo_view* tokens, const int32_t* tokens_ptr, const hlo_view* parents, const int32_t* parents_ptr,
+                           const hlo_view* picks, const int32_t* picks_ptr, const int32_t* counts, const hlo_cache* cache,
+                           const hlo_view* path, int32_t* path_ptr, int32_t* accepted, int32_t* next, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
  * Fault injection for tests of the error path (no counterpart in the pages: the library's own test
  * support). When the environment variable HLOFUSION_FAULT holds an entry point's name (for example
  * "hlo_transpose_fusion") or "all", that entry point validates its arguments as usual and then returns

@@ -38,7 +38,8 @@ EXPORTS = ("hlo_reduce_fusion", "hlo_reduce_fusion_noalloc", "hlo_reduce_workspa
            "hlo_layout_convert",
            "hlo_quant_fusion", "hlo_quant_binary", "hlo_quant_broadcast_in_dim", "hlo_quant_reshape",
            "hlo_reduce_max_argmax", "hlo_rms_norm", "hlo_rms_norm_backward", "hlo_rms_norm_workspace_size",
-           "hlo_dropout", "hlo_rotary", "hlo_rotary_turns", "hlo_logits_process", "hlo_device_faults",
+           "hlo_dropout", "hlo_rotary", "hlo_rotary_turns", "hlo_logits_process", "hlo_cache_append",
+           "hlo_cache_attention", "hlo_cache_attention_workspace_size", "hlo_tree_mask", "hlo_tree_accept", "hlo_device_faults",
            "hlo_selftest_bounded_wait", "hlo_jit_kernels", "hlo_jit_source", "hlo_last_error", "hlo_version")
 QUANT_BINARY_OPS = {"add": 0, "divide": 1, "maximum": 2, "minimum": 3, "multiply": 4}
 
@@ -152,6 +153,10 @@ def lib() -> ctypes.CDLL:
             h.hlo_rotary_turns.restype = ctypes.c_int
             h.hlo_logits_process.argtypes = [V, vp, V, vp, V, vp, vp, vp, vp, vp, vp, V, vp, V, vp, vp, vp]
             h.hlo_logits_process.restype = ctypes.c_int
+            h.hlo_cache_attention_workspace_size.argtypes = [i64, i64, i64, i64, i64]
+            h.hlo_cache_attention_workspace_size.restype = ctypes.c_size_t
+            h.hlo_tree_mask.argtypes = [vp, i32, vp, vp]
+            h.hlo_tree_mask.restype = ctypes.c_int
             h.hlo_device_faults.argtypes = [P(ctypes.c_uint32), i32]
             h.hlo_device_faults.restype = ctypes.c_int
             h.hlo_selftest_bounded_wait.argtypes = [vp]
@@ -561,3 +566,63 @@ def logits_process(logits, out=None, bias=None, history=None, lengths=None, prom
     if status:
         _check(status)
     return out if out is not None else token
+
+
+# A paged cache is a pair of tensors k_cache, v_cache [pages, page_size, kv, dim] (any strides, last 1), `pages`, s32 [batch,
+# max_pages], and `lengths`, s32 [batch]: entry i of sequence b lies in page pages[b, i // page_size] at place i %
+# page_size, and new token t becomes entry lengths[b] + t. counts, s32 [batch]: how many new tokens each sequence has.
+def cache_append(k, v, k_cache, v_cache, pages, lengths, counts=None, q=None, q_out=None, positions=None, turns=None,
+                 interleaved=False, scale=1.0, k_scale=1.0, v_scale=1.0, n_pairs=None, stream=None):
+    """hlo_cache_append: writes the new tokens' keys [batch, seq, kv, dim], turned by their positions (their entries' numbers
+    without positions), and values into the cache, and the turned queries into q_out. An f8E4M3FN cache holds x / k_scale
+    and x / v_scale. turns as in rotary(); without them nothing turns."""
+    call = _call or _load_call()
+    status = call.cache_append(k, v, k_cache, v_cache, pages, lengths, counts, q, q_out, positions, turns, n_pairs, interleaved, scale, k_scale, v_scale, None if stream is None else _stream(stream))
+    if status:
+        _check(status)
+    return q_out
+
+
+def cache_attention_workspace_size(batch: int, seq: int, heads: int, kv: int, dim: int) -> int:
+    """hlo_cache_attention_workspace_size: scratch bytes of cache_attention on the current device, for q [batch, seq, heads,
+    dim] over a cache of kv heads."""
+    return int(lib().hlo_cache_attention_workspace_size(int(batch), int(seq), int(heads), int(kv), int(dim)))
+
+
+def cache_attention(q, k_cache, v_cache, pages, lengths, out, counts=None, mask=None, scale=None, k_scale=1.0, v_scale=1.0,
+                    lse=None, workspace=None, workspace_bytes=None, stream=None):
+    """hlo_cache_attention: out = softmax(scale q K^T) V for the new tokens q [batch, seq, heads, dim], whose own entries the
+    cache holds already. A token sees the entries before lengths[b], and of the new ones those of its mask's bits (s32
+    [batch, seq, ceil(seq / 32)], or one tree for all: see tree_mask), without a mask those up to itself. scale None: 1 / sqrt(dim).
+    lse: f32 [batch, seq, heads], the logarithms of the softmax's sums. The workspace is a contiguous tensor on the
+    GPU, or a raw address with workspace_bytes."""
+    call = _call or _load_call()
+    status = call.cache_attention(q, k_cache, v_cache, pages, lengths, out, counts, mask, scale, k_scale, v_scale, lse, workspace, workspace_bytes, None if stream is None else _stream(stream))
+    if status:
+        _check(status)
+    return out
+
+
+def tree_mask(parents):
+    """hlo_tree_mask: (mask, depths) of a tree as numpy arrays, int32 [n, ceil(n / 32)] and [n], for cache_attention's mask and
+    the positions lengths + depths. parents: for each node an earlier one, or -1."""
+    up = np.ascontiguousarray(parents, dtype=np.int32)
+    if up.ndim != 1:
+        raise HloError(STATUS_INVALID_ARG, f"tree_mask: parents of rank {up.ndim}, expected 1")
+    n = up.shape[0]
+    mask, depths = np.zeros((n, (n + 31) // 32), dtype=np.int32), np.zeros(n, dtype=np.int32)
+    _check(lib().hlo_tree_mask(up.ctypes.data, n, mask.ctypes.data, depths.ctypes.data))
+    return mask, depths
+
+
+def tree_accept(tokens, parents, picks, path, accepted, next_token, counts=None, k_cache=None, v_cache=None, pages=None,
+                lengths=None, stream=None):
+    """hlo_tree_accept: the nodes of a drafted tree (s32 [batch, seq]; parents may be one row for all) that the model's greedy
+    tokens `picks` choose from node 0 on: path, their number accepted, and the token after them, next_token. With a cache (of
+    one layer, or with a dimension of layers first) their entries move together, so that lengths + accepted is the
+    sequence's new length."""
+    call = _call or _load_call()
+    status = call.tree_accept(tokens, parents, picks, path, accepted, next_token, counts, k_cache, v_cache, pages, lengths, None if stream is None else _stream(stream))
+    if status:
+        _check(status)
+    return path

@@ -1,5 +1,5 @@
 // _hlocall: the marshalling of the layer entry points (hlo_rms_norm, hlo_rms_norm_backward, hlo_dropout, hlo_rotary,
-// hlo_logits_process) as a CPython extension. A serving step makes hundreds of these calls on a few
+// hlo_logits_process, hlo_cache_append, hlo_cache_attention, hlo_tree_accept) as a CPython extension. A serving step makes hundreds of these calls on a few
 // kilobytes each, where building the descriptors in Python costs more than the kernel (measured on the
 // GPU's host for one token's norm: 11 us a call through ctypes, of which the launch is about 2); here the
 // tensors' own fields are read. Every function takes its operands by position and returns the hlo_status;
@@ -11,6 +11,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstring>
 #include <exception>
@@ -341,6 +342,112 @@ PyObject* logits_process(PyObject*, PyObject* const* a, Py_ssize_t n) {
        a[1], a[10]);
 }
 
+// k_cache, v_cache, pages, lengths and the scales (NULL: 1) as one cache of `batch` sequences; its views stay in `o`.
+struct CacheArgs {
+  Operand k, v, table;
+  hlo_cache c;
+};
+bool read_cache(PyObject* k, PyObject* v, PyObject* pages, PyObject* lengths, PyObject* k_scale, PyObject* v_scale, int64_t batch,
+                CacheArgs* o) {
+  void* len;
+  if (!read(k, &o->k) || !read(v, &o->v) || !read(pages, &o->table) || !read_vector(lengths, batch, HLO_S32, "lengths", &len)) return false;
+  if (!o->k.given || !o->v.given || !o->table.given) return refuse("k_cache, v_cache and pages are wanted");
+  o->c.k = o->k.v;
+  o->c.v = o->v.v;
+  o->c.k_ptr = o->k.p;
+  o->c.v_ptr = o->v.p;
+  o->c.table = o->table.v;
+  o->c.table_ptr = static_cast<int32_t*>(o->table.p);
+  o->c.lengths = static_cast<int32_t*>(len);
+  o->c.k_scale = k_scale ? PyFloat_AsDouble(k_scale) : 1.0;
+  o->c.v_scale = v_scale ? PyFloat_AsDouble(v_scale) : 1.0;
+  return !PyErr_Occurred();
+}
+int64_t first_of(const Operand& o) { return o.given && o.v.rank > 0 ? o.v.dims[0] : 0; }
+
+// rotary's turns: their address, and the number of pairs (`wanted`, None: turns' count, the most that is taken)
+bool read_turns(PyObject* t, PyObject* wanted, const char* who, void** turns, int32_t* count) {
+  int64_t pairs = -1;
+  int32_t words = kWords;
+  if (!read_vector(t, &pairs, &words, "turns", turns)) return false;
+  if (t == Py_None) pairs = 0;
+  if (wanted != Py_None) {
+    const int64_t n = PyLong_AsLongLong(wanted);
+    if (PyErr_Occurred()) return false;
+    if (pairs >= 0 && n > pairs) return refuse("%s: %lld pairs, but turns has %lld", who, (long long)n, (long long)pairs);
+    pairs = n;
+  }
+  *count = (int32_t)(pairs > INT32_MAX ? INT32_MAX : pairs < -1 ? -1 : pairs);  // -1 is refused
+  return true;
+}
+
+// k, v, k_cache, v_cache, pages, lengths, counts, q, q_out, positions, turns, n_pairs, interleaved, scale, k_scale, v_scale, stream
+PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 17)) return nullptr;
+  Operand k, v, q, qout, pos;
+  CacheArgs c;
+  if (!read(a[0], &k) || !read(a[1], &v) || !read(a[7], &q) || !read(a[8], &qout) || !read(a[9], &pos)) return nullptr;
+  const int64_t b = first_of(k);
+  void *counts, *turns, *stream;
+  int32_t pairs;
+  if (!read_cache(a[2], a[3], a[4], a[5], a[14], a[15], b, &c) || !read_vector(a[6], b, HLO_S32, "counts", &counts) ||
+      !read_turns(a[10], a[11], "cache_append", &turns, &pairs) || !read_stream(a[16], &stream))
+    return nullptr;
+  const double scale = PyFloat_AsDouble(a[13]);
+  const int inter = PyObject_IsTrue(a[12]);
+  if (PyErr_Occurred()) return nullptr;
+  CALL(hlo_cache_append(&c.c, k.view(), k.p, v.view(), v.p, q.view(), q.p, qout.view(), qout.p, static_cast<int32_t*>(counts), pos.view(),
+                        static_cast<int32_t*>(pos.p), static_cast<uint64_t*>(turns), pairs, inter, scale, stream),
+       a[2], a[3], a[8]);
+}
+
+// q, k_cache, v_cache, pages, lengths, out, counts, mask, scale (None: 1 / sqrt(dim)), k_scale, v_scale, lse, workspace, workspace_bytes, stream
+PyObject* cache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 15)) return nullptr;
+  Operand q, out, mask;
+  CacheArgs c;
+  if (!read(a[0], &q) || !read(a[5], &out) || !read(a[7], &mask)) return nullptr;
+  const int64_t b = first_of(q);
+  if (mask.given && mask.v.rank == 2) {  // one tree for every sequence
+    mask.v.rank = 3;
+    for (int d = 2; d > 0; --d) mask.v.dims[d] = mask.v.dims[d - 1], mask.v.strides[d] = mask.v.strides[d - 1];
+    mask.v.dims[0] = b;
+    mask.v.strides[0] = 0;
+  }
+  void *counts, *lse, *ws, *stream;
+  size_t bytes;
+  if (!read_cache(a[1], a[2], a[3], a[4], a[9], a[10], b, &c) || !read_vector(a[6], b, HLO_S32, "counts", &counts) ||
+      !read_vector(a[11], q.given ? rows_of(q.v) : 0, HLO_F32, "lse", &lse) || !read_scratch(a[12], a[13], &ws, &bytes) ||
+      !read_stream(a[14], &stream))
+    return nullptr;
+  const int64_t dim = q.given ? last_of(q.v) : 0;
+  const double scale = a[8] == Py_None ? 1.0 / std::sqrt((double)(dim > 0 ? dim : 1)) : PyFloat_AsDouble(a[8]);
+  if (PyErr_Occurred()) return nullptr;
+  CALL(hlo_cache_attention(&c.c, q.view(), q.p, static_cast<int32_t*>(counts), mask.view(), static_cast<int32_t*>(mask.p), scale, out.view(),
+                           out.p, static_cast<float*>(lse), ws, bytes, stream),
+       a[5], a[11], a[12]);
+}
+
+// tokens, parents, picks, path, accepted, next, counts, k_cache, v_cache, pages, lengths, stream
+PyObject* tree_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 12)) return nullptr;
+  Operand tokens, parents, picks, path;
+  CacheArgs c;
+  if (!read(a[0], &tokens) || !read(a[1], &parents) || !read(a[2], &picks) || !read(a[3], &path)) return nullptr;
+  const int64_t b = first_of(tokens);
+  repeat_row(&parents, b);
+  void *accepted, *next, *counts, *stream;
+  const bool with = a[7] != Py_None || a[8] != Py_None;
+  if (!read_vector(a[4], b, HLO_S32, "accepted", &accepted) || !read_vector(a[5], b, HLO_S32, "next", &next) ||
+      !read_vector(a[6], b, HLO_S32, "counts", &counts) || (with && !read_cache(a[7], a[8], a[9], a[10], nullptr, nullptr, b, &c)) ||
+      !read_stream(a[11], &stream))
+    return nullptr;
+  CALL(hlo_tree_accept(tokens.view(), static_cast<int32_t*>(tokens.p), parents.view(), static_cast<int32_t*>(parents.p), picks.view(),
+                       static_cast<int32_t*>(picks.p), static_cast<int32_t*>(counts), with ? &c.c : nullptr, path.view(),
+                       static_cast<int32_t*>(path.p), static_cast<int32_t*>(accepted), static_cast<int32_t*>(next), stream),
+       a[3], a[4], a[5], a[7], a[8]);
+}
+
 // DeviceView, HloError, Dropout and Quant
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count_is(n, 4)) return nullptr;
@@ -357,6 +464,9 @@ PyMethodDef methods[] = {{"setup", (PyCFunction)(void (*)(void))setup, METH_FAST
                          {"rms_norm_backward", (PyCFunction)(void (*)(void))rms_norm_backward, METH_FASTCALL, nullptr},
                          {"dropout", (PyCFunction)(void (*)(void))dropout, METH_FASTCALL, nullptr},
                          {"rotary", (PyCFunction)(void (*)(void))rotary, METH_FASTCALL, nullptr},
+                         {"cache_append", (PyCFunction)(void (*)(void))cache_append, METH_FASTCALL, nullptr},
+                         {"cache_attention", (PyCFunction)(void (*)(void))cache_attention, METH_FASTCALL, nullptr},
+                         {"tree_accept", (PyCFunction)(void (*)(void))tree_accept, METH_FASTCALL, nullptr},
                          {"logits_process", (PyCFunction)(void (*)(void))logits_process, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hlocall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
