@@ -237,10 +237,26 @@ static cudaError_t run_any(AttendPlan& p, void* ws, cudaStream_t s) {
   return e == cudaSuccess ? launch_attend_join(p, kAnyRows, p.dim, blocks, s) : e;
 }
 
-size_t attend_workspace(int64_t batch, int64_t seq, int64_t heads, int64_t kv, int64_t dim) {
-  return attend_layout(nullptr, nullptr, any_blocks(dim), kAnyRows, (int)dim);
+// Whether entries can be copied 16 bytes at a time.
+static bool aligned_entries(const AttendPlan& p) {
+  const int64_t eb = p.f8 ? 1 : 2;
+  uintptr_t bits = (uintptr_t)p.k | (uintptr_t)p.v | (uintptr_t)(p.dim * eb);
+  for (int d = 0; d < 3; ++d) bits |= (uintptr_t)(p.k_stride[d] * eb) | (uintptr_t)(p.v_stride[d] * eb);
+  return bits % 16 == 0;
 }
 
-cudaError_t launch_attend(AttendPlan p, void* ws, cudaStream_t s) { return run_any(p, ws, s); }
+static int padded_columns(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+size_t attend_workspace(int64_t batch, int64_t seq, int64_t heads, int64_t kv, int64_t dim) {
+  const size_t any = attend_layout(nullptr, nullptr, any_blocks(dim), kAnyRows, (int)dim);
+  const int rows = seq * (heads / kv) > 16 && dim <= 128 ? 32 : 16;
+  return std::max(any, attend_layout(nullptr, nullptr, 2 * device_sm_count(), rows, padded_columns(dim)));
+}
+
+cudaError_t launch_attend(AttendPlan p, void* ws, cudaStream_t s) {
+  if (p.dt == F32 || !aligned_entries(p)) return run_any(p, ws, s);
+  if (p.dt == BF16) return p.f8 ? launch_attend_rows_bf16_f8(p, ws, s) : launch_attend_rows_bf16(p, ws, s);
+  return p.f8 ? launch_attend_rows_f16_f8(p, ws, s) : launch_attend_rows_f16(p, ws, s);
+}
 
 }  // namespace hlo
