@@ -1,0 +1,592 @@
+// Attention over a paged cache for many rows a key head (prompts, large trees), on the fifth-generation tensor cores.
+//
+// A block has 256 rows of one key head as two tiles of 128, and streams the entries in tiles of 128 through a ring in
+// shared memory; each tile is multiplied with both. Sixteen warps in four groups:
+//   groups 0, 1   the softmax of tile 0 and tile 1, a row a thread: scores from tensor memory into registers, running maximum
+//                 and sum, weights back into tensor memory in the scores' place, where the second product takes them from
+//   group 2       requests queries, keys and values (pages of any size, 16 bytes a copy, in the products' 128-byte swizzle)
+//   group 3       one thread issues the products: while one tile's softmax runs, the other tile's products do
+// Tensor memory: scores 128 columns and outputs DP columns for each tile. The maximum moves only where a score exceeds it
+// by 2^8; then the group rescales its outputs there. No product of its tile runs then: the scores' arrival implies that the
+// product before has ended, and the next one waits for the weights.
+// Order of the products: S0(0) S1(0) | V0(0) S0(1) V1(0) S1(1) | ... : a tile's next scores follow its weights' product, so
+// they may overwrite the weights.
+//
+// Infinite and NaN values in tiles that a mask cuts are cleared by the copying warps before the products see them, and added
+// again for the rows that see them (cleared_values). Every wait is bounded: when one runs out, the block records the fault,
+// stops, waits for its copies and products, frees its tensor memory and leaves its rows unwritten.
+#pragma once
+#include "async_copy.cuh"
+#include "attend_mma.cuh"
+
+namespace hlo {
+
+template <int DP>
+struct TileShape {
+  static constexpr int kRows = 256, kKeys = 128;
+  static constexpr int kPanel = 128 * 128;                // 128 rows of 64 16-bit elements
+  static constexpr int kTile = kPanel * (DP / 64);        // queries of a tile, or a slot of the ring
+  static constexpr int kSlots = DP == 64 ? 8 : 4;
+  static constexpr int kSmem = (2 + kSlots) * kTile + 1024;  // and what rounding the base up to 1024 takes
+  static constexpr int kThreads = 512;
+  static constexpr int kScores = 128;                     // columns; tile s: scores at 128 s, outputs at 256 + DP s
+};
+
+struct TileBarriers {
+  uint64_t kv_full[8], kv_empty[8], q_full, q_empty, s_full[2], p_full[2], o_full[2], drained;
+};
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tile_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tile_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tile_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// d (+)= a b. Operands in shared memory by descriptor; a also in tensor memory.
+__device__ __forceinline__ void tile_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add) {
+  asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b),
+               "r"(what), "r"((uint32_t)add)
+               : "memory");
+}
+__device__ __forceinline__ void tile_mma_weights(uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool add) {
+  asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a), "l"(b),
+               "r"(what), "r"((uint32_t)add)
+               : "memory");
+}
+
+// A matrix in panels of 64 elements (128 bytes, swizzled) by rows: groups of 8 rows 1024 bytes apart, panels `panel` apart
+// (used where the rows are the products' inner dimension).
+__device__ __forceinline__ uint64_t tile_descriptor(uint32_t at, uint32_t panel) {
+  return (uint64_t)((at >> 4) & 0x3FFF) | (uint64_t)((panel >> 4) & 0x3FFF) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
+
+__device__ __forceinline__ void tile_load32(uint32_t (&r)[32], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+        "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tile_store32(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tile_store16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at), "r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+      "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tile_wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tile_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Which of the 32 entries from `e` on a row's token sees (bit i: entry e + i), by the mask alone.
+__device__ __forceinline__ uint32_t tile_sees(const AttendPlan& p, const AttendItem& it, int token, int e) {
+  const int u = e - it.length;  // the first one among the new tokens
+  if (!p.mask) {
+    const int n = token + 1 - u;  // it sees the first n
+    return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1;
+  }
+  if (u <= -32) return 0xFFFFFFFFu;
+  const uint32_t* const row = p.mask + it.b * p.mask_stride[0] + token * p.mask_stride[1];
+  const int words = (p.m.seq + 31) >> 5;
+  if (u < 0) return (row[0] << -u) | ((1u << -u) - 1);
+  const int k = u >> 5;
+  const uint32_t lo = k < words ? row[k] : 0u, hi = k + 1 < words ? row[k + 1] : 0u;
+  return __funnelshift_r(lo, hi, u & 31);
+}
+
+template <int DT, bool F8, int DP>
+__global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_constant__ AttendPlan p, bool same_strides, bool q_vectors, bool out_vectors) {
+  using S = TileShape<DP>;
+  constexpr bool BF = DT == BF16 && !F8;  // the products' type
+  constexpr int SLOTS = S::kSlots, CH = DP / 8;  // 16-byte chunks of a row
+  extern __shared__ char raw[];
+  __shared__ __align__(8) TileBarriers bars;
+  __shared__ AttendScan scan;
+  __shared__ uint32_t tmem_at, there[8][4];  // there: which of a tile's entries exist
+  __shared__ float row_unit[2][S::kRows];    // a row's scores in units of a factor 2 (bf16 queries over codes)
+  __shared__ int cleared[4];                 // the item whose values were cleared, by the item's number mod 4
+  __shared__ volatile int dead;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  char* const base = raw + ((1024 - (attend_smem(raw) & 1023)) & 1023);
+  const uint32_t q_at = attend_smem(base), ring_at = q_at + 2 * S::kTile;
+  const auto bar = [&](const uint64_t& b) { return smem_addr(&b); };
+  if (tid == 0) {
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(bar(bars.kv_full[i]), 128);
+      mbar_init(bar(bars.kv_empty[i]), 1);
+    }
+    mbar_init(bar(bars.q_full), 128);
+    mbar_init(bar(bars.q_empty), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(bars.s_full[s]), 1);
+      mbar_init(bar(bars.p_full[s]), 128);
+      mbar_init(bar(bars.o_full[s]), 1);
+    }
+    mbar_init(bar(bars.drained), 1);
+    fence_mbar_init();
+    dead = 0;
+  }
+  if (tid < 4) cleared[tid] = -1;
+  wait_for_last();
+  if (w == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(attend_smem(&tmem_at)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tile_fence_before();
+  }
+  AttendShare share = attend_share<S::kRows, S::kKeys, S::kThreads>(p, scan);
+  __syncthreads();
+  tile_fence_after();
+  const uint32_t tmem = tmem_at;
+  int4 begun = make_int4(-1, 0, 0, 0);
+  int item = 0;
+  uint32_t tile0 = 0;  // tiles of entries before this stretch's
+  // Waits for a phase; false when the wait ran out here or in another warp.
+  const auto wait = [&](const uint64_t& b, uint32_t parity) {
+    if (mbar_wait(bar(b), parity & 1)) return !dead;
+    dead = 1;
+    record_fault(kFaultCopyTimeout);
+    return false;
+  };
+  // The same for a whole warp.
+  const auto wait_all = [&](const uint64_t& b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
+  // What a stretch of a tile is to every group.
+  struct Part {
+    int first, end, tiles, rows, units, take;
+    int64_t row0;
+  };
+  const auto part_of = [&](const AttendShare& s) {
+    Part a;
+    a.units = attend_units<S::kRows, S::kKeys>(p, s.it, s.it.tile);
+    a.take = (int)min(s.left, (int64_t)(a.units - s.unit));
+    a.row0 = (int64_t)s.it.tile * S::kRows;
+    a.rows = (int)min((int64_t)S::kRows, (int64_t)s.it.count * p.group - a.row0);
+    a.first = s.unit * S::kKeys;
+    a.end = min(s.it.total, a.first + a.take * S::kKeys);
+    a.tiles = (max(0, a.end - a.first) + S::kKeys - 1) / S::kKeys;
+    return a;
+  };
+  const auto advance = [&](AttendShare& s, const Part& a) {
+    s.left -= a.take;
+    s.at += a.take;
+    s.unit += a.take;
+    ++item;
+    tile0 += a.tiles;
+    if (s.left > 0 && s.unit == a.units) {
+      s.unit = 0;
+      if (!attend_next<S::kRows>(p, s.it)) s.left = 0;
+    }
+  };
+
+  if (w < 8) {
+    // ---- the softmax ----------------------------------------------------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    const int s = w >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)(32 * (w & 3)) << 16;
+    const uint32_t scores = tmem + lanes + S::kScores * s, outs = tmem + lanes + 256 + DP * s;
+    uint32_t seen_scores = 0, seen_outs = 0;  // phases
+    while (share.left > 0) {
+      const Part a = part_of(share);
+      const AttendItem& it = share.it;
+      const bool live = a.rows > 128 * s;
+      if (live) {
+        const int row = 128 * s + r;
+        const bool mine = row < a.rows;
+        const AttendRow at = attend_row(p, it, a.row0 + row);
+        float unit = p.score_scale, top = __int_as_float(0xFF800000), sum = 0.0f;
+        for (int j = 0; j < a.tiles; ++j) {
+          if (!wait_all(bars.s_full[s], seen_scores)) goto done;
+          ++seen_scores;
+          tile_fence_after();
+          if (DT == BF16 && F8 && j == 0) unit = row_unit[item & 1][row];
+          uint32_t x[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tile_load32(x[c], scores + 32 * c);
+          const int e0 = a.first + j * S::kKeys;
+          uint32_t given[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) given[c] = there[(tile0 + j) & 7][c];
+          const bool hides = e0 + S::kKeys > it.length;
+          tile_wait_loads();
+          if (hides || (given[0] & given[1] & given[2] & given[3]) != 0xFFFFFFFFu) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t see = given[c];
+              if (hides && mine) see &= tile_sees(p, it, at.token, e0 + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(see >> i & 1)) x[c][i] = 0xFF800000u;
+            }
+          }
+          float m[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            m[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+            for (int i = 1; i < 32; ++i) m[c] = fmaxf(m[c], __uint_as_float(x[c][i]));
+          }
+          const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * unit;
+          if (__any_sync(0xffffffffu, most > top + 8.0f)) {
+            const float next = fmaxf(top, most);
+            const float f = next == top ? 1.0f : exp2_fast(top - next);
+            top = next;
+            sum *= f;
+            if (j > 0) {
+#pragma unroll
+              for (int c = 0; c < DP; c += 16) {
+                uint32_t o[16];
+                asm volatile(
+                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                    : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]), "=r"(o[8]), "=r"(o[9]),
+                      "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+                    : "r"(outs + c));
+                tile_wait_loads();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tile_store16(outs + c, o);
+              }
+            }
+          }
+          const float low = top == __int_as_float(0xFF800000) ? 0.0f : -top;
+          float2 total[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t weights[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])), make_float2(unit, unit),
+                                          make_float2(low, low));
+              const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+              total[(i >> 1) & 1] = __fadd2_rn(total[(i >> 1) & 1], e);
+              weights[i / 2] = pack_pair<BF>(e.x, e.y);
+            }
+            tile_store16(scores + 16 * c, weights);
+          }
+          sum += (total[0].x + total[0].y) + (total[1].x + total[1].y);
+          tile_wait_stores();
+          tile_fence_before();
+          mbar_arrive(bar(bars.p_full[s]));
+        }
+        if (a.tiles > 0) {
+          if (!wait_all(bars.o_full[s], seen_outs)) goto done;
+          ++seen_outs;
+          tile_fence_after();
+        }
+        const bool begins = share.unit == 0, whole = begins && a.take == a.units;
+        const int64_t slot = attend_slot(begins) * (int64_t)S::kRows + row;
+        const bool again = a.tiles > 0 && cleared[item & 3] == item;
+        const int from = it.length <= a.first ? a.first : a.first + (it.length - a.first) / S::kKeys * S::kKeys;
+        const float f = sum == 0.0f ? 0.0f : p.value_scale / sum;
+        uint16_t* const to = reinterpret_cast<uint16_t*>(p.out) + it.b * p.out_stride[0] + at.token * p.out_stride[1] + at.head * p.out_stride[2];
+        if (mine && whole && p.lse) p.lse[((int64_t)it.b * p.m.seq + at.token) * p.heads + at.head] = attend_lse(top, sum);
+        if (mine && !whole) p.stats[slot] = make_float2(top, sum);
+#pragma unroll 1
+        for (int c = 0; c < DP; c += 32) {
+          uint32_t o[32];
+          if (a.tiles > 0) {
+            tile_load32(o, outs + c);
+            tile_wait_loads();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0;
+          }
+          if (!mine) continue;
+          if (again) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c + i < p.dim) o[i] = __float_as_uint(__uint_as_float(o[i]) + cleared_values<F8>(p, it, at.token, from, a.end, c + i));
+          }
+          if (!whole) {
+            float4* const part = reinterpret_cast<float4*>(p.sums + slot * DP + c);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              part[i / 4] = make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+            continue;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float u = __uint_as_float(o[i + 2 * k]), v = __uint_as_float(o[i + 2 * k + 1]);
+              h[k] = sum == 0.0f ? 0u : pack_pair<DT == BF16>(u * f, v * f);
+            }
+            if (c + i >= p.dim) continue;
+            if (out_vectors) {
+              *reinterpret_cast<uint4*>(to + c + i) = make_uint4(h[0], h[1], h[2], h[3]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) to[c + i + k] = (uint16_t)(h[k / 2] >> (16 * (k & 1)));
+            }
+          }
+        }
+        if (begins && !whole) begun = make_int4(it.b, it.head, it.tile, (int)((share.at + a.units - 1) / share.per));
+        tile_fence_before();
+      }
+      advance(share, a);
+    }
+  } else if (w < 12) {
+    // ---- the copies -----------------------------------------------------------------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    constexpr int EB = F8 ? 1 : 2;
+    const int pw = w - 8, ch = lane % CH;
+    uint32_t slots = 0;                  // slots filled so far
+    uint32_t q_loads = 0;
+    // copies in flight: the barriers of the last two groups, and whether a group's values have to be looked through
+    uint32_t pending[2] = {0, 0}, look_through[2] = {0, 0};
+    int look_item[2] = {0, 0};
+    // chunk `c` of row r of a tile of 128 rows
+    const auto chunk_at = [&](uint32_t tile, int r, int c) { return tile + (c >> 3) * S::kPanel + r * 128 + ((c & 7) ^ (r & 7)) * 16; };
+    const auto land = [&](int k) {  // group k has come
+      if (!pending[k]) return;
+      if (look_through[k]) {
+        bool any = false;
+#pragma unroll 1
+        for (int i = 0; i < CH; ++i) {
+          const int r = 32 * pw + i * (32 / CH) + lane / CH;
+          any |= clear_vector<false, BF>(reinterpret_cast<uint4*>(base + (chunk_at(look_through[k], r, ch) - q_at)));
+        }
+        if (any) cleared[look_item[k] & 3] = look_item[k];
+      }
+      fence_proxy_async();
+      mbar_arrive(pending[k]);
+      pending[k] = 0;
+    };
+    const auto sent = [&](uint32_t b, uint32_t look, int number) {  // a group's copies have been requested
+      copy_commit();
+      copy_wait<2>();
+      land(0);
+      pending[0] = pending[1];
+      look_through[0] = look_through[1];
+      look_item[0] = look_item[1];
+      pending[1] = b;
+      look_through[1] = look;
+      look_item[1] = number;
+    };
+    const auto flush = [&] {
+      copy_wait<0>();
+      land(0);
+      land(1);
+    };
+    while (share.left > 0) {
+      const Part a = part_of(share);
+      const AttendItem& it = share.it;
+      if (a.tiles > 0) {
+        const int32_t* const table = p.m.table + it.b * p.m.table_stride;
+        int page = -1, place = 0;
+        const auto look = [&](int j) {
+          page = -1;
+          const int e = a.first + j * S::kKeys + 32 * pw + lane;
+          if (e < a.end) cache_place(p.m, table, e, &page, &place);
+        };
+        look(0);
+        // the queries
+        flush();
+        if (q_loads > 0 && !wait_all(bars.q_empty, q_loads - 1)) goto done;
+        ++q_loads;
+        const int halves = a.rows > 128 ? 2 : 1;
+#pragma unroll 1
+        for (int h = 0; h < halves; ++h) {
+          const int mine = 128 * h + 32 * pw + lane;
+          const AttendRow at = attend_row(p, it, a.row0 + mine);
+          const int64_t off = mine < a.rows ? it.b * p.q_stride[0] + at.token * p.q_stride[1] + at.head * p.q_stride[2] : -1;
+#pragma unroll 1
+          for (int i = 0; i < CH; ++i) {
+            const int e = i * (32 / CH) + lane / CH, r = 32 * pw + e;
+            const int64_t o = __shfl_sync(0xffffffffu, off, e);
+            const uint16_t* const from = reinterpret_cast<const uint16_t*>(p.q) + o + 8 * ch;
+            const bool ok = o >= 0 && 8 * ch < p.dim;
+            const uint32_t to = chunk_at(q_at + h * S::kTile, r, ch);
+            if (!(DT == BF16 && F8) && q_vectors) {
+              copy16(to, ok ? (const void*)from : p.q, ok);
+              continue;
+            }
+            uint32_t v[4] = {0, 0, 0, 0};
+            if (ok) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[k] = (uint32_t)from[2 * k] | (uint32_t)from[2 * k + 1] << 16;
+            }
+            if constexpr (DT == BF16 && F8) {  // as in attend_rows_kernel: a power of two takes the row's greatest element to 2^14
+              float most = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[k] << 16)), fabsf(__uint_as_float(v[k] & 0xFFFF0000u))));
+#pragma unroll
+              for (int x = 1; x < CH; x *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+              const int ex = max((int)(__float_as_uint(most) >> 23) - 127, -100);
+              const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[k] = pack_pair<false>(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xFFFF0000u) * up);
+              if (ch == 0) row_unit[item & 1][128 * h + r] = p.score_scale * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+            }
+            *reinterpret_cast<uint4*>(base + (to - q_at)) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+        sent(bar(bars.q_full), 0, item);
+        // keys and values
+        const char* const kbase = reinterpret_cast<const char*>(p.k) + it.head * p.k_stride[2] * EB;
+        const char* const vbase = reinterpret_cast<const char*>(p.v) + it.head * p.v_stride[2] * EB;
+        for (int j = 0; j < a.tiles; ++j) {
+          const uint32_t given = __ballot_sync(0xffffffffu, page >= 0);
+          if (lane == 0) there[(tile0 + j) & 7][pw] = given;
+          int64_t off[2];
+          off[0] = (page * p.k_stride[0] + place * p.k_stride[1]) * EB;
+          off[1] = same_strides ? off[0] : (page * p.v_stride[0] + place * p.v_stride[1]) * EB;
+          look(j + 1);
+          const bool hides = a.first + (j + 1) * S::kKeys > it.length;
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            const int slot = slots % SLOTS;
+            if (slots >= SLOTS && !wait_all(bars.kv_empty[slot], slots / SLOTS - 1)) goto done;
+            ++slots;
+            const uint32_t tile = ring_at + slot * S::kTile;
+            const char* const from = side ? vbase : kbase;
+            if constexpr (!F8) {
+              const bool column = 8 * ch < p.dim;
+#pragma unroll 4
+              for (int i = 0; i < CH; ++i) {
+                const int e = i * (32 / CH) + lane / CH;
+                const int64_t o = __shfl_sync(0xffffffffu, off[side], e);
+                const bool ok = column && (given >> e & 1);
+                copy16(chunk_at(tile, 32 * pw + e, ch), ok ? from + o + ch * 16 : from, ok);
+              }
+              sent(bar(bars.kv_full[slot]), side && hides ? tile : 0, item);
+            } else {
+              // 16 codes become two chunks of f16
+              constexpr int CC = DP / 16;
+              const int cc = lane % CC;
+              const bool column = 16 * cc < p.dim;
+              uint4 got[CC];
+#pragma unroll
+              for (int i = 0; i < CC; ++i) {
+                const int e = i * (32 / CC) + lane / CC;
+                const int64_t o = __shfl_sync(0xffffffffu, off[side], e);
+                got[i] = column && (given >> e & 1) ? *reinterpret_cast<const uint4*>(from + o + cc * 16) : make_uint4(0, 0, 0, 0);
+              }
+              flush();  // the queries
+              bool any = false;
+#pragma unroll
+              for (int i = 0; i < CC; ++i) {
+                const int r = 32 * pw + i * (32 / CC) + lane / CC;
+                uint32_t u[4] = {got[i].x, got[i].y, got[i].z, got[i].w};
+                if (side && hides) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) any |= clear_word<true, false>(u[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                  *reinterpret_cast<uint4*>(base + (chunk_at(tile, r, 2 * cc + k) - q_at)) =
+                      make_uint4(f16_of_codes(u[2 * k]), f16_of_codes(u[2 * k] >> 16), f16_of_codes(u[2 * k + 1]), f16_of_codes(u[2 * k + 1] >> 16));
+              }
+              if (any) cleared[item & 3] = item;
+              fence_proxy_async();
+              mbar_arrive(bar(bars.kv_full[slot]));
+            }
+          }
+        }
+      }
+      advance(share, a);
+    }
+    flush();
+  } else {
+    // ---- the products ---------------------------------------------------------------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (w == 12 && lane == 0) {
+      constexpr uint32_t type = BF ? 1 : 0;
+      constexpr uint32_t common = 1u << 4 | type << 7 | type << 10 | (128u >> 4) << 24;
+      constexpr uint32_t score_what = common | (uint32_t)(S::kKeys >> 3) << 17, out_what = common | 1u << 16 | (uint32_t)(DP >> 3) << 17;
+      uint32_t slots = 0, q_loads = 0, weights[2] = {0, 0};
+      bool ok = true;
+      while (ok && share.left > 0) {
+        const Part a = part_of(share);
+        const int live = a.rows > 128 ? 2 : 1;
+        if (a.tiles > 0) {
+          ok = wait(bars.q_full, q_loads++);
+          // the product of the weights with the values of slot number v, of which the first tile's begins the sum
+          const auto second = [&](int s, uint32_t v, bool add) {
+            ok = ok && wait(bars.p_full[s], weights[s]++) && wait(bars.kv_full[v % SLOTS], v / SLOTS);
+            if (!ok) return;
+            tile_fence_after();
+            const uint32_t at = ring_at + (v % SLOTS) * S::kTile;
+#pragma unroll
+            for (int k = 0; k < S::kKeys / 16; ++k)
+              tile_mma_weights(tmem + 256 + DP * s, tmem + S::kScores * s + 8 * k, tile_descriptor(at + k * 2048, S::kPanel), out_what, add || k > 0);
+          };
+          for (int j = 0; ok && j < a.tiles; ++j) {
+            const uint32_t k0 = slots + 2 * j;
+            ok = wait(bars.kv_full[k0 % SLOTS], k0 / SLOTS);
+            for (int s = 0; ok && s < live; ++s) {
+              if (j > 0) {
+                second(s, k0 - 1, j > 1);
+                if (ok && s == live - 1) tile_commit(bar(bars.kv_empty[(k0 - 1) % SLOTS]));
+              }
+              if (!ok) break;
+              tile_fence_after();
+              const uint32_t qa = q_at + s * S::kTile, ka = ring_at + (k0 % SLOTS) * S::kTile;
+#pragma unroll
+              for (int k = 0; k < DP / 16; ++k)
+                tile_mma(tmem + S::kScores * s, tile_descriptor(qa + (k >> 2) * S::kPanel + (k & 3) * 32, 16),
+                         tile_descriptor(ka + (k >> 2) * S::kPanel + (k & 3) * 32, 16), score_what, k > 0);
+              tile_commit(bar(bars.s_full[s]));
+            }
+            if (!ok) break;
+            tile_commit(bar(bars.kv_empty[k0 % SLOTS]));
+            if (j == a.tiles - 1) tile_commit(bar(bars.q_empty));
+          }
+          slots += 2 * a.tiles;
+          for (int s = 0; ok && s < live; ++s) {
+            second(s, slots - 1, a.tiles > 1);
+            if (ok) tile_commit(bar(bars.o_full[s]));
+          }
+          if (ok) tile_commit(bar(bars.kv_empty[(slots - 1) % SLOTS]));
+        }
+        advance(share, a);
+      }
+      // every product that was issued has ended before the memory is given back
+      tile_commit(bar(bars.drained));
+      mbar_wait(bar(bars.drained), 0);
+    }
+    __syncwarp();
+  }
+done:
+  copy_wait<0>();
+  if (tid == 0) p.shares[blockIdx.x] = begun;
+  tile_fence_before();
+  __syncthreads();
+  tile_fence_after();
+  if (w == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  allow_next();
+}
+
+template <int DT, bool F8, int DP>
+cudaError_t run_attend_tile(AttendPlan& p, void* ws, cudaStream_t s) {
+  using S = TileShape<DP>;
+  const int blocks = device_sm_count();
+  attend_layout(&p, ws, blocks, S::kRows, DP);
+  bool same = true, q_vectors = (uintptr_t)p.q % 16 == 0, out_vectors = (uintptr_t)p.out % 16 == 0;
+  for (int d = 0; d < 2; ++d) same = same && p.k_stride[d] == p.v_stride[d];
+  for (int d = 0; d < 3; ++d) {
+    q_vectors = q_vectors && p.q_stride[d] % 8 == 0;
+    out_vectors = out_vectors && p.out_stride[d] % 8 == 0;
+  }
+  const auto kernel = attend_tile_kernel<DT, F8, DP>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_after(kernel, dim3((unsigned)blocks), dim3(S::kThreads), S::kSmem, s, 1, p, same, q_vectors, out_vectors);
+  return e == cudaSuccess ? launch_attend_join(p, S::kRows, DP, blocks, s) : e;
+}
+
+}  // namespace hlo

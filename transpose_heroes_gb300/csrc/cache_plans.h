@@ -59,6 +59,11 @@ cudaError_t launch_attend_rows_bf16(AttendPlan& p, void* workspace, cudaStream_t
 cudaError_t launch_attend_rows_bf16_f8(AttendPlan& p, void* workspace, cudaStream_t s);
 cudaError_t launch_attend_rows_f16(AttendPlan& p, void* workspace, cudaStream_t s);
 cudaError_t launch_attend_rows_f16_f8(AttendPlan& p, void* workspace, cudaStream_t s);
+// Many rows a key head; heads of at most 128 elements.
+cudaError_t launch_attend_tile_bf16(AttendPlan& p, void* workspace, cudaStream_t s);
+cudaError_t launch_attend_tile_bf16_f8(AttendPlan& p, void* workspace, cudaStream_t s);
+cudaError_t launch_attend_tile_f16(AttendPlan& p, void* workspace, cudaStream_t s);
+cudaError_t launch_attend_tile_f16_f8(AttendPlan& p, void* workspace, cudaStream_t s);
 size_t attend_workspace(int64_t batch, int64_t seq, int64_t heads, int64_t kv, int64_t dim);
 
 struct AcceptPlan {

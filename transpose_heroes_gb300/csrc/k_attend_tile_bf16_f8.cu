@@ -1,0 +1,10 @@
+// Attention for many rows a key head, bf16 queries over an f8E4M3FN cache.
+#include "attend_tile.cuh"
+
+namespace hlo {
+
+cudaError_t launch_attend_tile_bf16_f8(AttendPlan& p, void* ws, cudaStream_t s) {
+  return p.dim <= 64 ? run_attend_tile<BF16, true, 64>(p, ws, s) : run_attend_tile<BF16, true, 128>(p, ws, s);
+}
+
+}  // namespace hlo
