@@ -1,5 +1,6 @@
 """The layer operators in use: differentiable forms for training, and a small decoder that serves and trains
-with them (matrix products and attention itself are plain torch).
+with them (matrix products, and attention in training, are plain torch). It serves over a paged cache, a token at a time or
+with drafted trees that the model accepts a branch of.
 
     python -m transpose_heroes_gb300.decoder     # trains a few steps on a toy text, then continues it
 
@@ -17,9 +18,9 @@ import math
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import Dropout
+from . import Dropout, cache_append, cache_attention, cache_attention_workspace_size
 from . import dropout as _dropout
-from . import logits_process, rms_norm, rms_norm_backward, rms_norm_workspace_size, rotary, rotary_turns
+from . import logits_process, rms_norm, rms_norm_backward, rms_norm_workspace_size, rotary, rotary_turns, tree_accept, tree_mask
 
 
 def _rows(t):
@@ -99,6 +100,47 @@ def drop(x, params):
     return _Drop.apply(x, params)
 
 
+class PagedCache:
+    """Keys and values of `batch` sequences in all layers of a decoder, in pages of `page` entries: k, v [layers, pages, page, kv,
+    dim], table [batch, max_pages], lengths [batch]. Room for `capacity` entries a sequence; pages are dealt out once."""
+
+    def __init__(self, model, batch, capacity, page=16, dtype=None):
+        device, width = model.embed.device, -(-capacity // page)
+        shape = (len(model.layers), batch * width, page, model.kv, model.dim)
+        self.k, self.v = (torch.empty(shape, dtype=dtype or model.embed.dtype, device=device) for _ in range(2))
+        self.table = torch.arange(batch * width, dtype=torch.int32, device=device).view(batch, width)
+        self.lengths = torch.zeros(batch, dtype=torch.int32, device=device)
+        self._scratch = torch.empty(0, dtype=torch.uint8, device=device)
+
+    def scratch(self, q):
+        """cache_attention's workspace for queries like q, kept for the next call."""
+        size = cache_attention_workspace_size(*q.shape[:3], self.k.shape[3], q.shape[3])
+        if self._scratch.numel() < size:
+            self._scratch = torch.empty(size, dtype=torch.uint8, device=q.device)
+        return self._scratch
+
+
+def draft_tree(tokens, most):
+    """(tokens, parents) of a tree of at most `most` + 1 nodes whose root is the last of `tokens`: what followed the earlier places of
+    the last two tokens (or of the last one), the latest places first, continuations with a common beginning sharing nodes."""
+    nodes, parents, places = [tokens[-1]], [-1], {}
+    for gram in (2, 1):
+        tail = tokens[-gram:]
+        for at in range(len(tokens) - gram - 1, -1, -1):
+            if len(tail) < gram or tokens[at:at + gram] != tail:
+                continue
+            node = 0
+            for t in tokens[at + gram:at + gram + most]:
+                if (node, t) not in places:
+                    if len(nodes) > most:
+                        return nodes, parents
+                    places[node, t] = len(nodes)
+                    nodes.append(t)
+                    parents.append(node)
+                node = places[node, t]
+    return nodes, parents
+
+
 class Decoder:
     """A decoder of pre-norm layers: attention with rotary positions and shared key heads, and a gated
     feed-forward block; dropout on what each block adds to the residual stream."""
@@ -154,30 +196,76 @@ class Decoder:
         return y[-1:] @ self.head
 
     @torch.no_grad()
-    def generate(self, prompt, count, repetition=1.0, frequency=0.0, presence=0.0, mask=None):
+    def extend(self, tokens, cache, counts=None, mask=None, depths=None):
+        """The last norm's output [batch, n, width] for the new tokens [batch, n] of every sequence, whose keys and values are
+        written behind the cache's lengths (which stay). mask, depths: a tree's, as tree_mask makes them; without them each
+        token follows the one before it. counts: new tokens of each sequence."""
+        batch, n = tokens.shape
+        h = self.embed[tokens]
+        y, added = torch.empty_like(h), None
+        positions = None if depths is None else cache.lengths[:, None] + depths
+        for i, w in enumerate(self.layers):
+            if added is None:
+                rms_norm(h, y, weight=w["n1"])
+            else:
+                rms_norm(added, y, weight=w["n1"], residual=h, sum_out=h)
+            qkv = (y @ w["qkv"]).view(batch, n, self.heads + 2 * self.kv, self.dim)
+            q, k, v = qkv.split([self.heads, self.kv, self.kv], 2)
+            place = (cache.k[i], cache.v[i], cache.table, cache.lengths)
+            cache_append(k, v, *place, counts=counts, q=q, q_out=q, positions=positions, turns=self.turns)  # q turns in place
+            a = torch.zeros(batch, n, self.heads, self.dim, dtype=h.dtype, device=h.device)  # rows behind counts stay 0
+            cache_attention(q, *place, a, counts=counts, mask=mask, workspace=cache.scratch(q))
+            added = a.flatten(2) @ w["o"]
+            rms_norm(added, y, weight=w["n2"], residual=h, sum_out=h)
+            added = (torch.nn.functional.silu(y @ w["gate"]) * (y @ w["up"])) @ w["down"]
+        rms_norm(added, y, weight=self.last, residual=h, sum_out=h)
+        return y
+
+    @torch.no_grad()
+    def generate(self, prompt, count, repetition=1.0, frequency=0.0, presence=0.0, mask=None, draft=0):
         """`count` greedy tokens after `prompt` (a list); mask: s32 bits of the allowed tokens, or None. Stops early
-        when the mask leaves nothing."""
+        when the mask leaves nothing. draft: each step also tries up to so many tokens that followed the same ones before (the
+        tokens are those of a step for each, with fewer steps)."""
         dev = self.embed.device
-        history = torch.zeros(1, len(prompt) + count, dtype=torch.int32, device=dev)
-        history[0, :len(prompt)] = torch.tensor(prompt, dtype=torch.int32)
-        vector = lambda x, t: torch.tensor([x], dtype=t, device=dev)  # noqa: E731
-        length, prompts = vector(len(prompt), torch.int32), vector(len(prompt), torch.int32)
-        terms = [vector(x, torch.float32) for x in (repetition, frequency, presence)]
-        token = vector(-1, torch.int32)
-        cache, tokens, first = [None] * len(self.layers), list(prompt), 0
-        step = torch.tensor(tokens, device=dev)
-        while len(tokens) < len(prompt) + count:
-            logits = self.forward(step, cache, first)
-            logits_process(logits, history=history, lengths=length, prompt_lengths=prompts, repetition=terms[0],
-                           frequency=terms[1], presence=terms[2], mask=mask, token=token)
-            first = len(tokens)
-            new = int(token)
-            if new < 0:
-                break
-            history[0, first] = new
-            length += 1
-            tokens.append(new)
-            step = torch.tensor([new], device=dev)
+        whole = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+        tokens, made = list(prompt), 0
+        cache = PagedCache(self, 1, len(prompt) + count + draft + 1)
+        last = self.extend(torch.tensor([tokens], device=dev), cache)[:, -1]
+        cache.lengths += len(tokens)
+        nodes, parents = [tokens[-1]], [-1]
+        while made < count:
+            # each node's logits, with the history that ends in it
+            n = len(nodes)
+            rows = []
+            for c in range(n):
+                way = []
+                while parents[c] >= 0:
+                    way.append(nodes[c])
+                    c = parents[c]
+                rows.append(tokens + way[::-1])
+            longest = max(map(len, rows))
+            history = whole([r + [0] * (longest - len(r)) for r in rows])
+            same = lambda x: torch.full((n,), x, dtype=torch.float32, device=dev)  # noqa: E731
+            picks = torch.empty(1, n, dtype=torch.int32, device=dev)
+            logits_process(last @ self.head, history=history, lengths=whole([len(r) for r in rows]), prompt_lengths=whole([len(prompt)] * n),
+                           repetition=same(repetition), frequency=same(frequency), presence=same(presence), mask=mask, token=picks)
+            path, accepted, new = torch.empty_like(picks), whole([0]), whole([0])
+            if made == 0:  # the prompt's last token is in the cache already
+                path, accepted, new = whole([[0]]), whole([0]), picks[:, 0]
+            else:
+                tree_accept(whole([nodes]), whole([parents]), picks, path, accepted, new, k_cache=cache.k, v_cache=cache.v, pages=cache.table,
+                            lengths=cache.lengths)
+            cache.lengths += accepted
+            found = [nodes[c] for c in path[0].tolist() if c > 0] + [int(new)]
+            if found[-1] < 0:
+                found.pop()
+                count = made + min(len(found), count - made)
+            tokens += found[:count - made]
+            made += min(len(found), count - made)
+            if made < count:
+                nodes, parents = draft_tree(tokens, min(draft, count - made)) if draft else ([tokens[-1]], [-1])
+                bits, depths = (torch.from_numpy(x).to(dev) for x in tree_mask(parents))
+                last = self.extend(whole([nodes]), cache, mask=bits, depths=depths)[0]
         return tokens[len(prompt):]
 
     # ---- training ------------------------------------------------------------------------------------------
@@ -215,6 +303,7 @@ def main():
         if step % 10 == 9:
             print(f"step {step + 1}: loss {float(loss.detach()):.4f}")
     print("continues 3 1 4 1 5 with", model.generate([3, 1, 4, 1, 5], 8))
+    print("the same with drafts:", model.generate([3, 1, 4, 1, 5, 9, 2, 6, 3, 1, 4, 1, 5], 8, draft=4))
     print("and penalised for repeating itself:", model.generate([3, 1, 4, 1, 5], 8, frequency=100.0))
 
 
