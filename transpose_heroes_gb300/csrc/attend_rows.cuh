@@ -90,12 +90,12 @@ __global__ void __launch_bounds__(128, RowsShape<F8, DP, MT>::kBlocks)
   while (share.left > 0) {
     const AttendItem it = share.it;
     const int units = attend_units<S::kRows, S::kUnit>(p, it, it.tile);
-    const int take = (int)min(share.left, (int64_t)(units - share.unit));
-    const int64_t row0 = (int64_t)it.tile * S::kRows;
-    const int rows = (int)min((int64_t)S::kRows, (int64_t)it.count * p.group - row0);
+    const int take = min(share.left, units - share.unit);
+    const int row0 = it.tile * S::kRows;
+    const int rows = min(S::kRows, it.count * p.group - row0);
     const int32_t* const table = p.m.table + it.b * p.m.table_stride;
     const int first = share.unit * S::kUnit, end = min(it.total, first + take * S::kUnit);
-    const int tiles = (max(0, end - first) + KT - 1) / KT;
+    const int tiles = (max(0, end - first) + KT - 1) / KT, open = attend_open<S::kRows>(p, it);
     const int n = (tiles - w + 3) / 4;  // of this warp: w, w + 4, ...
     const char* const kbase = reinterpret_cast<const char*>(p.k) + it.head * p.k_stride[2] * EB;
     const char* const vbase = reinterpret_cast<const char*>(p.v) + it.head * p.v_stride[2] * EB;
@@ -105,11 +105,12 @@ __global__ void __launch_bounds__(128, RowsShape<F8, DP, MT>::kBlocks)
     const auto look = [&](int i) {
       page = -1;
       const int e = first + (w + 4 * i) * KT + lane;
-      if (i < n && lane < KT && e < end) cache_place(p.m, table, e, &page, &place);
+      if (i < n && lane < KT && e < end) page = cache_look(p.m, table, e, &place);
     };
     const auto request = [&](int i) {
       if (i < n) {
         const int s = i % STAGES;
+        page = cache_page(p.m, page);
         const uint32_t given = __ballot_sync(0xffffffffu, page >= 0);
         if (lane == 0) there[w][s] = given;
         const int64_t ko = (page * p.k_stride[0] + place * p.k_stride[1]) * EB;
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(128, RowsShape<F8, DP, MT>::kBlocks)
       const int s = i % STAGES, e0 = first + (w + 4 * i) * KT;
       const uint32_t ks = mine_at + s * S::kStage, vs = ks + KT * ROW;
       const uint32_t given = there[w][s];
-      const bool hides = e0 + KT > it.length;  // some rows may not see all of it
+      const bool hides = e0 + KT > open;  // some rows may not see all of it
       float x[MT][NT][4];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(128, RowsShape<F8, DP, MT>::kBlocks)
       }
       const AttendRow at = attend_row(p, it, row0 + r);
       if (cleared && c < p.dim) {
-        const int from = it.length <= first ? first : first + (it.length - first) / KT * KT;
+        const int from = open <= first ? first : first + (open - first) / KT * KT;
         y.x += cleared_values<F8>(p, it, at.token, from, end, c);
         y.y += cleared_values<F8>(p, it, at.token, from, end, c + 1);
         y.z += cleared_values<F8>(p, it, at.token, from, end, c + 2);
@@ -387,10 +388,9 @@ __global__ void __launch_bounds__(128, RowsShape<F8, DP, MT>::kBlocks)
         to[3] = (uint16_t)(hi >> 16);
       }
     }
-    if (!whole && begins) begun = make_int4(it.b, it.head, it.tile, (int)((share.at + units - 1) / share.per));
+    if (!whole && begins) begun = attend_note(share, units, take);
     __syncthreads();
     share.left -= take;
-    share.at += take;
     share.unit += take;
     if (share.left > 0 && share.unit == units) {
       share.unit = 0;

@@ -5,7 +5,7 @@
 //   groups 0, 1   the softmax of tile 0 and tile 1, a row a thread: scores from tensor memory into registers, running maximum
 //                 and sum, weights back into tensor memory in the scores' place, where the second product takes them from
 //   group 2       requests queries, keys and values (pages of any size, 16 bytes a copy, in the products' 128-byte swizzle)
-//   group 3       one thread issues the products: while one tile's softmax runs, the other tile's products do
+//   group 3       one warp issues the products: while one tile's softmax runs, the other tile's products do
 // Tensor memory: scores 128 columns and outputs DP columns for each tile. The maximum moves only where a score exceeds it
 // by 2^8; then the group rescales its outputs there. No product of its tile runs then: the scores' arrival implies that the
 // product before has ended, and the next one waits for the weights.
@@ -27,7 +27,8 @@ struct TileShape {
   static constexpr int kPanel = 128 * 128;                // 128 rows of 64 16-bit elements
   static constexpr int kTile = kPanel * (DP / 64);        // queries of a tile, or a slot of the ring
   static constexpr int kSlots = DP == 64 ? 8 : 4;
-  static constexpr int kSmem = (2 + kSlots) * kTile + 1024;  // and what rounding the base up to 1024 takes
+  static constexpr int kStaging = 32 * 64;                // of a softmax warp: 64 bytes of each of its rows
+  static constexpr int kSmem = (2 + kSlots) * kTile + 8 * kStaging + 1024;  // and what rounding the base up to 1024 takes
   static constexpr int kThreads = 512;
   static constexpr int kScores = 128;                     // columns; tile s: scores at 128 s, outputs at 256 + DP s
 };
@@ -39,22 +40,32 @@ struct TileBarriers {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// Whether phase `parity` has ended, without waiting.
+__device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{ .reg .pred P; mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2; selp.u32 %0, 1, 0, P; }" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+  return done != 0;
+}
+// Arrives when all products that the warp has issued have ended.
 __device__ __forceinline__ void tile_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile("{ .reg .pred q; elect.sync _|q, 0xFFFFFFFF; @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void tile_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tile_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// d (+)= a b. Operands in shared memory by descriptor; a also in tensor memory.
+// d (+)= a b, issued by one thread of a converged warp. Operands in shared memory by descriptor; a also in tensor memory.
 __device__ __forceinline__ void tile_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add) {
-  asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b),
-               "r"(what), "r"((uint32_t)add)
-               : "memory");
+  asm volatile(
+      "{ .reg .pred p, q; elect.sync _|q, 0xFFFFFFFF; setp.ne.u32 p, %4, 0; @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(what), "r"((uint32_t)add)
+      : "memory");
 }
 __device__ __forceinline__ void tile_mma_weights(uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool add) {
-  asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a), "l"(b),
-               "r"(what), "r"((uint32_t)add)
-               : "memory");
+  asm volatile(
+      "{ .reg .pred p, q; elect.sync _|q, 0xFFFFFFFF; setp.ne.u32 p, %4, 0; @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(what), "r"((uint32_t)add)
+      : "memory");
 }
 
 // A matrix in panels of 64 elements (128 bytes, swizzled) by rows: groups of 8 rows 1024 bytes apart, panels `panel` apart
@@ -151,7 +162,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
   AttendShare share = attend_share<S::kRows, S::kKeys, S::kThreads>(p, scan);
   __syncthreads();
   tile_fence_after();
-  const uint32_t tmem = tmem_at;
+  const uint32_t tmem = 0;  // all 512 columns: they begin at column 0
   int4 begun = make_int4(-1, 0, 0, 0);
   int item = 0;
   uint32_t tile0 = 0;  // tiles of entries before this stretch's
@@ -166,23 +177,22 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
   const auto wait_all = [&](const uint64_t& b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
   // What a stretch of a tile is to every group.
   struct Part {
-    int first, end, tiles, rows, units, take;
-    int64_t row0;
+    int first, end, tiles, rows, units, take, open, row0;
   };
   const auto part_of = [&](const AttendShare& s) {
     Part a;
     a.units = attend_units<S::kRows, S::kKeys>(p, s.it, s.it.tile);
-    a.take = (int)min(s.left, (int64_t)(a.units - s.unit));
-    a.row0 = (int64_t)s.it.tile * S::kRows;
-    a.rows = (int)min((int64_t)S::kRows, (int64_t)s.it.count * p.group - a.row0);
+    a.take = min(s.left, a.units - s.unit);
+    a.row0 = s.it.tile * S::kRows;
+    a.rows = min(S::kRows, s.it.count * p.group - a.row0);
     a.first = s.unit * S::kKeys;
+    a.open = attend_open<S::kRows>(p, s.it);
     a.end = min(s.it.total, a.first + a.take * S::kKeys);
     a.tiles = (max(0, a.end - a.first) + S::kKeys - 1) / S::kKeys;
     return a;
   };
   const auto advance = [&](AttendShare& s, const Part& a) {
     s.left -= a.take;
-    s.at += a.take;
     s.unit += a.take;
     ++item;
     tile0 += a.tiles;
@@ -194,7 +204,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
 
   if (w < 8) {
     // ---- the softmax ----------------------------------------------------------------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int s = w >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (w & 3)) << 16;
     const uint32_t scores = tmem + lanes + S::kScores * s, outs = tmem + lanes + 256 + DP * s;
@@ -220,7 +230,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
           uint32_t given[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) given[c] = there[(tile0 + j) & 7][c];
-          const bool hides = e0 + S::kKeys > it.length;
+          const bool hides = e0 + S::kKeys > a.open;
           tile_wait_loads();
           if (hides || (given[0] & given[1] & given[2] & given[3]) != 0xFFFFFFFFu) {
 #pragma unroll
@@ -289,11 +299,15 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
         const bool begins = share.unit == 0, whole = begins && a.take == a.units;
         const int64_t slot = attend_slot(begins) * (int64_t)S::kRows + row;
         const bool again = a.tiles > 0 && cleared[item & 3] == item;
-        const int from = it.length <= a.first ? a.first : a.first + (it.length - a.first) / S::kKeys * S::kKeys;
+        const int from = a.open <= a.first ? a.first : a.first + (a.open - a.first) / S::kKeys * S::kKeys;
         const float f = sum == 0.0f ? 0.0f : p.value_scale / sum;
-        uint16_t* const to = reinterpret_cast<uint16_t*>(p.out) + it.b * p.out_stride[0] + at.token * p.out_stride[1] + at.head * p.out_stride[2];
+        const int64_t to = it.b * p.out_stride[0] + at.token * p.out_stride[1] + at.head * p.out_stride[2];
         if (mine && whole && p.lse) p.lse[((int64_t)it.b * p.m.seq + at.token) * p.heads + at.head] = attend_lse(top, sum);
         if (mine && !whole) p.stats[slot] = make_float2(top, sum);
+        // 64 bytes of each row at a time through shared memory, so that a warp's stores fill whole sectors
+        char* const staging = base + (2 + SLOTS) * S::kTile + w * S::kStaging;
+        const auto staged = [&](int row, int c) { return reinterpret_cast<uint4*>(staging + row * 64 + (c ^ ((row >> 1) & 3)) * 16); };
+        const uint32_t given = __ballot_sync(0xffffffffu, mine);
 #pragma unroll 1
         for (int c = 0; c < DP; c += 32) {
           uint32_t o[32];
@@ -304,44 +318,59 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0;
           }
-          if (!mine) continue;
-          if (again) {
+          if (again && mine) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (c + i < p.dim) o[i] = __float_as_uint(__uint_as_float(o[i]) + cleared_values<F8>(p, it, at.token, from, a.end, c + i));
           }
-          if (!whole) {
-            float4* const part = reinterpret_cast<float4*>(p.sums + slot * DP + c);
+          if (whole) {
+            uint32_t h[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              part[i / 4] = make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
-            continue;
-          }
+            for (int i = 0; i < 16; ++i)
+              h[i] = sum == 0.0f ? 0u : pack_pair<DT == BF16>(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint32_t h[4];
+            for (int i = 0; i < 4; ++i) *staged(lane, i) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+            __syncwarp();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float u = __uint_as_float(o[i + 2 * k]), v = __uint_as_float(o[i + 2 * k + 1]);
-              h[k] = sum == 0.0f ? 0u : pack_pair<DT == BF16>(u * f, v * f);
+            for (int i = 0; i < 4; ++i) {
+              const int other = 8 * i + (lane >> 2), col = c + 8 * (lane & 3);
+              uint16_t* const at_other = reinterpret_cast<uint16_t*>(p.out) + __shfl_sync(0xffffffffu, to, other) + col;
+              if (!(given >> other & 1) || col >= p.dim) continue;
+              if (out_vectors) {
+                *reinterpret_cast<uint4*>(at_other) = *staged(other, lane & 3);
+              } else {
+#pragma unroll 1
+                for (int k = 0; k < 8; ++k) at_other[k] = reinterpret_cast<const uint16_t*>(staged(other, lane & 3))[k];
+              }
             }
-            if (c + i >= p.dim) continue;
-            if (out_vectors) {
-              *reinterpret_cast<uint4*>(to + c + i) = make_uint4(h[0], h[1], h[2], h[3]);
-            } else {
+            __syncwarp();
+          } else {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) to[c + i + k] = (uint16_t)(h[k / 2] >> (16 * (k & 1)));
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int k = 16 * half + 4 * i;
+                *staged(lane, i) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+              }
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int other = 8 * i + (lane >> 2);
+                if (given >> other & 1)
+                  *reinterpret_cast<uint4*>(p.sums + (slot - lane + other) * DP + c + 16 * half + 4 * (lane & 3)) = *staged(other, lane & 3);
+              }
+              __syncwarp();
             }
           }
         }
-        if (begins && !whole) begun = make_int4(it.b, it.head, it.tile, (int)((share.at + a.units - 1) / share.per));
+        if (begins && !whole) begun = attend_note(share, a.units, a.take);
         tile_fence_before();
       }
       advance(share, a);
     }
   } else if (w < 12) {
     // ---- the copies -----------------------------------------------------------------------------------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     constexpr int EB = F8 ? 1 : 2;
     const int pw = w - 8, ch = lane % CH;
     uint32_t slots = 0;                  // slots filled so far
@@ -349,6 +378,8 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
     // copies in flight: the barriers of the last two groups, and whether a group's values have to be looked through
     uint32_t pending[2] = {0, 0}, look_through[2] = {0, 0};
     int look_item[2] = {0, 0};
+    const bool one_page = p.dim == DP && p.m.page_size % 32 == 0;  // the 32 entries of a warp lie in one page, `step` bytes apart
+    const int64_t step[2] = {p.k_stride[1] * EB, p.v_stride[1] * EB};
     // chunk `c` of row r of a tile of 128 rows
     const auto chunk_at = [&](uint32_t tile, int r, int c) { return tile + (c >> 3) * S::kPanel + r * 128 + ((c & 7) ^ (r & 7)) * 16; };
     const auto land = [&](int k) {  // group k has come
@@ -368,8 +399,10 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
     };
     const auto sent = [&](uint32_t b, uint32_t look, int number) {  // a group's copies have been requested
       copy_commit();
-      copy_wait<2>();
-      land(0);
+      if (pending[0]) {
+        copy_wait<2>();
+        land(0);
+      }
       pending[0] = pending[1];
       look_through[0] = look_through[1];
       look_item[0] = look_item[1];
@@ -382,6 +415,30 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
       land(0);
       land(1);
     };
+    // 8 elements of a query row that cannot be copied as they are
+    const auto put_query = [&](uint32_t to, const uint16_t* from, bool ok, int row) {
+      uint32_t v[4] = {0, 0, 0, 0};
+      if (ok && q_vectors) {
+        const uint4 u = *reinterpret_cast<const uint4*>(from);
+        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+      } else if (ok) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = (uint32_t)from[2 * k] | (uint32_t)from[2 * k + 1] << 16;
+      }
+      if constexpr (DT == BF16 && F8) {  // as in attend_rows_kernel: a power of two takes the row's greatest element to 2^14
+        float most = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[k] << 16)), fabsf(__uint_as_float(v[k] & 0xFFFF0000u))));
+#pragma unroll
+        for (int x = 1; x < CH; x *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+        const int ex = max((int)(__float_as_uint(most) >> 23) - 127, -100);
+        const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = pack_pair<false>(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xFFFF0000u) * up);
+        if (ch == 0) row_unit[item & 1][row] = p.score_scale * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+      }
+      *reinterpret_cast<uint4*>(base + (to - q_at)) = make_uint4(v[0], v[1], v[2], v[3]);
+    };
     while (share.left > 0) {
       const Part a = part_of(share);
       const AttendItem& it = share.it;
@@ -391,77 +448,83 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
         const auto look = [&](int j) {
           page = -1;
           const int e = a.first + j * S::kKeys + 32 * pw + lane;
-          if (e < a.end) cache_place(p.m, table, e, &page, &place);
+          if (e < a.end) page = cache_look(p.m, table, e, &place);
         };
         look(0);
-        // the queries
-        flush();
-        if (q_loads > 0 && !wait_all(bars.q_empty, q_loads - 1)) goto done;
-        ++q_loads;
-        const int halves = a.rows > 128 ? 2 : 1;
-#pragma unroll 1
-        for (int h = 0; h < halves; ++h) {
-          const int mine = 128 * h + 32 * pw + lane;
-          const AttendRow at = attend_row(p, it, a.row0 + mine);
-          const int64_t off = mine < a.rows ? it.b * p.q_stride[0] + at.token * p.q_stride[1] + at.head * p.q_stride[2] : -1;
-#pragma unroll 1
-          for (int i = 0; i < CH; ++i) {
-            const int e = i * (32 / CH) + lane / CH, r = 32 * pw + e;
-            const int64_t o = __shfl_sync(0xffffffffu, off, e);
-            const uint16_t* const from = reinterpret_cast<const uint16_t*>(p.q) + o + 8 * ch;
-            const bool ok = o >= 0 && 8 * ch < p.dim;
-            const uint32_t to = chunk_at(q_at + h * S::kTile, r, ch);
-            if (!(DT == BF16 && F8) && q_vectors) {
-              copy16(to, ok ? (const void*)from : p.q, ok);
-              continue;
-            }
-            uint32_t v[4] = {0, 0, 0, 0};
-            if (ok) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) v[k] = (uint32_t)from[2 * k] | (uint32_t)from[2 * k + 1] << 16;
-            }
-            if constexpr (DT == BF16 && F8) {  // as in attend_rows_kernel: a power of two takes the row's greatest element to 2^14
-              float most = 0.0f;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[k] << 16)), fabsf(__uint_as_float(v[k] & 0xFFFF0000u))));
-#pragma unroll
-              for (int x = 1; x < CH; x *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
-              const int ex = max((int)(__float_as_uint(most) >> 23) - 127, -100);
-              const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) v[k] = pack_pair<false>(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xFFFF0000u) * up);
-              if (ch == 0) row_unit[item & 1][128 * h + r] = p.score_scale * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
-            }
-            *reinterpret_cast<uint4*>(base + (to - q_at)) = make_uint4(v[0], v[1], v[2], v[3]);
+        // the queries, whose place the last stretch's products leave late: behind the first keys
+        const auto queries = [&] {
+          if (q_loads > 0) {
+            if (!__all_sync(0xffffffffu, mbar_done(bar(bars.q_empty), (q_loads - 1) & 1))) flush();
+            if (!wait_all(bars.q_empty, q_loads - 1)) return false;
           }
-        }
-        sent(bar(bars.q_full), 0, item);
+          ++q_loads;
+          const int halves = a.rows > 128 ? 2 : 1;
+          const bool plain = !(DT == BF16 && F8) && q_vectors;
+#pragma unroll 1
+          for (int h = 0; h < halves; ++h) {
+            const int mine = 128 * h + 32 * pw + lane;
+            const AttendRow at = attend_row(p, it, a.row0 + mine);
+            const int64_t off = mine < a.rows ? it.b * p.q_stride[0] + at.token * p.q_stride[1] + at.head * p.q_stride[2] : -1;
+            const uint32_t tile = q_at + h * S::kTile;
+#pragma unroll 8
+            for (int i = 0; i < CH; ++i) {
+              const int e = i * (32 / CH) + lane / CH, r = 32 * pw + e;
+              const int64_t o = __shfl_sync(0xffffffffu, off, e);
+              const uint16_t* const from = reinterpret_cast<const uint16_t*>(p.q) + (o < 0 ? 0 : o + 8 * ch);
+              const bool ok = o >= 0 && 8 * ch < p.dim;
+              const uint32_t to = chunk_at(tile, r, ch);
+              if (plain) copy16(to, ok ? (const void*)from : p.q, ok);
+              else put_query(to, from, ok, 128 * h + r);
+            }
+          }
+          sent(bar(bars.q_full), 0, item);
+          return true;
+        };
         // keys and values
         const char* const kbase = reinterpret_cast<const char*>(p.k) + it.head * p.k_stride[2] * EB;
         const char* const vbase = reinterpret_cast<const char*>(p.v) + it.head * p.v_stride[2] * EB;
         for (int j = 0; j < a.tiles; ++j) {
+          page = cache_page(p.m, page);
           const uint32_t given = __ballot_sync(0xffffffffu, page >= 0);
           if (lane == 0) there[(tile0 + j) & 7][pw] = given;
           int64_t off[2];
           off[0] = (page * p.k_stride[0] + place * p.k_stride[1]) * EB;
           off[1] = same_strides ? off[0] : (page * p.v_stride[0] + place * p.v_stride[1]) * EB;
           look(j + 1);
-          const bool hides = a.first + (j + 1) * S::kKeys > it.length;
+          const bool hides = a.first + (j + 1) * S::kKeys > a.open;
 #pragma unroll
           for (int side = 0; side < 2; ++side) {
+            if (j == 0 && side == 1 && !queries()) goto done;
             const int slot = slots % SLOTS;
-            if (slots >= SLOTS && !wait_all(bars.kv_empty[slot], slots / SLOTS - 1)) goto done;
+            if (slots >= SLOTS) {
+              // what is on its way is announced before the warp waits: the products may need it to free the slot
+              if (!__all_sync(0xffffffffu, mbar_done(bar(bars.kv_empty[slot]), (slots / SLOTS - 1) & 1))) flush();
+              if (!wait_all(bars.kv_empty[slot], slots / SLOTS - 1)) goto done;
+            }
             ++slots;
             const uint32_t tile = ring_at + slot * S::kTile;
             const char* const from = side ? vbase : kbase;
             if constexpr (!F8) {
+              // row e = i (32 / CH) + lane / CH of the warp's 32: its place in shared memory repeats every CH / 4 steps, but for the step
               const bool column = 8 * ch < p.dim;
-#pragma unroll 4
-              for (int i = 0; i < CH; ++i) {
-                const int e = i * (32 / CH) + lane / CH;
-                const int64_t o = __shfl_sync(0xffffffffu, off[side], e);
-                const bool ok = column && (given >> e & 1);
-                copy16(chunk_at(tile, 32 * pw + e, ch), ok ? from + o + ch * 16 : from, ok);
+              uint32_t to[CH / 4];
+#pragma unroll
+              for (int i = 0; i < CH / 4; ++i) to[i] = chunk_at(tile, 32 * pw + i * (32 / CH) + lane / CH, ch);
+              if (one_page && given == 0xFFFFFFFFu && column) {
+                const char* at = from + __shfl_sync(0xffffffffu, off[side], 0) + step[side] * (lane / CH) + ch * 16;
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                  copy16(to[i % (CH / 4)] + (i / (CH / 4)) * 1024, at, true);
+                  at += step[side] * (32 / CH);
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                  const int e = i * (32 / CH) + lane / CH;
+                  const int64_t o = __shfl_sync(0xffffffffu, off[side], e);
+                  const bool ok = column && (given >> e & 1);
+                  copy16(to[i % (CH / 4)] + (i / (CH / 4)) * 1024, ok ? from + o + ch * 16 : from, ok);
+                }
               }
               sent(bar(bars.kv_full[slot]), side && hides ? tile : 0, item);
             } else {
@@ -503,31 +566,33 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
     flush();
   } else {
     // ---- the products ---------------------------------------------------------------------------------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (w == 12 && lane == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (w == 12) {  // one thread issues, but the warp stays together: descriptors are then the same for all of it
       constexpr uint32_t type = BF ? 1 : 0;
       constexpr uint32_t common = 1u << 4 | type << 7 | type << 10 | (128u >> 4) << 24;
       constexpr uint32_t score_what = common | (uint32_t)(S::kKeys >> 3) << 17, out_what = common | 1u << 16 | (uint32_t)(DP >> 3) << 17;
+      // descriptors of addresses further on: the address' field, in units of 16 bytes, grows (it has room for all of shared memory)
+      const uint64_t q_d = tile_descriptor(q_at, S::kPanel), ring_d = tile_descriptor(ring_at, S::kPanel);
       uint32_t slots = 0, q_loads = 0, weights[2] = {0, 0};
       bool ok = true;
       while (ok && share.left > 0) {
         const Part a = part_of(share);
         const int live = a.rows > 128 ? 2 : 1;
         if (a.tiles > 0) {
-          ok = wait(bars.q_full, q_loads++);
+          ok = wait_all(bars.q_full, q_loads++);
           // the product of the weights with the values of slot number v, of which the first tile's begins the sum
           const auto second = [&](int s, uint32_t v, bool add) {
-            ok = ok && wait(bars.p_full[s], weights[s]++) && wait(bars.kv_full[v % SLOTS], v / SLOTS);
+            ok = wait_all(bars.p_full[s], weights[s]++) && wait_all(bars.kv_full[v % SLOTS], v / SLOTS);
             if (!ok) return;
             tile_fence_after();
-            const uint32_t at = ring_at + (v % SLOTS) * S::kTile;
+            const uint64_t values = ring_d + (v % SLOTS) * (S::kTile >> 4);
 #pragma unroll
             for (int k = 0; k < S::kKeys / 16; ++k)
-              tile_mma_weights(tmem + 256 + DP * s, tmem + S::kScores * s + 8 * k, tile_descriptor(at + k * 2048, S::kPanel), out_what, add || k > 0);
+              tile_mma_weights(tmem + 256 + DP * s, tmem + S::kScores * s + 8 * k, values + k * (2048 >> 4), out_what, add || k > 0);
           };
           for (int j = 0; ok && j < a.tiles; ++j) {
             const uint32_t k0 = slots + 2 * j;
-            ok = wait(bars.kv_full[k0 % SLOTS], k0 / SLOTS);
+            ok = wait_all(bars.kv_full[k0 % SLOTS], k0 / SLOTS);
             for (int s = 0; ok && s < live; ++s) {
               if (j > 0) {
                 second(s, k0 - 1, j > 1);
@@ -535,11 +600,12 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
               }
               if (!ok) break;
               tile_fence_after();
-              const uint32_t qa = q_at + s * S::kTile, ka = ring_at + (k0 % SLOTS) * S::kTile;
+              const uint64_t queries = q_d + s * (S::kTile >> 4), keys = ring_d + (k0 % SLOTS) * (S::kTile >> 4);
 #pragma unroll
-              for (int k = 0; k < DP / 16; ++k)
-                tile_mma(tmem + S::kScores * s, tile_descriptor(qa + (k >> 2) * S::kPanel + (k & 3) * 32, 16),
-                         tile_descriptor(ka + (k >> 2) * S::kPanel + (k & 3) * 32, 16), score_what, k > 0);
+              for (int k = 0; k < DP / 16; ++k) {
+                constexpr int panel = S::kPanel >> 4;
+                tile_mma(tmem + S::kScores * s, queries + (k >> 2) * panel + (k & 3) * 2, keys + (k >> 2) * panel + (k & 3) * 2, score_what, k > 0);
+              }
               tile_commit(bar(bars.s_full[s]));
             }
             if (!ok) break;

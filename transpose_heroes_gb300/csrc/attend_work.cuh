@@ -20,11 +20,12 @@ struct AttendItem {
   int tiles;
 };
 
+// Units of work of a tile: of the entries up to the last one that its last token may see.
 template <int M, int N>
 __device__ __forceinline__ int attend_units(const AttendPlan& p, const AttendItem& it, int tile) {
-  int keys = it.total;
-  if (!p.mask) keys = min(keys, it.length + min(it.count, (int)(((int64_t)(tile + 1) * M - 1) / p.group) + 1));
-  return max(1, (keys + N - 1) / N);  // rows that see nothing are written all the same
+  if (p.mask) return max(1, (int)(((uint32_t)it.total + N - 1) / N));  // rows that see nothing are written all the same
+  const uint32_t tokens = min((uint32_t)it.count, ((uint32_t)(tile + 1) * M - 1) / (uint32_t)p.group + 1);
+  return (int)(((uint32_t)it.length + tokens + N - 1) / N);
 }
 
 template <int M>
@@ -32,7 +33,30 @@ __device__ __forceinline__ void attend_sequence(const AttendPlan& p, AttendItem&
   it.length = cache_length(p.m, it.b);
   it.count = cache_count(p.m, it.b);
   it.total = (int)min((int64_t)it.length + it.count, (int64_t)p.m.capacity);
-  it.tiles = (it.count * p.group + M - 1) / M;
+  it.tiles = (int)(((uint32_t)it.count * (uint32_t)p.group + M - 1) / M);
+}
+
+// Units of the first n tiles of a key head. Without a mask tile t sees length + (t + 1) M / group entries: where the group is a
+// power of two this is a sum of floor((a + i) / r), or of an arithmetic series, and no loop over a long prompt's tiles.
+template <int M, int N>
+__device__ __forceinline__ int64_t attend_units_upto(const AttendPlan& p, const AttendItem& it, int n) {
+  if (p.mask) return (int64_t)n * attend_units<M, N>(p, it, 0);
+  const int each = M / p.group;  // tokens of a tile
+  int64_t u = 0;
+  if (each * p.group != M || (each & (each - 1)) != 0) {
+    for (int t = 0; t < n; ++t) u += attend_units<M, N>(p, it, t);
+    return u;
+  }
+  const int full = min(n, it.count / each);
+  if (n > full) u = (int64_t)(n - full) * (((uint32_t)it.length + (uint32_t)it.count + N - 1) / N);
+  const uint32_t up = (uint32_t)it.length + N - 1;
+  if (each > N) return u + (int64_t)full * (up / N) + (int64_t)(each / N) * full * (full + 1) / 2;
+  const uint32_t r = N / each, c = up / each;
+  const auto floors = [r](uint32_t y) {  // the sum of floor(j / r) over j < y
+    const uint64_t q = y / r, rest = y % r;
+    return r * (q * (q - (q > 0)) / 2) + rest * q;
+  };
+  return u + (int64_t)(floors(c + full + 1) - floors(c + 1));
 }
 
 template <int M, int N>
@@ -40,18 +64,13 @@ __device__ __forceinline__ int64_t attend_units_of(const AttendPlan& p, int b) {
   AttendItem it;
   it.b = b;
   attend_sequence<M>(p, it);
-  int64_t u = 0;
-  if (p.mask) u = (int64_t)it.tiles * attend_units<M, N>(p, it, 0);
-  else
-    for (int t = 0; t < it.tiles; ++t) u += attend_units<M, N>(p, it, t);
-  return u * p.kv;
+  return attend_units_upto<M, N>(p, it, it.tiles) * p.kv;
 }
 
-// A block's stretch: `left` units, the first of them unit `unit` of tile `it`.
+// A block's stretch: `left` units, the first of them unit `unit` of tile `it`; per: units a block.
 struct AttendShare {
   AttendItem it;
-  int64_t at, left, per;  // at: the first unit's number among all; per: units a block
-  int unit;
+  int left, per, unit;
 };
 
 struct AttendScan {
@@ -79,9 +98,9 @@ __device__ __forceinline__ AttendShare attend_share(const AttendPlan& p, AttendS
   for (int i = 0; i < W; ++i) all += s.warp[i];
   __syncthreads();
   AttendShare r;
-  r.per = max((int64_t)1, (all + gridDim.x - 1) / gridDim.x);
-  r.at = blockIdx.x * r.per;
-  r.left = max((int64_t)0, min(r.per, all - r.at));
+  const int64_t per = max((int64_t)1, (all + gridDim.x - 1) / gridDim.x), start = blockIdx.x * per;
+  r.per = (int)per;
+  r.left = (int)max((int64_t)0, min(per, all - start));
   r.unit = 0;
   if (r.left == 0) return r;
   if (tid == 0) s.b = 0, s.at = 0;
@@ -101,35 +120,28 @@ __device__ __forceinline__ AttendShare attend_share(const AttendPlan& p, AttendS
     for (int i = 0; i < w; ++i) before += s.warp[i];
     upto += before;
     for (int i = 0; i < W; ++i) carry += s.warp[i];
-    if (upto - u <= r.at && r.at < upto) {
+    if (upto - u <= start && start < upto) {
       s.b = b;
-      s.at = r.at - (upto - u);
+      s.at = start - (upto - u);
     }
     __syncthreads();
-    if (carry > r.at) break;  // the same for all threads
+    if (carry > start) break;  // the same for all threads
   }
   r.it.b = s.b;
   attend_sequence<M>(p, r.it);
   int64_t off = s.at;
-  if (p.mask) {
-    const int u = attend_units<M, N>(p, r.it, 0);
-    const int64_t t = off / u;
-    r.unit = (int)(off - t * u);
-    r.it.head = (int)(t / max(1, r.it.tiles));
-    r.it.tile = (int)(t - (int64_t)r.it.head * r.it.tiles);
-  } else {
-    const int64_t one = max((int64_t)1, attend_units_of<M, N>(p, r.it.b) / p.kv);
-    r.it.head = (int)(off / one);
-    off -= r.it.head * one;
-    r.it.tile = 0;
-    for (;;) {
-      const int u = attend_units<M, N>(p, r.it, r.it.tile);
-      if (off < u) break;
-      off -= u;
-      ++r.it.tile;
-    }
-    r.unit = (int)off;
+  const int64_t one = max((int64_t)1, attend_units_upto<M, N>(p, r.it, r.it.tiles));
+  r.it.head = (int)(off / one);
+  off -= r.it.head * one;
+  // the last tile that begins at or before `off`
+  int lo = 0, hi = max(1, r.it.tiles);
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (attend_units_upto<M, N>(p, r.it, mid) <= off) lo = mid;
+    else hi = mid;
   }
+  r.it.tile = lo;
+  r.unit = (int)(off - attend_units_upto<M, N>(p, r.it, lo));
   return r;
 }
 
@@ -156,7 +168,17 @@ __device__ __forceinline__ bool attend_sees(const AttendPlan& p, const AttendIte
   return (p.mask[it.b * p.mask_stride[0] + t * p.mask_stride[1] + (u >> 5)] >> (u & 31)) & 1;
 }
 
-// The slot of a stretch that is not a whole tile's work, and the note for the join where the tile begins in it.
+// Entries that every row of the tile sees: the first ones, up to here.
+template <int M>
+__device__ __forceinline__ int attend_open(const AttendPlan& p, const AttendItem& it) {
+  return p.mask ? it.length : it.length + (int)((uint32_t)it.tile * M / (uint32_t)p.group) + 1;
+}
+
+// The note for the join of a tile that begins in this block and ends in another, and a stretch's slot where it is not a whole
+// tile's work. The block that notes it ends where its share does.
+__device__ __forceinline__ int4 attend_note(const AttendShare& s, int units, int take) {
+  return make_int4(s.it.b, s.it.head, s.it.tile, (int)blockIdx.x + (units - take + s.per - 1) / s.per);
+}
 __device__ __forceinline__ int attend_slot(bool begins) { return 2 * (int)blockIdx.x + (begins ? 1 : 0); }
 
 // Natural logarithm of a row's sum, from the maximum m and sum l in units of a factor 2.
@@ -168,9 +190,9 @@ __device__ __forceinline__ float attend_lse(float m, float l) {
 struct AttendRow {
   int token, head;
 };
-__device__ __forceinline__ AttendRow attend_row(const AttendPlan& p, const AttendItem& it, int64_t row) {
-  const int t = (int)(row / p.group);
-  return {t, it.head * p.group + (int)(row - (int64_t)t * p.group)};
+__device__ __forceinline__ AttendRow attend_row(const AttendPlan& p, const AttendItem& it, int row) {
+  const int t = (int)((uint32_t)row / (uint32_t)p.group);
+  return {t, it.head * p.group + row - t * p.group};
 }
 
 cudaError_t launch_attend_join(const AttendPlan& p, int m, int cols, int blocks, cudaStream_t s);

@@ -86,15 +86,16 @@ cudaError_t launch_accept(const AcceptPlan& p, cudaStream_t s);
 __device__ __forceinline__ int cache_length(const CacheMap& m, int b) { return min(max(m.lengths[b], 0), m.capacity); }
 __device__ __forceinline__ int cache_count(const CacheMap& m, int b) { return m.counts ? min(max(m.counts[b], 0), m.seq) : m.seq; }
 
-// Page and place of entry `slot` (0 <= slot < 2^31) of a sequence whose table row is `row`; page -1: it is not there.
-__device__ __forceinline__ void cache_place(const CacheMap& m, const int32_t* row, int slot, int* page, int* place) {
+// Page and place of entry `slot` (0 <= slot < 2^31) of a sequence whose table row is `row`. The page as the table has it, or -1
+// behind the table's end: cache_page() tells whether it is there, and a load that nothing looks at yet is not waited for.
+__device__ __forceinline__ int cache_look(const CacheMap& m, const int32_t* row, int slot, int* place) {
   const int at = m.page_shift >= 0 ? slot >> m.page_shift : (int)((uint32_t)slot / (uint32_t)m.page_size);
   *place = slot - at * m.page_size;
-  *page = -1;
-  if (at < m.max_pages) {
-    const int pg = row[at];
-    if (pg >= 0 && pg < m.pages) *page = pg;
-  }
+  return at < m.max_pages ? row[at] : -1;
+}
+__device__ __forceinline__ int cache_page(const CacheMap& m, int page) { return (uint32_t)page < (uint32_t)m.pages ? page : -1; }
+__device__ __forceinline__ void cache_place(const CacheMap& m, const int32_t* row, int slot, int* page, int* place) {
+  *page = cache_page(m, cache_look(m, row, slot, place));
 }
 #endif
 

@@ -22,8 +22,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   it.head = share.y;
   it.tile = share.z;
   it.count = cache_count(p.m, it.b);
-  const int64_t row0 = (int64_t)it.tile * m;
-  const int rows = (int)min((int64_t)m, (int64_t)it.count * p.group - row0);
+  const int row0 = it.tile * m, rows = min(m, it.count * p.group - row0);
   const int n = share.w - (int)blockIdx.x + 1;  // blocks
   const auto slot = [&](int i) { return i == 0 ? 2 * (int64_t)blockIdx.x + 1 : 2 * ((int64_t)blockIdx.x + i); };
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
@@ -95,9 +94,9 @@ __global__ void __launch_bounds__(128) attend_any_kernel(const __grid_constant__
   while (share.left > 0) {
     const AttendItem it = share.it;
     const int units = attend_units<kAnyRows, kAnyKeys>(p, it, it.tile);
-    const int take = (int)min(share.left, (int64_t)(units - share.unit));
-    const int64_t row0 = (int64_t)it.tile * kAnyRows;
-    const int rows = (int)min((int64_t)kAnyRows, (int64_t)it.count * p.group - row0);
+    const int take = min(share.left, units - share.unit);
+    const int row0 = it.tile * kAnyRows;
+    const int rows = min(kAnyRows, it.count * p.group - row0);
     const int32_t* const table = p.m.table + it.b * p.m.table_stride;
     __syncthreads();
     for (int i = tid; i < kAnyRows * p.dim; i += 128) {
@@ -140,8 +139,8 @@ __global__ void __launch_bounds__(128) attend_any_kernel(const __grid_constant__
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int64_t row = row0 + 4 * w + r;
-        const bool seen = page >= 0 && 4 * w + r < rows && attend_sees(p, it, (int)(row / p.group), key0 + lane);
+        const int row = row0 + 4 * w + r;
+        const bool seen = page >= 0 && 4 * w + r < rows && attend_sees(p, it, (int)((uint32_t)row / (uint32_t)p.group), key0 + lane);
         const float x = seen ? s[r] * p.score_scale : __int_as_float(0xFF800000);
         float most = x;
 #pragma unroll
@@ -157,7 +156,7 @@ __global__ void __launch_bounds__(128) attend_any_kernel(const __grid_constant__
       }
       __syncthreads();
       // entries that some row does not see must not reach it, whatever they hold: their weight there is exactly 0
-      const bool mixed = key0 + kAnyKeys > it.length;
+      const bool mixed = key0 + kAnyKeys > attend_open<kAnyRows>(p, it);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int c = tid + 128 * j;
@@ -191,7 +190,7 @@ __global__ void __launch_bounds__(128) attend_any_kernel(const __grid_constant__
     } else {
       const int64_t slot = attend_slot(begins);
       if (tid < kAnyRows) p.stats[slot * kAnyRows + tid] = stat[tid];
-      if (begins) begun = make_int4(it.b, it.head, it.tile, (int)((share.at + units - 1) / share.per));
+      if (begins) begun = attend_note(share, units, take);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -211,7 +210,6 @@ __global__ void __launch_bounds__(128) attend_any_kernel(const __grid_constant__
       }
     }
     share.left -= take;
-    share.at += take;
     share.unit += take;
     if (share.left > 0 && share.unit == units) {
       share.unit = 0;
