@@ -34,8 +34,21 @@ struct TileShape {
 };
 
 struct TileBarriers {
-  uint64_t kv_full[8], kv_empty[8], q_full, q_empty, s_full[2], p_full[2], o_full[2], drained;
+  uint64_t kv_full[8], kv_empty[8], landed[8], cleaned, q_full, q_empty, s_full[2], p_full[2], o_full[2], drained;
 };
+
+// The cache as the tensor copies see it: [pages, kv, page_size, dim], boxes of `rows` entries by 64 elements.
+struct TileMaps {
+  CUtensorMap k, v;
+  int rows;
+};
+
+__device__ __forceinline__ void tile_copy(uint32_t to, const CUtensorMap* map, int x, int place, int head, int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(place), "r"(head), "r"(page), "r"(bar)
+      : "memory");
+}
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -120,8 +133,9 @@ __device__ __forceinline__ uint32_t tile_sees(const AttendPlan& p, const AttendI
   return __funnelshift_r(lo, hi, u & 31);
 }
 
-template <int DT, bool F8, int DP>
-__global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_constant__ AttendPlan p, bool same_strides, bool q_vectors, bool out_vectors) {
+template <int DT, bool F8, int DP, bool TMA>
+__global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_constant__ AttendPlan p, const __grid_constant__ TileMaps maps, bool same_strides,
+                                                             bool q_vectors, bool out_vectors) {
   using S = TileShape<DP>;
   constexpr bool BF = DT == BF16 && !F8;  // the products' type
   constexpr int SLOTS = S::kSlots, CH = DP / 8;  // 16-byte chunks of a row
@@ -138,10 +152,12 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
   const auto bar = [&](const uint64_t& b) { return smem_addr(&b); };
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(bar(bars.kv_full[i]), 128);
+      mbar_init(bar(bars.kv_full[i]), TMA ? 1 : 128);
       mbar_init(bar(bars.kv_empty[i]), 1);
+      mbar_init(bar(bars.landed[i]), 1);
     }
-    mbar_init(bar(bars.q_full), 128);
+    mbar_init(bar(bars.cleaned), 96);
+    mbar_init(bar(bars.q_full), TMA ? 96 : 128);
     mbar_init(bar(bars.q_empty), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(bars.s_full[s]), 1);
@@ -375,13 +391,154 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
     const int pw = w - 8, ch = lane % CH;
     uint32_t slots = 0;                  // slots filled so far
     uint32_t q_loads = 0;
+    // chunk `c` of row r of a tile of 128 rows
+    const auto chunk_at = [&](uint32_t tile, int r, int c) { return tile + (c >> 3) * S::kPanel + r * 128 + ((c & 7) ^ (r & 7)) * 16; };
+    // 8 elements of a query row that cannot be copied as they are
+    const auto put_query = [&](uint32_t to, const uint16_t* from, bool ok, int row) {
+      uint32_t v[4] = {0, 0, 0, 0};
+      if (ok && q_vectors) {
+        const uint4 u = *reinterpret_cast<const uint4*>(from);
+        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+      } else if (ok) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = (uint32_t)from[2 * k] | (uint32_t)from[2 * k + 1] << 16;
+      }
+      if constexpr (DT == BF16 && F8) {  // as in attend_rows_kernel: a power of two takes the row's greatest element to 2^14
+        float most = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[k] << 16)), fabsf(__uint_as_float(v[k] & 0xFFFF0000u))));
+#pragma unroll
+        for (int x = 1; x < CH; x *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+        const int ex = max((int)(__float_as_uint(most) >> 23) - 127, -100);
+        const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = pack_pair<false>(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xFFFF0000u) * up);
+        if (ch == 0) row_unit[item & 1][row] = p.score_scale * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+      }
+      *reinterpret_cast<uint4*>(base + (to - q_at)) = make_uint4(v[0], v[1], v[2], v[3]);
+    };
+    // requests 32 rows of the queries: rows 32 k ..
+    const auto put_queries = [&](const Part& a, const AttendItem& it, int k) {
+      const int mine = 32 * k + lane;
+      const AttendRow at = attend_row(p, it, a.row0 + mine);
+      const int64_t off = mine < a.rows ? it.b * p.q_stride[0] + at.token * p.q_stride[1] + at.head * p.q_stride[2] : -1;
+      const uint32_t tile = q_at + (k >> 2) * S::kTile;
+      const bool plain = !(DT == BF16 && F8) && q_vectors;
+#pragma unroll 8
+      for (int i = 0; i < CH; ++i) {
+        const int e = i * (32 / CH) + lane / CH, r = 32 * (k & 3) + e;
+        const int64_t o = __shfl_sync(0xffffffffu, off, e);
+        const uint16_t* const from = reinterpret_cast<const uint16_t*>(p.q) + (o < 0 ? 0 : o + 8 * ch);
+        const bool ok = o >= 0 && 8 * ch < p.dim;
+        const uint32_t to = chunk_at(tile, r, ch);
+        if (plain) copy16(to, ok ? (const void*)from : p.q, ok);
+        else put_query(to, from, ok, 32 * k + e);
+      }
+    };
+    if constexpr (TMA) {
+      if (w == 8) {
+        // one warp requests the tiles, a box of entries a lane
+        const int boxes = S::kKeys / maps.rows;
+        uint32_t turns = 0, through = 0;  // a bit a slot: phases of `landed`; whether the last copy went to `landed`
+        while (share.left > 0) {
+          const Part a = part_of(share);
+          const AttendItem& it = share.it;
+          const int32_t* const table = p.m.table + it.b * p.m.table_stride;
+          int page = -1, place = 0;
+          const auto look = [&](int j) {
+            page = -1;
+            const int e = a.first + j * S::kKeys + lane * maps.rows;
+            if (lane < boxes && e < a.end) page = cache_look(p.m, table, e, &place);
+          };
+          if (a.tiles > 0) look(0);
+          for (int j = 0; j < a.tiles; ++j) {
+            const int pg = cache_page(p.m, page), pl = place;
+            look(j + 1);
+            uint32_t given[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int e = 32 * k + lane;
+              given[k] = __ballot_sync(0xffffffffu, __shfl_sync(0xffffffffu, pg, e / maps.rows) >= 0 && a.first + j * S::kKeys + e < a.end);
+            }
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+              const int slot = slots % SLOTS;
+              if (slots >= SLOTS && !wait_all(bars.kv_empty[slot], slots / SLOTS - 1)) goto gone;
+              ++slots;
+              // values that some row may not see are looked through first
+              const bool look_through = side && a.first + (j + 1) * S::kKeys > a.open;
+              if (look_through) turns ^= 1u << slot;
+              through = (through & ~(1u << slot)) | (uint32_t)look_through << slot;
+              const uint32_t b = look_through ? bar(bars.landed[slot]) : bar(bars.kv_full[slot]);
+              if (lane == 0) {
+                if (side == 0) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) there[(tile0 + j) & 7][k] = given[k];
+                }
+                mbar_arrive_expect_tx(b, S::kTile);
+              }
+              __syncwarp();
+              if (lane < boxes) {  // a page that is not there lies behind the last one: zeros
+                const uint32_t to = ring_at + slot * S::kTile + lane * maps.rows * 128;
+#pragma unroll
+                for (int c = 0; c < DP / 64; ++c)
+                  tile_copy(to + c * S::kPanel, side ? &maps.v : &maps.k, 64 * c, pl, it.head, pg < 0 ? (int)p.m.pages : pg, b);
+              }
+            }
+          }
+          advance(share, a);
+        }
+      gone:
+        if (dead) {  // given up: the copies on their way still have to come
+          for (uint32_t k = 0; k < min(slots, (uint32_t)SLOTS); ++k)
+            mbar_wait((through >> k & 1) ? bar(bars.landed[k]) : bar(bars.kv_full[k]), (through >> k & 1) ? (turns >> k & 1) ^ 1 : (slots - 1 - k) / SLOTS & 1);
+        }
+      } else {
+        // the others bring the queries, and look through values
+        const int mine = tid - 288;
+        uint32_t turns = 0, joins = 0;  // phases of `landed`, a bit a slot, and of `cleaned`
+        while (share.left > 0) {
+          const Part a = part_of(share);
+          if (a.tiles > 0) {
+            if (q_loads > 0 && !wait_all(bars.q_empty, q_loads - 1)) goto done;
+            ++q_loads;
+            for (int k = w - 9; k < (a.rows > 128 ? 8 : 4); k += 3) put_queries(a, share.it, k);
+            copy_commit();
+            copy_wait<0>();
+            fence_proxy_async();
+            mbar_arrive(bar(bars.q_full));
+            for (int j = max(0, (a.open - a.first) / S::kKeys); j < a.tiles; ++j) {
+              const int slot = (slots + 2 * j + 1) % SLOTS;
+              if (!wait_all(bars.landed[slot], turns >> slot)) goto done;
+              turns ^= 1u << slot;
+              const int given = a.end - (a.first + j * S::kKeys);  // entries behind them are other sequences', or nobody's
+              bool any = false;
+              for (int i = mine; i < S::kKeys * CH; i += 96) {
+                const int r = i / CH;
+                uint4* const at = reinterpret_cast<uint4*>(base + (chunk_at(ring_at + slot * S::kTile, r, i % CH) - q_at));
+                if (r >= given) *at = make_uint4(0, 0, 0, 0);
+                else any |= clear_vector<false, BF>(at);
+              }
+              if (any) cleared[item & 3] = item;
+              fence_proxy_async();
+              mbar_arrive(bar(bars.cleaned));
+              if (w == 9) {
+                if (!wait_all(bars.cleaned, joins)) goto done;
+                if (lane == 0) mbar_arrive(bar(bars.kv_full[slot]));
+              }
+              ++joins;
+            }
+            slots += 2 * a.tiles;
+          }
+          advance(share, a);
+        }
+      }
+    } else {
     // copies in flight: the barriers of the last two groups, and whether a group's values have to be looked through
     uint32_t pending[2] = {0, 0}, look_through[2] = {0, 0};
     int look_item[2] = {0, 0};
     const bool one_page = p.dim == DP && p.m.page_size % 32 == 0;  // the 32 entries of a warp lie in one page, `step` bytes apart
     const int64_t step[2] = {p.k_stride[1] * EB, p.v_stride[1] * EB};
-    // chunk `c` of row r of a tile of 128 rows
-    const auto chunk_at = [&](uint32_t tile, int r, int c) { return tile + (c >> 3) * S::kPanel + r * 128 + ((c & 7) ^ (r & 7)) * 16; };
     const auto land = [&](int k) {  // group k has come
       if (!pending[k]) return;
       if (look_through[k]) {
@@ -415,30 +572,6 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
       land(0);
       land(1);
     };
-    // 8 elements of a query row that cannot be copied as they are
-    const auto put_query = [&](uint32_t to, const uint16_t* from, bool ok, int row) {
-      uint32_t v[4] = {0, 0, 0, 0};
-      if (ok && q_vectors) {
-        const uint4 u = *reinterpret_cast<const uint4*>(from);
-        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-      } else if (ok) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = (uint32_t)from[2 * k] | (uint32_t)from[2 * k + 1] << 16;
-      }
-      if constexpr (DT == BF16 && F8) {  // as in attend_rows_kernel: a power of two takes the row's greatest element to 2^14
-        float most = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[k] << 16)), fabsf(__uint_as_float(v[k] & 0xFFFF0000u))));
-#pragma unroll
-        for (int x = 1; x < CH; x *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
-        const int ex = max((int)(__float_as_uint(most) >> 23) - 127, -100);
-        const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = pack_pair<false>(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xFFFF0000u) * up);
-        if (ch == 0) row_unit[item & 1][row] = p.score_scale * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
-      }
-      *reinterpret_cast<uint4*>(base + (to - q_at)) = make_uint4(v[0], v[1], v[2], v[3]);
-    };
     while (share.left > 0) {
       const Part a = part_of(share);
       const AttendItem& it = share.it;
@@ -458,25 +591,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
             if (!wait_all(bars.q_empty, q_loads - 1)) return false;
           }
           ++q_loads;
-          const int halves = a.rows > 128 ? 2 : 1;
-          const bool plain = !(DT == BF16 && F8) && q_vectors;
-#pragma unroll 1
-          for (int h = 0; h < halves; ++h) {
-            const int mine = 128 * h + 32 * pw + lane;
-            const AttendRow at = attend_row(p, it, a.row0 + mine);
-            const int64_t off = mine < a.rows ? it.b * p.q_stride[0] + at.token * p.q_stride[1] + at.head * p.q_stride[2] : -1;
-            const uint32_t tile = q_at + h * S::kTile;
-#pragma unroll 8
-            for (int i = 0; i < CH; ++i) {
-              const int e = i * (32 / CH) + lane / CH, r = 32 * pw + e;
-              const int64_t o = __shfl_sync(0xffffffffu, off, e);
-              const uint16_t* const from = reinterpret_cast<const uint16_t*>(p.q) + (o < 0 ? 0 : o + 8 * ch);
-              const bool ok = o >= 0 && 8 * ch < p.dim;
-              const uint32_t to = chunk_at(tile, r, ch);
-              if (plain) copy16(to, ok ? (const void*)from : p.q, ok);
-              else put_query(to, from, ok, 128 * h + r);
-            }
-          }
+          for (int k = pw; k < (a.rows > 128 ? 8 : 4); k += 4) put_queries(a, share.it, k);
           sent(bar(bars.q_full), 0, item);
           return true;
         };
@@ -564,6 +679,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
       advance(share, a);
     }
     flush();
+    }
   } else {
     // ---- the products ---------------------------------------------------------------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -637,8 +753,35 @@ done:
   allow_next();
 }
 
-template <int DT, bool F8, int DP>
-cudaError_t run_attend_tile(AttendPlan& p, void* ws, cudaStream_t s) {
+// The maps of a cache whose pages hold whole boxes of 8 to 128 entries (a power of two, so that a tile of 128 is some of
+// them); false where there are none, for strides that no map takes or other pages: 16-byte copies bring those.
+template <int DT>
+bool tile_maps(const AttendPlan& p, TileMaps* maps) {
+  maps->rows = 1;
+  while (maps->rows < 128 && p.m.page_size % (2 * maps->rows) == 0) maps->rows *= 2;
+  const auto encode = tensor_map_encoder();
+  if (maps->rows < 8 || !encode || p.m.pages < 1) return false;
+  for (int side = 0; side < 2; ++side) {
+    const int64_t* const s = side ? p.v_stride : p.k_stride;  // page, place, head; 0 for one of them only
+    const cuuint64_t dims[4] = {(cuuint64_t)p.dim, (cuuint64_t)p.m.page_size, (cuuint64_t)p.kv, (cuuint64_t)p.m.pages};
+    const int64_t steps[3] = {s[1], s[2], s[0]};
+    cuuint64_t strides[3];
+    for (int d = 0; d < 3; ++d) {
+      if (steps[d] == 0 && dims[d + 1] > 1) return false;
+      if (steps[d] * 2 >= (int64_t)1 << 40) return false;
+      strides[d] = steps[d] == 0 ? 16 : (cuuint64_t)steps[d] * 2;
+    }
+    const cuuint32_t box[4] = {64, (cuuint32_t)maps->rows, 1, 1}, ones[4] = {1, 1, 1, 1};
+    const CUresult r = encode(side ? &maps->v : &maps->k, DT == BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                              const_cast<void*>(side ? p.v : p.k), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return false;
+  }
+  return true;
+}
+
+template <int DT, bool F8, int DP, bool TMA>
+cudaError_t run_attend_tile(AttendPlan& p, const TileMaps& maps, void* ws, cudaStream_t s) {
   using S = TileShape<DP>;
   const int blocks = device_sm_count();
   attend_layout(&p, ws, blocks, S::kRows, DP);
@@ -648,11 +791,21 @@ cudaError_t run_attend_tile(AttendPlan& p, void* ws, cudaStream_t s) {
     q_vectors = q_vectors && p.q_stride[d] % 8 == 0;
     out_vectors = out_vectors && p.out_stride[d] % 8 == 0;
   }
-  const auto kernel = attend_tile_kernel<DT, F8, DP>;
+  const auto kernel = attend_tile_kernel<DT, F8, DP, TMA>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_after(kernel, dim3((unsigned)blocks), dim3(S::kThreads), S::kSmem, s, 1, p, same, q_vectors, out_vectors);
+  e = launch_after(kernel, dim3((unsigned)blocks), dim3(S::kThreads), S::kSmem, s, 1, p, maps, same, q_vectors, out_vectors);
   return e == cudaSuccess ? launch_attend_join(p, S::kRows, DP, blocks, s) : e;
+}
+
+template <int DT, bool F8>
+cudaError_t run_attend_tile_type(AttendPlan& p, void* ws, cudaStream_t s) {
+  TileMaps maps = {};
+  if constexpr (!F8) {
+    if (tile_maps<DT>(p, &maps))
+      return p.dim <= 64 ? run_attend_tile<DT, F8, 64, true>(p, maps, ws, s) : run_attend_tile<DT, F8, 128, true>(p, maps, ws, s);
+  }
+  return p.dim <= 64 ? run_attend_tile<DT, F8, 64, false>(p, maps, ws, s) : run_attend_tile<DT, F8, 128, false>(p, maps, ws, s);
 }
 
 }  // namespace hlo

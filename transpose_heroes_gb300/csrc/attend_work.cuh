@@ -171,7 +171,7 @@ __device__ __forceinline__ bool attend_sees(const AttendPlan& p, const AttendIte
 // Entries that every row of the tile sees: the first ones, up to here.
 template <int M>
 __device__ __forceinline__ int attend_open(const AttendPlan& p, const AttendItem& it) {
-  return p.mask ? it.length : it.length + (int)((uint32_t)it.tile * M / (uint32_t)p.group) + 1;
+  return p.mask ? it.length : min(it.total, it.length + (int)((uint32_t)it.tile * M / (uint32_t)p.group) + 1);
 }
 
 // The note for the join of a tile that begins in this block and ends in another, and a stretch's slot where it is not a whole

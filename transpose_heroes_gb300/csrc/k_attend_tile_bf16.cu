@@ -3,8 +3,6 @@
 
 namespace hlo {
 
-cudaError_t launch_attend_tile_bf16(AttendPlan& p, void* ws, cudaStream_t s) {
-  return p.dim <= 64 ? run_attend_tile<BF16, false, 64>(p, ws, s) : run_attend_tile<BF16, false, 128>(p, ws, s);
-}
+cudaError_t launch_attend_tile_bf16(AttendPlan& p, void* ws, cudaStream_t s) { return run_attend_tile_type<BF16, false>(p, ws, s); }
 
 }  // namespace hlo
