@@ -40,7 +40,9 @@ struct TileBarriers {
 // The cache as the tensor copies see it: [pages, kv, page_size, dim], boxes of `rows` entries by 64 elements.
 struct TileMaps {
   CUtensorMap k, v;
+  CUtensorMap q;  // [batch, seq, heads, dim], boxes of a tile's tokens and the group's heads, where a group divides the tile
   int rows;
+  int queries;    // whether q is there
 };
 
 __device__ __forceinline__ void tile_copy(uint32_t to, const CUtensorMap* map, int x, int place, int head, int page, uint32_t bar) {
@@ -59,25 +61,26 @@ __device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity) {
   asm volatile("{ .reg .pred P; mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2; selp.u32 %0, 1, 0, P; }" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
   return done != 0;
 }
-// Arrives when all products that the warp has issued have ended.
-__device__ __forceinline__ void tile_commit(uint32_t bar) {
-  asm volatile("{ .reg .pred q; elect.sync _|q, 0xFFFFFFFF; @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar)
+// Arrives when all products that the leader has issued have ended.
+__device__ __forceinline__ void tile_commit(uint32_t leader, uint32_t bar) {
+  asm volatile("{ .reg .pred q; setp.ne.u32 q, %1, 0; @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
+               "r"(leader)
                : "memory");
 }
 __device__ __forceinline__ void tile_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tile_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// d (+)= a b, issued by one thread of a converged warp. Operands in shared memory by descriptor; a also in tensor memory.
-__device__ __forceinline__ void tile_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add) {
+// d (+)= a b, issued by the leader of a converged warp. Operands in shared memory by descriptor; a also in tensor memory.
+__device__ __forceinline__ void tile_mma(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add) {
   asm volatile(
-      "{ .reg .pred p, q; elect.sync _|q, 0xFFFFFFFF; setp.ne.u32 p, %4, 0; @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(what), "r"((uint32_t)add)
+      "{ .reg .pred p, q; setp.ne.u32 q, %5, 0; setp.ne.u32 p, %4, 0; @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a),
+      "l"(b), "r"(what), "r"((uint32_t)add), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void tile_mma_weights(uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool add) {
+__device__ __forceinline__ void tile_mma_weights(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool add) {
   asm volatile(
-      "{ .reg .pred p, q; elect.sync _|q, 0xFFFFFFFF; setp.ne.u32 p, %4, 0; @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(what), "r"((uint32_t)add)
+      "{ .reg .pred p, q; setp.ne.u32 q, %5, 0; setp.ne.u32 p, %4, 0; @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a),
+      "l"(b), "r"(what), "r"((uint32_t)add), "r"(leader)
       : "memory");
 }
 
@@ -142,7 +145,8 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
   extern __shared__ char raw[];
   __shared__ __align__(8) TileBarriers bars;
   __shared__ AttendScan scan;
-  __shared__ uint32_t tmem_at, there[8][4];  // there: which of a tile's entries exist
+  __shared__ uint32_t tmem_at;
+  __shared__ __align__(16) uint32_t there[8][4];  // there: which of a tile's entries exist
   __shared__ float row_unit[2][S::kRows];    // a row's scores in units of a factor 2 (bf16 queries over codes)
   __shared__ int cleared[4];                 // the item whose values were cleared, by the item's number mod 4
   __shared__ volatile int dead;
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
       mbar_init(bar(bars.landed[i]), 1);
     }
     mbar_init(bar(bars.cleaned), 96);
-    mbar_init(bar(bars.q_full), TMA ? 96 : 128);
+    mbar_init(bar(bars.q_full), TMA ? maps.queries ? 1 : 96 : 128);
     mbar_init(bar(bars.q_empty), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(bars.s_full[s]), 1);
@@ -239,31 +243,30 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
           ++seen_scores;
           tile_fence_after();
           if (DT == BF16 && F8 && j == 0) unit = row_unit[item & 1][row];
-          uint32_t x[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tile_load32(x[c], scores + 32 * c);
           const int e0 = a.first + j * S::kKeys;
-          uint32_t given[4];
+          const uint4 given = *reinterpret_cast<const uint4*>(there[(tile0 + j) & 7]);
+          const bool hides = e0 + S::kKeys > a.open, cut = hides || (given.x & given.y & given.z & given.w) != 0xFFFFFFFFu;
+          uint32_t x[4][32];
+          float m[4];
+          tile_load32(x[0], scores);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) given[c] = there[(tile0 + j) & 7][c];
-          const bool hides = e0 + S::kKeys > a.open;
-          tile_wait_loads();
-          if (hides || (given[0] & given[1] & given[2] & given[3]) != 0xFFFFFFFFu) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t see = given[c];
+          for (int c = 0; c < 4; ++c) {  // a quarter's maximum while the next one comes
+            tile_wait_loads();
+            if (c < 3) tile_load32(x[c + 1], scores + 32 * (c + 1));
+            if (cut) {
+              uint32_t see = c == 0 ? given.x : c == 1 ? given.y : c == 2 ? given.z : given.w;
               if (hides && mine) see &= tile_sees(p, it, at.token, e0 + 32 * c);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!(see >> i & 1)) x[c][i] = 0xFF800000u;
             }
-          }
-          float m[4];
+            float u = __uint_as_float(x[c][0]), v = __uint_as_float(x[c][1]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            m[c] = __uint_as_float(x[c][0]);
-#pragma unroll
-            for (int i = 1; i < 32; ++i) m[c] = fmaxf(m[c], __uint_as_float(x[c][i]));
+            for (int i = 2; i < 32; i += 2) {
+              u = fmaxf(u, __uint_as_float(x[c][i]));
+              v = fmaxf(v, __uint_as_float(x[c][i + 1]));
+            }
+            m[c] = fmaxf(u, v);
           }
           const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * unit;
           if (__any_sync(0xffffffffu, most > top + 8.0f)) {
@@ -500,13 +503,15 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
         while (share.left > 0) {
           const Part a = part_of(share);
           if (a.tiles > 0) {
-            if (q_loads > 0 && !wait_all(bars.q_empty, q_loads - 1)) goto done;
-            ++q_loads;
-            for (int k = w - 9; k < (a.rows > 128 ? 8 : 4); k += 3) put_queries(a, share.it, k);
-            copy_commit();
-            copy_wait<0>();
-            fence_proxy_async();
-            mbar_arrive(bar(bars.q_full));
+            if (!maps.queries) {
+              if (q_loads > 0 && !wait_all(bars.q_empty, q_loads - 1)) goto done;
+              ++q_loads;
+              for (int k = w - 9; k < (a.rows > 128 ? 8 : 4); k += 3) put_queries(a, share.it, k);
+              copy_commit();
+              copy_wait<0>();
+              fence_proxy_async();
+              mbar_arrive(bar(bars.q_full));
+            }
             for (int j = max(0, (a.open - a.first) / S::kKeys); j < a.tiles; ++j) {
               const int slot = (slots + 2 * j + 1) % SLOTS;
               if (!wait_all(bars.landed[slot], turns >> slot)) goto done;
@@ -689,6 +694,8 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
       constexpr uint32_t score_what = common | (uint32_t)(S::kKeys >> 3) << 17, out_what = common | 1u << 16 | (uint32_t)(DP >> 3) << 17;
       // descriptors of addresses further on: the address' field, in units of 16 bytes, grows (it has room for all of shared memory)
       const uint64_t q_d = tile_descriptor(q_at, S::kPanel), ring_d = tile_descriptor(ring_at, S::kPanel);
+      uint32_t leader;
+      asm volatile("{ .reg .pred q; elect.sync _|q, 0xFFFFFFFF; selp.u32 %0, 1, 0, q; }" : "=r"(leader));
       uint32_t slots = 0, q_loads = 0, weights[2] = {0, 0};
       bool ok = true;
       while (ok && share.left > 0) {
@@ -704,7 +711,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
             const uint64_t values = ring_d + (v % SLOTS) * (S::kTile >> 4);
 #pragma unroll
             for (int k = 0; k < S::kKeys / 16; ++k)
-              tile_mma_weights(tmem + 256 + DP * s, tmem + S::kScores * s + 8 * k, values + k * (2048 >> 4), out_what, add || k > 0);
+              tile_mma_weights(leader, tmem + 256 + DP * s, tmem + S::kScores * s + 8 * k, values + k * (2048 >> 4), out_what, add || k > 0);
           };
           for (int j = 0; ok && j < a.tiles; ++j) {
             const uint32_t k0 = slots + 2 * j;
@@ -712,7 +719,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
             for (int s = 0; ok && s < live; ++s) {
               if (j > 0) {
                 second(s, k0 - 1, j > 1);
-                if (ok && s == live - 1) tile_commit(bar(bars.kv_empty[(k0 - 1) % SLOTS]));
+                if (ok && s == live - 1) tile_commit(leader, bar(bars.kv_empty[(k0 - 1) % SLOTS]));
               }
               if (!ok) break;
               tile_fence_after();
@@ -720,26 +727,45 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
 #pragma unroll
               for (int k = 0; k < DP / 16; ++k) {
                 constexpr int panel = S::kPanel >> 4;
-                tile_mma(tmem + S::kScores * s, queries + (k >> 2) * panel + (k & 3) * 2, keys + (k >> 2) * panel + (k & 3) * 2, score_what, k > 0);
+                tile_mma(leader, tmem + S::kScores * s, queries + (k >> 2) * panel + (k & 3) * 2, keys + (k >> 2) * panel + (k & 3) * 2, score_what, k > 0);
               }
-              tile_commit(bar(bars.s_full[s]));
+              tile_commit(leader, bar(bars.s_full[s]));
             }
             if (!ok) break;
-            tile_commit(bar(bars.kv_empty[k0 % SLOTS]));
-            if (j == a.tiles - 1) tile_commit(bar(bars.q_empty));
+            tile_commit(leader, bar(bars.kv_empty[k0 % SLOTS]));
+            if (j == a.tiles - 1) tile_commit(leader, bar(bars.q_empty));
           }
           slots += 2 * a.tiles;
           for (int s = 0; ok && s < live; ++s) {
             second(s, slots - 1, a.tiles > 1);
-            if (ok) tile_commit(bar(bars.o_full[s]));
+            if (ok) tile_commit(leader, bar(bars.o_full[s]));
           }
-          if (ok) tile_commit(bar(bars.kv_empty[(slots - 1) % SLOTS]));
+          if (ok) tile_commit(leader, bar(bars.kv_empty[(slots - 1) % SLOTS]));
         }
         advance(share, a);
       }
       // every product that was issued has ended before the memory is given back
-      tile_commit(bar(bars.drained));
+      tile_commit(leader, bar(bars.drained));
       mbar_wait(bar(bars.drained), 0);
+    }
+    if (TMA && w == 13 && maps.queries) {  // the queries, as soon as the last stretch's scores have been computed
+      uint32_t q_loads = 0;
+      while (share.left > 0) {
+        const Part a = part_of(share);
+        if (a.tiles > 0) {
+          if (q_loads > 0 && !wait_all(bars.q_empty, q_loads - 1)) break;
+          ++q_loads;
+          const int halves = a.rows > 128 ? 2 : 1, tokens = 128 / p.group, b = share.it.b;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(bars.q_full), halves * S::kTile);
+            for (int h = 0; h < halves; ++h)
+              for (int c = 0; c < DP / 64; ++c)
+                tile_copy(q_at + h * S::kTile + c * S::kPanel, &maps.q, 64 * c, share.it.head * p.group, (2 * share.it.tile + h) * tokens, b, bar(bars.q_full));
+          }
+        }
+        advance(share, a);
+      }
+      if (dead && q_loads > 0) mbar_wait(bar(bars.q_full), (q_loads - 1) & 1);  // given up: the copies on their way still have to come
     }
     __syncwarp();
   }
@@ -761,22 +787,28 @@ bool tile_maps(const AttendPlan& p, TileMaps* maps) {
   while (maps->rows < 128 && p.m.page_size % (2 * maps->rows) == 0) maps->rows *= 2;
   const auto encode = tensor_map_encoder();
   if (maps->rows < 8 || !encode || p.m.pages < 1) return false;
-  for (int side = 0; side < 2; ++side) {
-    const int64_t* const s = side ? p.v_stride : p.k_stride;  // page, place, head; 0 for one of them only
-    const cuuint64_t dims[4] = {(cuuint64_t)p.dim, (cuuint64_t)p.m.page_size, (cuuint64_t)p.kv, (cuuint64_t)p.m.pages};
-    const int64_t steps[3] = {s[1], s[2], s[0]};
+  // an array [n2, n1, n0, dim] with those strides (0 where a dimension is 1), in boxes [1, b1, b0, 64]
+  const auto encoded = [&](CUtensorMap* map, const void* at, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int b0, int b1) {
+    const cuuint64_t dims[4] = {(cuuint64_t)p.dim, (cuuint64_t)n0, (cuuint64_t)n1, (cuuint64_t)n2};
+    const int64_t steps[3] = {s0, s1, s2};
     cuuint64_t strides[3];
     for (int d = 0; d < 3; ++d) {
       if (steps[d] == 0 && dims[d + 1] > 1) return false;
-      if (steps[d] * 2 >= (int64_t)1 << 40) return false;
+      if (steps[d] >= (int64_t)1 << 39) return false;
       strides[d] = steps[d] == 0 ? 16 : (cuuint64_t)steps[d] * 2;
     }
-    const cuuint32_t box[4] = {64, (cuuint32_t)maps->rows, 1, 1}, ones[4] = {1, 1, 1, 1};
-    const CUresult r = encode(side ? &maps->v : &maps->k, DT == BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-                              const_cast<void*>(side ? p.v : p.k), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return false;
+    const cuuint32_t box[4] = {64, (cuuint32_t)b0, (cuuint32_t)b1, 1}, ones[4] = {1, 1, 1, 1};
+    return encode(map, DT == BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(at), dims, strides, box,
+                  ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  for (int side = 0; side < 2; ++side) {
+    const int64_t* const s = side ? p.v_stride : p.k_stride;  // page, place, head
+    if (!encoded(side ? &maps->v : &maps->k, side ? p.v : p.k, p.m.page_size, s[1], p.kv, s[2], p.m.pages, s[0], maps->rows, 1)) return false;
   }
+  bool fits = 128 % p.group == 0 && (uintptr_t)p.q % 16 == 0;
+  for (int d = 0; d < 3; ++d) fits = fits && p.q_stride[d] % 8 == 0;
+  maps->queries = fits && encoded(&maps->q, p.q, p.heads, p.q_stride[2], p.m.seq, p.q_stride[1], p.m.batch, p.q_stride[0], p.group, 128 / p.group);
   return true;
 }
 
