@@ -60,11 +60,25 @@ __device__ __forceinline__ bool clear_word(uint32_t& w) {
   w &= ~bad;
   return bad != 0;
 }
+// Whether 16 bytes hold such an element. Of two 16-bit elements an exponent of ones carries into the sign's place.
+template <bool F8, bool BF>
+__device__ __forceinline__ bool wants_clearing(const uint4& v) {
+  if constexpr (F8) {
+    constexpr uint32_t ones = 0x7F7F7F7Fu, step = 0x01010101u;  // 0x7F + 1: the code's sign
+    return ((((v.x & ones) + step) | ((v.y & ones) + step) | ((v.z & ones) + step) | ((v.w & ones) + step)) & 0x80808080u) != 0;
+  } else {
+    constexpr uint32_t ones = BF ? 0x7F807F80u : 0x7C007C00u, step = BF ? 0x00800080u : 0x04000400u;
+    return ((((v.x & ones) + step) | ((v.y & ones) + step) | ((v.z & ones) + step) | ((v.w & ones) + step)) & 0x80008000u) != 0;
+  }
+}
 template <bool F8, bool BF>
 __device__ __forceinline__ bool clear_vector(uint4* at) {
   uint4 v = *at;
-  const bool a = clear_word<F8, BF>(v.x), b = clear_word<F8, BF>(v.y), c = clear_word<F8, BF>(v.z), d = clear_word<F8, BF>(v.w);
-  if (!(a || b || c || d)) return false;
+  if (!wants_clearing<F8, BF>(v)) return false;
+  clear_word<F8, BF>(v.x);
+  clear_word<F8, BF>(v.y);
+  clear_word<F8, BF>(v.z);
+  clear_word<F8, BF>(v.w);
   *at = v;
   return true;
 }

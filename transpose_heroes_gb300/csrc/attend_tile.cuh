@@ -101,14 +101,12 @@ __device__ __forceinline__ void tile_load32(uint32_t (&r)[32], uint32_t at) {
         "=r"(r[31])
       : "r"(at));
 }
-__device__ __forceinline__ void tile_store32(uint32_t at, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tile_load16(uint32_t (&r)[16], uint32_t at) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
-      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+        "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
 }
 __device__ __forceinline__ void tile_store16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
@@ -142,6 +140,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
   using S = TileShape<DP>;
   constexpr bool BF = DT == BF16 && !F8;  // the products' type
   constexpr int SLOTS = S::kSlots, CH = DP / 8;  // 16-byte chunks of a row
+  constexpr int kCleared = TMA ? 32 : S::kKeys;  // entries that are looked through at once
   extern __shared__ char raw[];
   __shared__ __align__(8) TileBarriers bars;
   __shared__ AttendScan scan;
@@ -165,7 +164,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
     mbar_init(bar(bars.q_empty), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(bars.s_full[s]), 1);
-      mbar_init(bar(bars.p_full[s]), 128);
+      mbar_init(bar(bars.p_full[s]), 4);
       mbar_init(bar(bars.o_full[s]), 1);
     }
     mbar_init(bar(bars.drained), 1);
@@ -186,9 +185,9 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
   int4 begun = make_int4(-1, 0, 0, 0);
   int item = 0;
   uint32_t tile0 = 0;  // tiles of entries before this stretch's
-  // Waits for a phase; false when the wait ran out here or in another warp.
+  // Waits for a phase; false when the wait ran out (the other groups' waits then run out too).
   const auto wait = [&](const uint64_t& b, uint32_t parity) {
-    if (mbar_wait(bar(b), parity & 1)) return !dead;
+    if (mbar_wait(bar(b), parity & 1)) return true;
     dead = 1;
     record_fault(kFaultCopyTimeout);
     return false;
@@ -278,11 +277,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
 #pragma unroll
               for (int c = 0; c < DP; c += 16) {
                 uint32_t o[16];
-                asm volatile(
-                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                    : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]), "=r"(o[8]), "=r"(o[9]),
-                      "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-                    : "r"(outs + c));
+                tile_load16(o, outs + c);
                 tile_wait_loads();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
@@ -308,7 +303,8 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
           sum += (total[0].x + total[0].y) + (total[1].x + total[1].y);
           tile_wait_stores();
           tile_fence_before();
-          mbar_arrive(bar(bars.p_full[s]));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(bars.p_full[s]));
         }
         if (a.tiles > 0) {
           if (!wait_all(bars.o_full[s], seen_outs)) goto done;
@@ -318,69 +314,80 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
         const bool begins = share.unit == 0, whole = begins && a.take == a.units;
         const int64_t slot = attend_slot(begins) * (int64_t)S::kRows + row;
         const bool again = a.tiles > 0 && cleared[item & 3] == item;
-        const int from = a.open <= a.first ? a.first : a.first + (a.open - a.first) / S::kKeys * S::kKeys;
-        const float f = sum == 0.0f ? 0.0f : p.value_scale / sum;
-        const int64_t to = it.b * p.out_stride[0] + at.token * p.out_stride[1] + at.head * p.out_stride[2];
+        const int from = a.open <= a.first ? a.first : a.first + (a.open - a.first) / kCleared * kCleared;
+        const float f = sum == 0.0f ? 0.0f : p.value_scale / sum;  // rows that saw nothing have outputs of 0
         if (mine && whole && p.lse) p.lse[((int64_t)it.b * p.m.seq + at.token) * p.heads + at.head] = attend_lse(top, sum);
         if (mine && !whole) p.stats[slot] = make_float2(top, sum);
-        // 64 bytes of each row at a time through shared memory, so that a warp's stores fill whole sectors
+        // 64 bytes of each row at a time (32 elements of out, or 16 sums) through shared memory, so that a warp's stores fill whole
+        // sectors
         char* const staging = base + (2 + SLOTS) * S::kTile + w * S::kStaging;
         const auto staged = [&](int row, int c) { return reinterpret_cast<uint4*>(staging + row * 64 + (c ^ ((row >> 1) & 3)) * 16); };
         const uint32_t given = __ballot_sync(0xffffffffu, mine);
+        char* const to = whole ? reinterpret_cast<char*>(reinterpret_cast<uint16_t*>(p.out) + it.b * p.out_stride[0] + at.token * p.out_stride[1] +
+                                                         at.head * p.out_stride[2])
+                               : reinterpret_cast<char*>(p.sums + slot * DP);
+        const int step = whole ? 32 : 16, columns = whole ? p.dim : DP, piece = lane & 3;
+        char* at_other[4];
+        bool stores[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int other = 8 * i + (lane >> 2);
+          at_other[i] = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, (unsigned long long)to, other)) + 16 * piece;
+          stores[i] = given >> other & 1;
+        }
 #pragma unroll 1
-        for (int c = 0; c < DP; c += 32) {
-          uint32_t o[32];
-          if (a.tiles > 0) {
+        for (int c = 0; c < DP; c += step) {
+          uint32_t h[16];
+          if (a.tiles == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) h[i] = 0;
+          } else if (whole) {
+            uint32_t o[32];
             tile_load32(o, outs + c);
             tile_wait_loads();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 y = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), make_float2(f, f));
+              h[i] = pack_pair<DT == BF16>(y.x, y.y);
+            }
           } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0;
+            tile_load16(h, outs + c);
+            tile_wait_loads();
           }
-          if (again && mine) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c + i < p.dim) o[i] = __float_as_uint(__uint_as_float(o[i]) + cleared_values<F8>(p, it, at.token, from, a.end, c + i));
+          for (int i = 0; i < 4; ++i) *staged(lane, i) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+          if (again && mine) {  // scaling does not change what is infinite or NaN
+#pragma unroll 1
+            for (int i = 0; i < step; ++i) {
+              if (c + i >= p.dim) break;
+              const float v = cleared_values<F8>(p, it, at.token, from, a.end, c + i);
+              if (v == 0.0f) continue;
+              void* const element = reinterpret_cast<char*>(staged(lane, whole ? i >> 3 : i >> 2)) + (whole ? 2 * (i & 7) : 4 * (i & 3));
+              if (whole) store_from_f32(element, DT, 0, load_plain(element, DT, 0) + v);
+              else *reinterpret_cast<float*>(element) += v;
+            }
           }
-          if (whole) {
-            uint32_t h[16];
+          __syncwarp();
+          const bool column = c + piece * (step / 4) < columns;
+          if (out_vectors || !whole) {
+            uint4 z[4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              h[i] = sum == 0.0f ? 0u : pack_pair<DT == BF16>(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) *staged(lane, i) = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-            __syncwarp();
+            for (int i = 0; i < 4; ++i) z[i] = *staged(8 * i + (lane >> 2), piece);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int other = 8 * i + (lane >> 2), col = c + 8 * (lane & 3);
-              uint16_t* const at_other = reinterpret_cast<uint16_t*>(p.out) + __shfl_sync(0xffffffffu, to, other) + col;
-              if (!(given >> other & 1) || col >= p.dim) continue;
-              if (out_vectors) {
-                *reinterpret_cast<uint4*>(at_other) = *staged(other, lane & 3);
-              } else {
-#pragma unroll 1
-                for (int k = 0; k < 8; ++k) at_other[k] = reinterpret_cast<const uint16_t*>(staged(other, lane & 3))[k];
-              }
+              if (column && stores[i]) *reinterpret_cast<uint4*>(at_other[i]) = z[i];
+              at_other[i] += 64;
             }
-            __syncwarp();
           } else {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int k = 16 * half + 4 * i;
-                *staged(lane, i) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-              }
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int other = 8 * i + (lane >> 2);
-                if (given >> other & 1)
-                  *reinterpret_cast<uint4*>(p.sums + (slot - lane + other) * DP + c + 16 * half + 4 * (lane & 3)) = *staged(other, lane & 3);
-              }
-              __syncwarp();
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll 1
+              for (int k = 0; k < 8; ++k)
+                if (column && stores[i]) reinterpret_cast<uint16_t*>(at_other[i])[k] = reinterpret_cast<const uint16_t*>(staged(8 * i + (lane >> 2), piece))[k];
+              at_other[i] += 64;
             }
           }
+          __syncwarp();
         }
         if (begins && !whole) begun = attend_note(share, a.units, a.take);
         tile_fence_before();
@@ -498,7 +505,6 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
         }
       } else {
         // the others bring the queries, and look through values
-        const int mine = tid - 288;
         uint32_t turns = 0, joins = 0;  // phases of `landed`, a bit a slot, and of `cleaned`
         while (share.left > 0) {
           const Part a = part_of(share);
@@ -516,13 +522,28 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
               const int slot = (slots + 2 * j + 1) % SLOTS;
               if (!wait_all(bars.landed[slot], turns >> slot)) goto done;
               turns ^= 1u << slot;
-              const int given = a.end - (a.first + j * S::kKeys);  // entries behind them are other sequences', or nobody's
+              const int given = min(S::kKeys, a.end - (a.first + j * S::kKeys));  // entries behind them are other sequences', or nobody's
               bool any = false;
-              for (int i = mine; i < S::kKeys * CH; i += 96) {
-                const int r = i / CH;
-                uint4* const at = reinterpret_cast<uint4*>(base + (chunk_at(ring_at + slot * S::kTile, r, i % CH) - q_at));
-                if (r >= given) *at = make_uint4(0, 0, 0, 0);
-                else any |= clear_vector<false, BF>(at);
+              // 32 rows a warp, from those on that some row of the queries may not see
+              const int block0 = max(0, (a.open - a.first) - j * S::kKeys) / 32;
+              for (int k = block0 + w - 9; k < 4; k += 3) {
+                char* const rows = base + (ring_at - q_at) + slot * S::kTile + (ch >> 3) * S::kPanel + k * 4096 + (lane / CH) * 128;
+                const int left = given - 32 * k - lane / CH;
+                constexpr int step = 32 / CH;
+                uint32_t bad = 0;
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                  const uint4 v = *reinterpret_cast<const uint4*>(rows + i * step * 128 + ((ch & 7) ^ ((i * step + lane / CH) & 7)) * 16);
+                  bad |= wants_clearing<false, BF>(v) || i * step >= left;
+                }
+                if (bad) {
+#pragma unroll 1
+                  for (int i = 0; i < CH; ++i) {
+                    uint4* const at = reinterpret_cast<uint4*>(rows + i * step * 128 + ((ch & 7) ^ ((i * step + lane / CH) & 7)) * 16);
+                    if (i * step >= left) *at = make_uint4(0, 0, 0, 0);
+                    else any |= clear_vector<false, BF>(at);
+                  }
+                }
               }
               if (any) cleared[item & 3] = item;
               fence_proxy_async();
