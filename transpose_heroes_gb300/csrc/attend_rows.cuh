@@ -29,8 +29,9 @@ struct RowsShape {
   static constexpr int kPitch = DP + 4;                          // of the rows that the warps add up (f32)
   static constexpr int kRows = 16 * MT, kUnit = 4 * kKeys;
   static_assert(kRows * kPitch * 4 <= kWarp, "a warp's output takes the place of its ring");
-  static constexpr int kSmem = 4 * kWarp;
-  static constexpr int kBlocks = kSmem <= 100 * 1024 ? 2 : 1;    // an SM
+  static constexpr int kQueries = MT > 1 ? kRows * (DP * 2 + 16) : 0;  // queries in shared memory: rows 16 bytes apart in the banks
+  static constexpr int kSmem = 4 * kWarp + kQueries;
+  static constexpr int kBlocks = kSmem <= 110 * 1024 ? 2 : 1;    // an SM
 };
 
 // Where 16-byte chunk c of entry r lies in its row: ldmatrix reads eight entries' same chunk, and they fall on different banks.
@@ -80,6 +81,7 @@ __global__ void __launch_bounds__(128, RowsShape<F8, DP, MT>::kBlocks)
   __shared__ AttendScan scan;
   __shared__ float2 stat[4][S::kRows];
   __shared__ uint32_t there[4][STAGES];  // which of a stage's entries exist
+  __shared__ float row_unit[S::kRows];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, quad = lane & 3;
   char* const mine = ring + w * S::kWarp;
   const uint32_t mine_at = attend_smem(mine);
@@ -137,48 +139,75 @@ __global__ void __launch_bounds__(128, RowsShape<F8, DP, MT>::kBlocks)
       look(i + 1);
     }
 
-    // the queries, as the products' left operands
-    uint32_t q[MT][DP / 16][4];
+    // The queries, as the products' left operands: in registers for 16 rows; for 32 in shared memory, in the same order, since
+    // their 64 registers are wanted for the products in flight (32 rows of 128 over codes: MEASURED).
+    constexpr bool kept = MT == 1;
+    uint32_t q[MT][kept ? DP / 16 : 1][4];
     float unit[MT][2];  // a row's scores in units of a factor 2
     int token[MT][2];
+    constexpr int kPitchQ = DP * 2 + 16;
+    char* const q_rows = ring + 4 * S::kWarp;
+    // a row's scale over codes: 2^e <= most < 2^(e + 1), for most of at least 2^-100 (smaller rows' scores vanish all the same)
+    const auto scaled = [&](uint32_t (&v)[DP / 16][2]) {
+      float most = 0.0f;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+      for (int c = 0; c < DP / 16; ++c)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) most = fmaxf(most, fmaxf(fabsf(__uint_as_float(v[c][k] << 16)), fabsf(__uint_as_float(v[c][k] & 0xFFFF0000u))));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      const int e = max((int)(__float_as_uint(most) >> 23) - 127, -100);
+      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+#pragma unroll
+      for (int c = 0; c < DP / 16; ++c)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) v[c][k] = pack_pair<false>(__uint_as_float(v[c][k] << 16) * up, __uint_as_float(v[c][k] & 0xFFFF0000u) * up);
+      return __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+    };
+    const auto load_row = [&](int r, uint32_t (&v)[DP / 16][2]) {  // a lane's part of row r; what its scores are multiplied by
+      const AttendRow at = attend_row(p, it, row0 + r);
+      const uint16_t* const row =
+          r < rows ? reinterpret_cast<const uint16_t*>(p.q) + it.b * p.q_stride[0] + at.token * p.q_stride[1] + at.head * p.q_stride[2] : nullptr;
+#pragma unroll
+      for (int c = 0; c < DP / 16; ++c) {
+        v[c][0] = query_pair(row, 16 * c + (F8 ? 4 * quad : 2 * quad), p.dim, q_words);
+        v[c][1] = query_pair(row, 16 * c + (F8 ? 4 * quad + 2 : 2 * quad + 8), p.dim, q_words);
+      }
+      if constexpr (DT == BF16 && F8) return p.score_scale * scaled(v);
+      return p.score_scale;
+    };
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) token[m][h] = attend_row(p, it, row0 + 16 * m + g + 8 * h).token;
+    if constexpr (kept) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = 16 * m + g + 8 * h;
-        const AttendRow at = attend_row(p, it, row0 + r);
-        token[m][h] = at.token;
-        unit[m][h] = p.score_scale;
-        const uint16_t* const row =
-            r < rows ? reinterpret_cast<const uint16_t*>(p.q) + it.b * p.q_stride[0] + at.token * p.q_stride[1] + at.head * p.q_stride[2] : nullptr;
+        uint32_t v[DP / 16][2];
+        unit[0][h] = load_row(g + 8 * h, v);
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) q[0][c][h] = v[c][0], q[0][c][h + 2] = v[c][1];
+      }
+    } else {  // each warp brings 4 MT rows
+#pragma unroll
+      for (int k = 0; k < S::kRows / 32; ++k) {
+        uint32_t v[DP / 16][2];
+        const int r = 8 * (w + 4 * k) + g;
+        const float u = load_row(r, v);
+        if (quad == 0) row_unit[r] = u;
 #pragma unroll
         for (int c = 0; c < DP / 16; ++c) {
-          q[m][c][h] = query_pair(row, 16 * c + (F8 ? 4 * quad : 2 * quad), p.dim, q_words);
-          q[m][c][h + 2] = query_pair(row, 16 * c + (F8 ? 4 * quad + 2 : 2 * quad + 8), p.dim, q_words);
-        }
-        if constexpr (DT == BF16 && F8) {
-          float most = 0.0f;
-#pragma unroll
-          for (int c = 0; c < DP / 16; ++c) {
-#pragma unroll
-            for (int k = h; k < 4; k += 2)
-              most = fmaxf(most, fmaxf(fabsf(__uint_as_float(q[m][c][k] << 16)), fabsf(__uint_as_float(q[m][c][k] & 0xFFFF0000u))));
-          }
-          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-          // 2^e <= most < 2^(e + 1), for most of at least 2^-100 (smaller rows' scores vanish all the same)
-          const int e = max((int)(__float_as_uint(most) >> 23) - 127, -100);
-          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-          unit[m][h] *= __uint_as_float((uint32_t)(127 - 14 + e) << 23);
-#pragma unroll
-          for (int c = 0; c < DP / 16; ++c) {
-#pragma unroll
-            for (int k = h; k < 4; k += 2)
-              q[m][c][k] = pack_pair<false>(__uint_as_float(q[m][c][k] << 16) * up, __uint_as_float(q[m][c][k] & 0xFFFF0000u) * up);
-          }
+          *reinterpret_cast<uint32_t*>(q_rows + r * kPitchQ + 32 * c + 4 * quad) = v[c][0];
+          *reinterpret_cast<uint32_t*>(q_rows + r * kPitchQ + 32 * c + 16 + 4 * quad) = v[c][1];
         }
       }
+      __syncthreads();
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) unit[m][h] = row_unit[16 * m + g + 8 * h];
     }
+    const uint32_t q_lane = attend_smem(q_rows) + ((lane & 7) + ((lane >> 3) & 1) * 8) * kPitchQ + (lane >> 4) * 16;
 
     float o[MT][DP / 8][4], top[MT][2], sum[MT][2];
 #pragma unroll
@@ -206,14 +235,23 @@ __global__ void __launch_bounds__(128, RowsShape<F8, DP, MT>::kBlocks)
         for (int t = 0; t < NT; ++t) x[m][t][0] = x[m][t][1] = x[m][t][2] = x[m][t][3] = 0.0f;
 #pragma unroll
       for (int c = 0; c < DP / 16; ++c) {
-        uint32_t b[4];
+        uint32_t b[4], a[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if constexpr (kept) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) a[m][k] = q[m][c][k];
+          } else {
+            ldmatrix4(a[m], q_lane + 16 * m * kPitchQ + 32 * c);
+          }
+        }
         if constexpr (F8) {
           ldmatrix4(b, ks + lane * ROW + rows_chunk<ROW>(lane, c) * 16);
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             const uint32_t b0 = f16_of_codes(b[t]), b1 = f16_of_codes(b[t] >> 16);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) mma16<BF>(x[m][t], q[m][c], b0, b1);
+            for (int m = 0; m < MT; ++m) mma16<BF>(x[m][t], a[m], b0, b1);
           }
         } else {
 #pragma unroll
@@ -222,8 +260,8 @@ __global__ void __launch_bounds__(128, RowsShape<F8, DP, MT>::kBlocks)
             ldmatrix4(b, ks + r * ROW + rows_chunk<ROW>(r, 2 * c + ((lane >> 3) & 1)) * 16);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-              mma16<BF>(x[m][2 * k], q[m][c], b[0], b[1]);
-              mma16<BF>(x[m][2 * k + 1], q[m][c], b[2], b[3]);
+              mma16<BF>(x[m][2 * k], a[m], b[0], b[1]);
+              mma16<BF>(x[m][2 * k + 1], a[m], b[2], b[3]);
             }
           }
         }

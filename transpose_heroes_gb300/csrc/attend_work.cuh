@@ -64,7 +64,14 @@ __device__ __forceinline__ int64_t attend_units_of(const AttendPlan& p, int b) {
   AttendItem it;
   it.b = b;
   attend_sequence<M>(p, it);
+  if (it.tiles == 1) return (int64_t)attend_units<M, N>(p, it, 0) * p.kv;
   return attend_units_upto<M, N>(p, it, it.tiles) * p.kv;
+}
+
+// a / b for a >= 0, b > 0; nearly always of 32 bits, which is several times shorter.
+static __device__ __noinline__ int64_t attend_divide_long(int64_t a, int64_t b) { return a / b; }
+__device__ __forceinline__ int64_t attend_divide(int64_t a, int64_t b) {
+  return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : attend_divide_long(a, b);
 }
 
 // A block's stretch: `left` units, the first of them unit `unit` of tile `it`; per: units a block.
@@ -98,7 +105,7 @@ __device__ __forceinline__ AttendShare attend_share(const AttendPlan& p, AttendS
   for (int i = 0; i < W; ++i) all += s.warp[i];
   __syncthreads();
   AttendShare r;
-  const int64_t per = max((int64_t)1, (all + gridDim.x - 1) / gridDim.x), start = blockIdx.x * per;
+  const int64_t per = max((int64_t)1, attend_divide(all + gridDim.x - 1, gridDim.x)), start = blockIdx.x * per;
   r.per = (int)per;
   r.left = (int)max((int64_t)0, min(per, all - start));
   r.unit = 0;
@@ -130,18 +137,27 @@ __device__ __forceinline__ AttendShare attend_share(const AttendPlan& p, AttendS
   r.it.b = s.b;
   attend_sequence<M>(p, r.it);
   int64_t off = s.at;
+  r.it.tile = 0;
+  if (r.it.tiles <= 1) {
+    const int u = attend_units<M, N>(p, r.it, 0);
+    r.it.head = (int)attend_divide(off, u);
+    r.unit = (int)(off - (int64_t)r.it.head * u);
+    return r;
+  }
   const int64_t one = max((int64_t)1, attend_units_upto<M, N>(p, r.it, r.it.tiles));
-  r.it.head = (int)(off / one);
+  r.it.head = (int)attend_divide(off, one);
   off -= r.it.head * one;
-  // the last tile that begins at or before `off`
-  int lo = 0, hi = max(1, r.it.tiles);
+  // the last tile that begins at or before `off`, and what lies before it
+  int lo = 0, hi = r.it.tiles;
+  int64_t before = 0;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (attend_units_upto<M, N>(p, r.it, mid) <= off) lo = mid;
+    const int64_t upto = attend_units_upto<M, N>(p, r.it, mid);
+    if (upto <= off) lo = mid, before = upto;
     else hi = mid;
   }
   r.it.tile = lo;
-  r.unit = (int)(off - attend_units_upto<M, N>(p, r.it, lo));
+  r.unit = (int)(off - before);
   return r;
 }
 
