@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(128, RowsShape<F8, DP, MT>::kBlocks)
   const uint32_t mine_at = attend_smem(mine);
   wait_for_last();
   AttendShare share = attend_share<S::kRows, S::kUnit, 128>(p, scan);
+  allow_next();  // every block runs from the start, so the join takes nobody's place
   int4 begun = make_int4(-1, 0, 0, 0);
   constexpr int EB = F8 ? 1 : 2;
   while (share.left > 0) {
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(128, RowsShape<F8, DP, MT>::kBlocks)
         to[3] = (uint16_t)(hi >> 16);
       }
     }
-    if (!whole && begins) begun = attend_note(share, units, take);
+    if (!whole && begins) begun = attend_note(share, units, take, rows);
     __syncthreads();
     share.left -= take;
     share.unit += take;
@@ -436,7 +437,6 @@ __global__ void __launch_bounds__(128, RowsShape<F8, DP, MT>::kBlocks)
     }
   }
   if (tid == 0) p.shares[blockIdx.x] = begun;
-  allow_next();
 }
 
 template <int DT, bool F8, int DP, int MT>

@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
           }
           __syncwarp();
         }
-        if (begins && !whole) begun = attend_note(share, a.units, a.take);
+        if (begins && !whole) begun = attend_note(share, a.units, a.take, a.rows);
         tile_fence_before();
       }
       advance(share, a);

@@ -192,8 +192,8 @@ __device__ __forceinline__ int attend_open(const AttendPlan& p, const AttendItem
 
 // The note for the join of a tile that begins in this block and ends in another, and a stretch's slot where it is not a whole
 // tile's work. The block that notes it ends where its share does.
-__device__ __forceinline__ int4 attend_note(const AttendShare& s, int units, int take) {
-  return make_int4(s.it.b, s.it.head, s.it.tile, (int)blockIdx.x + (units - take + s.per - 1) / s.per);
+__device__ __forceinline__ int4 attend_note(const AttendShare& s, int units, int take, int rows) {
+  return make_int4(s.it.b, s.it.head | rows << 16, s.it.tile, (int)blockIdx.x + (units - take + s.per - 1) / s.per);
 }
 __device__ __forceinline__ int attend_slot(bool begins) { return 2 * (int)blockIdx.x + (begins ? 1 : 0); }
 

@@ -8,48 +8,58 @@ namespace hlo {
 
 // ---- the join --------------------------------------------------------------------------------------------------
 // Block (c, y) adds up the tile that block c of the attention began and did not finish, if there is one: a row at a time,
-// its four warps taking every fourth block's share, with weights 2^(m_i - max m). Bound: the latency of two dependent
-// rounds of loads.
-constexpr int kJoinCols = 8;  // of 32: 256 columns at most
+// its four warps taking every fourth block's share, with weights 2^(m_i - max m). The shares' sums are requested before
+// their weights are known. Bound: the latency of two dependent loads, of the note and of what it points to.
+template <int COLS>
 __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendPlan p, int m, int cols) {
-  __shared__ float part[4][kJoinCols * 32];
+  __shared__ float part[4][COLS * 32];
   follow();
   const int4 share = p.shares[blockIdx.x];
   if (share.x < 0) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   AttendItem it;
   it.b = share.x;
-  it.head = share.y;
+  it.head = share.y & 0xFFFF;
   it.tile = share.z;
-  it.count = cache_count(p.m, it.b);
-  const int row0 = it.tile * m, rows = min(m, it.count * p.group - row0);
+  const int row0 = it.tile * m, rows = share.y >> 16;
   const int n = share.w - (int)blockIdx.x + 1;  // blocks
+  const float none = __int_as_float(0xFF800000);
   const auto slot = [&](int i) { return i == 0 ? 2 * (int64_t)blockIdx.x + 1 : 2 * ((int64_t)blockIdx.x + i); };
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    float top = __int_as_float(0xFF800000);
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, p.stats[slot(i) * m + r].x);
+    float acc[COLS], top = none, l = 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float base = top == __int_as_float(0xFF800000) ? 0.0f : top;
-    float l = 0.0f;
-    for (int i = lane; i < n; i += 32) {
-      const float2 s = p.stats[slot(i) * m + r];
-      l = fmaf(exp2f(s.x - base), s.y, l);
+    for (int j = 0; j < COLS; ++j) acc[j] = 0.0f;
+    for (int i0 = 0; i0 < n; i0 += 32) {  // 32 blocks at a time, each warp eight of them
+      float z[8][COLS];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + w + 4 * k;
+#pragma unroll
+        for (int j = 0; j < COLS; ++j)
+          z[k][j] = i < n && lane + 32 * j < cols ? p.sums[(slot(i) * m + r) * cols + lane + 32 * j] : 0.0f;
+      }
+      const float2 s = i0 + lane < n ? p.stats[slot(i0 + lane) * m + r] : make_float2(none, 0.0f);
+      float next = s.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, o));
+      next = fmaxf(next, top);
+      const float base = next == none ? 0.0f : next;
+      const float f = exp2f(s.x - base), old = exp2f(top - base);
+      l = fmaf(l, old, warp_sum(f * s.y));
+      top = next;
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) acc[j] *= old;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float g = __shfl_sync(0xffffffffu, f, w + 4 * k);
+        if (i0 + w + 4 * k < n) {
+#pragma unroll
+          for (int j = 0; j < COLS; ++j) acc[j] = fmaf(g, z[k][j], acc[j]);
+        }
+      }
     }
-    l = warp_sum(l);
-    float acc[kJoinCols];
 #pragma unroll
-    for (int j = 0; j < kJoinCols; ++j) acc[j] = 0.0f;
-#pragma unroll 4
-    for (int i = w; i < n; i += 4) {
-      const int64_t at = slot(i) * m + r;
-      const float f = exp2f(p.stats[at].x - base);
-#pragma unroll
-      for (int j = 0; j < kJoinCols; ++j)
-        if (lane + 32 * j < cols) acc[j] = fmaf(f, p.sums[at * cols + lane + 32 * j], acc[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < kJoinCols; ++j) part[w][lane + 32 * j] = acc[j];
+    for (int j = 0; j < COLS; ++j) part[w][lane + 32 * j] = acc[j];
     __syncthreads();
     const AttendRow at = attend_row(p, it, row0 + r);
     const float f = l == 0.0f ? 0.0f : p.value_scale / l;
@@ -63,7 +73,8 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 
 cudaError_t launch_attend_join(const AttendPlan& p, int m, int cols, int blocks, cudaStream_t s) {
   const int rows = (int)std::min<int64_t>({(int64_t)p.m.seq * p.group, m, 32});
-  return launch_after(attend_join_kernel, dim3((unsigned)blocks, (unsigned)rows), dim3(128), 0, s, 1, p, m, cols);
+  const auto kernel = cols <= 64 ? attend_join_kernel<2> : cols <= 128 ? attend_join_kernel<4> : attend_join_kernel<8>;
+  return launch_after(kernel, dim3((unsigned)blocks, (unsigned)rows), dim3(128), 0, s, 1, p, m, cols);
 }
 
 // ---- any type, size and alignment ----------------------------------------------------------------------------------
@@ -90,6 +101,7 @@ __global__ void __launch_bounds__(128) attend_any_kernel(const __grid_constant__
   for (int i = tid; i < (kAnyRows + 2 * kAnyKeys) * pitch; i += 128) mem[i] = 0.0f;  // the columns behind dim stay 0
   wait_for_last();
   AttendShare share = attend_share<kAnyRows, kAnyKeys, 128>(p, scan);
+  allow_next();  // every block runs from the start, so the join takes nobody's place
   int4 begun = make_int4(-1, 0, 0, 0);
   while (share.left > 0) {
     const AttendItem it = share.it;
@@ -190,7 +202,7 @@ __global__ void __launch_bounds__(128) attend_any_kernel(const __grid_constant__
     } else {
       const int64_t slot = attend_slot(begins);
       if (tid < kAnyRows) p.stats[slot * kAnyRows + tid] = stat[tid];
-      if (begins) begun = attend_note(share, units, take);
+      if (begins) begun = attend_note(share, units, take, rows);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -217,7 +229,6 @@ __global__ void __launch_bounds__(128) attend_any_kernel(const __grid_constant__
     }
   }
   if (tid == 0) p.shares[blockIdx.x] = begun;
-  allow_next();
 }
 
 static size_t any_smem(int64_t dim) { return (kAnyRows + 2 * kAnyKeys) * ((dim + 3) / 4 * 4 + 4) * sizeof(float); }
