@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
 
   if (w < 8) {
     // ---- the softmax ----------------------------------------------------------------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F8 ? 160 : 168));
     const int s = w >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (w & 3)) << 16;
     const uint32_t scores = tmem + lanes + S::kScores * s, outs = tmem + lanes + 256 + DP * s;
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
     }
   } else if (w < 12) {
     // ---- the copies -----------------------------------------------------------------------------------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F8 ? 120 : 104));
     constexpr int EB = F8 ? 1 : 2;
     const int pw = w - 8, ch = lane % CH;
     uint32_t slots = 0;                  // slots filled so far
@@ -624,6 +624,73 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
         // keys and values
         const char* const kbase = reinterpret_cast<const char*>(p.k) + it.head * p.k_stride[2] * EB;
         const char* const vbase = reinterpret_cast<const char*>(p.v) + it.head * p.v_stride[2] * EB;
+        if constexpr (F8) {
+          // 16 codes become two chunks of f16 on their way through registers: while a tile's keys are converted its values are
+          // coming, and then the next tile's keys
+          constexpr int CC = DP / 16;
+          const int cc = lane % CC;
+          const bool column = 16 * cc < p.dim;
+          uint32_t given = 0;
+          int64_t ko = 0, vo = 0;
+          const auto resolve = [&](int j) {
+            page = cache_page(p.m, page);
+            given = __ballot_sync(0xffffffffu, page >= 0);
+            ko = page * p.k_stride[0] + place * p.k_stride[1];
+            vo = same_strides ? ko : page * p.v_stride[0] + place * p.v_stride[1];
+            look(j + 1);
+          };
+          const auto fetch = [&](uint4 (&v)[CC], const char* from, int64_t off) {
+#pragma unroll
+            for (int i = 0; i < CC; ++i) {
+              const int e = i * (32 / CC) + lane / CC;
+              const int64_t o = __shfl_sync(0xffffffffu, off, e);
+              v[i] = column && (given >> e & 1) ? *reinterpret_cast<const uint4*>(from + o + cc * 16) : make_uint4(0, 0, 0, 0);
+            }
+          };
+          const auto put = [&](const uint4 (&v)[CC], bool look_through) {
+            const int slot = slots % SLOTS;
+            if (slots >= SLOTS && !wait_all(bars.kv_empty[slot], slots / SLOTS - 1)) return false;
+            ++slots;
+            const uint32_t tile = ring_at + slot * S::kTile;
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < CC; ++i) {
+              const int r = 32 * pw + i * (32 / CC) + lane / CC;
+              uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+              if (look_through && wants_clearing<true, false>(v[i])) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) any |= clear_word<true, false>(u[k]);
+              }
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<uint4*>(base + (chunk_at(tile, r, 2 * cc + k) - q_at)) =
+                    make_uint4(f16_of_codes(u[2 * k]), f16_of_codes(u[2 * k] >> 16), f16_of_codes(u[2 * k + 1]), f16_of_codes(u[2 * k + 1] >> 16));
+            }
+            if (any) cleared[item & 3] = item;
+            fence_proxy_async();
+            mbar_arrive(bar(bars.kv_full[slot]));
+            return true;
+          };
+          uint4 keys[CC], values[CC];
+          resolve(0);
+          fetch(keys, kbase, ko);
+          fetch(values, vbase, vo);
+          for (int j = 0; j < a.tiles; ++j) {
+            if (lane == 0) there[(tile0 + j) & 7][pw] = given;
+            if (!put(keys, false)) goto done;
+            if (j == 0) {
+              if (!queries()) goto done;
+              flush();
+            }
+            const bool more = j + 1 < a.tiles;
+            if (more) {
+              resolve(j + 1);
+              fetch(keys, kbase, ko);
+            }
+            if (!put(values, a.first + (j + 1) * S::kKeys > a.open)) goto done;
+            if (more) fetch(values, vbase, vo);
+          }
+        } else {
         for (int j = 0; j < a.tiles; ++j) {
           page = cache_page(p.m, page);
           const uint32_t given = __ballot_sync(0xffffffffu, page >= 0);
@@ -645,7 +712,7 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
             ++slots;
             const uint32_t tile = ring_at + slot * S::kTile;
             const char* const from = side ? vbase : kbase;
-            if constexpr (!F8) {
+            {
               // row e = i (32 / CH) + lane / CH of the warp's 32: its place in shared memory repeats every CH / 4 steps, but for the step
               const bool column = 8 * ch < p.dim;
               uint32_t to[CH / 4];
@@ -668,38 +735,9 @@ __global__ void __launch_bounds__(512, 1) attend_tile_kernel(const __grid_consta
                 }
               }
               sent(bar(bars.kv_full[slot]), side && hides ? tile : 0, item);
-            } else {
-              // 16 codes become two chunks of f16
-              constexpr int CC = DP / 16;
-              const int cc = lane % CC;
-              const bool column = 16 * cc < p.dim;
-              uint4 got[CC];
-#pragma unroll
-              for (int i = 0; i < CC; ++i) {
-                const int e = i * (32 / CC) + lane / CC;
-                const int64_t o = __shfl_sync(0xffffffffu, off[side], e);
-                got[i] = column && (given >> e & 1) ? *reinterpret_cast<const uint4*>(from + o + cc * 16) : make_uint4(0, 0, 0, 0);
-              }
-              flush();  // the queries
-              bool any = false;
-#pragma unroll
-              for (int i = 0; i < CC; ++i) {
-                const int r = 32 * pw + i * (32 / CC) + lane / CC;
-                uint32_t u[4] = {got[i].x, got[i].y, got[i].z, got[i].w};
-                if (side && hides) {
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) any |= clear_word<true, false>(u[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                  *reinterpret_cast<uint4*>(base + (chunk_at(tile, r, 2 * cc + k) - q_at)) =
-                      make_uint4(f16_of_codes(u[2 * k]), f16_of_codes(u[2 * k] >> 16), f16_of_codes(u[2 * k + 1]), f16_of_codes(u[2 * k + 1] >> 16));
-              }
-              if (any) cleared[item & 3] = item;
-              fence_proxy_async();
-              mbar_arrive(bar(bars.kv_full[slot]));
             }
           }
+        }
         }
       }
       advance(share, a);

@@ -54,6 +54,9 @@ struct AttendPlan {
   float* sums;             // 2 a block: each row's unnormalised output
 };
 cudaError_t launch_attend(AttendPlan p, void* workspace, cudaStream_t s);
+// f32 queries; entries on 16-byte boundaries.
+cudaError_t launch_attend_f32(AttendPlan& p, void* workspace, cudaStream_t s);
+cudaError_t launch_attend_f32_f8(AttendPlan& p, void* workspace, cudaStream_t s);
 // Few rows a key head, by the types of the queries and of the cache; entries on 16-byte boundaries.
 cudaError_t launch_attend_rows_bf16(AttendPlan& p, void* workspace, cudaStream_t s);
 cudaError_t launch_attend_rows_bf16_f8(AttendPlan& p, void* workspace, cudaStream_t s);

@@ -79,8 +79,8 @@ cudaError_t launch_attend_join(const AttendPlan& p, int m, int cols, int blocks,
 
 // ---- any type, size and alignment ----------------------------------------------------------------------------------
 // Tiles of 16 rows, 32 entries at a time, in f32 in shared memory. A warp has four rows: each lane one entry's four
-// products; then a thread has one or two columns of all 16 rows. f32 tensors always come here: products of f32 have
-// no matrix instruction that keeps their 24 bits. Bound: the FMA pipe and shared memory (five 16-byte reads for 16 FMAs).
+// products; then a thread has one or two columns of all 16 rows. Entries that do not lie on 16-byte boundaries come here. Bound: the
+// latency of its loads, element by element.
 constexpr int kAnyRows = 16, kAnyKeys = 32;
 
 __device__ __forceinline__ float attend_load(const void* p, int dt, int f8, int64_t i) {
@@ -248,7 +248,7 @@ static cudaError_t run_any(AttendPlan& p, void* ws, cudaStream_t s) {
 
 // Whether entries can be copied 16 bytes at a time.
 static bool aligned_entries(const AttendPlan& p) {
-  const int64_t eb = p.f8 ? 1 : 2;
+  const int64_t eb = p.f8 ? 1 : dt_bytes(p.dt);
   uintptr_t bits = (uintptr_t)p.k | (uintptr_t)p.v | (uintptr_t)(p.dim * eb);
   for (int d = 0; d < 3; ++d) bits |= (uintptr_t)(p.k_stride[d] * eb) | (uintptr_t)(p.v_stride[d] * eb);
   return bits % 16 == 0;
@@ -267,7 +267,8 @@ size_t attend_workspace(int64_t batch, int64_t seq, int64_t heads, int64_t kv, i
 }
 
 cudaError_t launch_attend(AttendPlan p, void* ws, cudaStream_t s) {
-  if (p.dt == F32 || !aligned_entries(p)) return run_any(p, ws, s);
+  if (!aligned_entries(p)) return run_any(p, ws, s);
+  if (p.dt == F32) return p.f8 ? launch_attend_f32_f8(p, ws, s) : launch_attend_f32(p, ws, s);
   if (many_rows((int64_t)p.m.seq * p.group, p.dim)) {
     if (p.dt == BF16) return p.f8 ? launch_attend_tile_bf16_f8(p, ws, s) : launch_attend_tile_bf16(p, ws, s);
     return p.f8 ? launch_attend_tile_f16_f8(p, ws, s) : launch_attend_tile_f16(p, ws, s);
