@@ -255,6 +255,20 @@ def test_pages_that_are_not_there(dtype, cache, seq):
         assert bool(((lse[0].double().cpu() - wlse).abs() <= elen).all())
 
 
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("seq", [1, 40])
+def test_a_cache_without_pages(dtype, cache, seq):
+    """Nothing can be written to it, and nobody sees anything."""
+    c = [torch.empty(0, 16, 2, 64, dtype=ref.DT[cache], device=DEV) for _ in range(2)]
+    q = ref.normal(np.random.default_rng(1), (2, seq, 4, 64), dtype).to(DEV)
+    for width in (0, 3):
+        table, lengths = torch.zeros(2, width, dtype=torch.int32, device=DEV), torch.tensor([0, 20], dtype=torch.int32, device=DEV)
+        lse = torch.zeros(2, seq, 4, device=DEV)
+        hf.cache_append(q[:, :, :2], q[:, :, 2:], *c, table, lengths)
+        out = hf.cache_attention(q, *c, table, lengths, torch.full_like(q, 7.0), lse=lse, workspace=workspace(q, 2))
+        assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+
+
 def test_lengths_outside_the_cache():
     """Clamped: negative lengths are 0, and entries behind the table's pages are seen by nobody."""
     rng = np.random.default_rng(21)
@@ -571,3 +585,42 @@ def test_versions_move():
     hf.cache_append(q[:, :, :1], q[:, :, :1], c.k, c.v, c.table, c.len)
     hf.cache_attention(q, c.k, c.v, c.table, c.len, out, workspace=ws)
     assert all(t._version > o for t, o in zip((c.k, c.v, out, ws), old))
+
+
+def test_the_binding_refuses_other_tensors(monkeypatch):
+    """With the launch switched off: nothing that should have been refused reaches the device."""
+    monkeypatch.setenv("HLOFUSION_FAULT", "all")
+    new = lambda *s, t=torch.float32: torch.zeros(*s, dtype=t, device=DEV)  # noqa: E731
+    i32 = torch.int32
+    base = dict(q=new(2, 3, 4, 16), k=new(9, 4, 2, 16), v=new(9, 4, 2, 16), table=new(2, 5, t=i32), lengths=new(2, t=i32), out=new(2, 3, 4, 16),
+                ws=new(1 << 24, t=torch.uint8))
+
+    def attention(counts=None, mask=None, lse=None, **kw):
+        a = {**base, **kw}
+        return hf.cache_attention(a["q"], a["k"], a["v"], a["table"], a["lengths"], a["out"], counts=counts, mask=mask, lse=lse, workspace=a["ws"])
+
+    def status(call):
+        with pytest.raises(hf.HloError) as e:
+            call()
+        return e.value.status
+
+    assert status(attention) == 3
+    i64 = torch.int64
+    for kw in (dict(lengths=new(2, t=i64)), dict(lengths=new(3, t=i32)), dict(lengths=None), dict(table=new(2, 5, t=i64)), dict(counts=new(2, t=i64)),
+               dict(counts=new(4, t=i32)[::2]), dict(mask=new(2, 3, 1, t=i64)), dict(lse=new(2, 3, 3)), dict(lse=new(2, 3, 4, t=torch.float16)),
+               dict(q=new(2, 3, 4, 16).cpu()), dict(k=new(9, 4, 2, 16, t=torch.float64)), dict(ws=new(1 << 24, t=torch.uint8).cpu()),
+               dict(lengths=new(2, t=i32).cpu()), dict(k=None)):
+        assert status(lambda: attention(**kw)) == 1, kw
+    assert status(lambda: attention(ws=new(16, t=torch.uint8))) == 4
+    q, k = base["q"], new(2, 3, 2, 16)
+    append = lambda **kw: hf.cache_append(k, k, base["k"], base["v"], base["table"], base["lengths"], **kw)  # noqa: E731
+    assert status(append) == 3 and status(lambda: append(q=q, q_out=base["out"], turns=new(8, t=i64))) == 3
+    for kw in (dict(turns=new(8)), dict(turns=new(9, t=i64)), dict(turns=new(8, t=i64), n_pairs=9), dict(positions=new(2, 3, t=i64)), dict(q=q),
+               dict(counts=new(3, t=i32))):
+        assert status(lambda: append(**kw)) == 1, kw
+    t = [new(2, 3, t=i32) for _ in range(4)]
+    accept = lambda a, n, **kw: hf.tree_accept(*t, a, n, **kw)  # noqa: E731
+    one, two = new(2, t=i32), new(2, t=i32)
+    assert status(lambda: accept(one, two)) == 3
+    assert status(lambda: accept(one, new(2, t=i64))) == 1 and status(lambda: accept(one, new(3, t=i32))) == 1
+    assert status(lambda: accept(one, two, k_cache=base["k"])) == 1

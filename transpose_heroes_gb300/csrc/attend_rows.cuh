@@ -6,9 +6,11 @@
 // 2^(m_w - m). m moves only where a score exceeds it by 2^8: until then the weights are at most 256, exact in f32 sums and
 // no worse rounded, and o need not be rescaled.
 //
-// Bound: HBM. Each entry is read once and multiplied by at most 32 rows (32 flops a byte): mma.sync is enough (it
-// has the place of a fifth of the SM's cycles at this rate), and needs no accumulators in tensor memory, whose tiles
-// of 128 rows would be mostly empty.
+// Bound: HBM. Each entry is read once and multiplied by at most 32 rows (32 flops a byte): mma.sync is enough (a
+// quarter of its rate), and needs no accumulators in tensor memory, whose tiles of 128 rows would be mostly empty. bf16, 8 key
+// heads of 128, 4 query heads each: 64 sequences to 8192 entries (1356 MB) 210 us, 95% of the copy rate; 32 rows (16 sequences
+// to 16384, 8 new tokens, 700 MB) 133 us, 77%. Over codes the conversions bound it: 134 us for those 64 sequences' 679 MB, 198 us for
+// 32 rows of 687 MB, where two warps a scheduler issue 0.3 instructions a cycle, waiting for one another's results.
 //
 // An 8-bit cache is converted to f16 in registers, which holds its codes exactly: ldmatrix hands a thread four neighbouring
 // codes of a key, so the products run over the head's elements in an order of their own, which the queries' registers
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(128, RowsShape<F8, DP, MT>::kBlocks)
     }
 
     // The queries, as the products' left operands: in registers for 16 rows; for 32 in shared memory, in the same order, since
-    // their 64 registers are wanted for the products in flight (32 rows of 128 over codes: MEASURED).
+    // their 64 registers are wanted for the products in flight (32 rows of 128 over codes, 687 MB: 198 us, 259 with all in registers, of which some were spilled).
     constexpr bool kept = MT == 1;
     uint32_t q[MT][kept ? DP / 16 : 1][4];
     float unit[MT][2];  // a row's scores in units of a factor 2

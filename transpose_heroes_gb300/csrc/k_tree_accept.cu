@@ -16,7 +16,8 @@ struct Move {
 // look at once for the parent that would choose them (the lowest child wins), so that the walk is a chase through shared
 // memory. A thread moves its column's entries in the path's order, eight loads before their eight stores: entry i goes to
 // a place that no later entry comes from (path[j] >= j > i), so nothing is overwritten before it is read.
-// Bound: latency; 16 layers, 1 x 3 moved entries (0.39 MB): see the table of measured cases.
+// Bound: the latency of a chain of dependent loads (parent, pick, page, entry): 16 nodes and 16 layers' 3 entries 3.3 us in a
+// captured graph; 64 sequences, 34 MB moved, 9.9 us, half of the copy rate.
 template <typename W>
 __global__ void __launch_bounds__(256) accept_kernel(const __grid_constant__ AcceptPlan p, int columns, int per_block) {
   extern __shared__ int nodes[];  // [seq] the child that each node chooses, [seq] the path, then the moves
