@@ -151,6 +151,45 @@ def test_many_sequences():
     attend(rng, [int(x) for x in rng.integers(0, 40, n)], [int(x) for x in rng.integers(0, 3, n)], 2, 4, 2, 64, 16, "bf16")
 
 
+@pytest.mark.parametrize("dtype,cache,page", [("bf16", "bf16", 16), ("f16", "f16", 7), ("bf16", "f8", 16), ("f32", "f32", 16)])
+def test_masks_of_several_tiles(dtype, cache, page):
+    """Trees and arbitrary masks wider than a tile of entries, whose words begin anywhere in it."""
+    for tree in ("tree", "random"):
+        attend(np.random.default_rng(50), [100, 7, 0], [300, 211, 129], 300, 4, 2, 64, page, dtype, cache, tree)
+
+
+@pytest.mark.parametrize("dtype,cache,page", [("bf16", "bf16", 16), ("f16", "f16", 5), ("bf16", "f8", 16), ("f32", "f32", 8)])
+@pytest.mark.parametrize("tree", ["causal", "tree"])
+def test_tokens_that_have_no_room(dtype, cache, page, tree):
+    """New tokens behind the table's pages are seen by nobody, and see what is there."""
+    rng = np.random.default_rng(51)
+    seq, n = 40, 150
+    c = ref.filled(rng, [n], [seq], seq, 2, 64, page, cache, DEV)
+    room = c.width - -(-25 // page)  # pages: some of the new tokens are left out
+    cap = room * page
+    q = ref.normal(rng, (1, seq, 8, 64), dtype).to(DEV)
+    sees = np.tril(np.ones((seq, seq), bool)) if tree == "causal" else ref.sees_of(ref.random_tree(rng, seq))
+    mask = None if tree == "causal" else ref.packed(sees).to(DEV)
+    for length in (n, cap - 3, cap, cap + 100):
+        out, lse = torch.empty_like(q), torch.empty(1, seq, 8, device=DEV)
+        hf.cache_attention(q, c.k, c.v, c.table[:, :room], torch.tensor([length], dtype=torch.int32, device=DEV), out, mask=mask, lse=lse,
+                           workspace=workspace(q, 2))
+        old = min(length, cap)
+        k, v = c.get(0, range(cap))
+        full = np.concatenate([np.ones((seq, old), bool), sees], 1)[:, :cap]
+        want, wlse, bound, elen = ref.attention(q[0].double().cpu(), k, v, full, 0.125)
+        weights = None if dtype == "f32" else "f16" if cache == "f8" else dtype
+        assert bool(((out[0].double().cpu() - want).abs() <= bound(weights) + 2 * ref.rounding(want, dtype)).all())
+        assert bool(((lse[0].double().cpu() - wlse).abs() <= elen).all())
+
+
+@pytest.mark.parametrize("page", [16, 5])
+def test_many_sequences_of_many_rows(page):
+    rng = np.random.default_rng(52)
+    n = 560
+    attend(rng, [int(x) for x in rng.integers(0, 60, n)], [int(x) for x in rng.integers(0, 18, n)], 17, 4, 2, 64, page, "bf16")
+
+
 @pytest.mark.parametrize("dtype,cache,seq", [("bf16", "bf16", 4), ("bf16", "bf16", 40), ("f16", "f8", 4), ("f16", "f8", 40), ("f32", "f32", 4)])
 def test_sharp_weights_and_far_maxima(dtype, cache, seq):
     """Scores of many hundreds: the running maximum moves often and far."""
@@ -192,7 +231,8 @@ def test_rows_that_see_nothing():
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("dtype,cache,seq", [("bf16", "bf16", 6), ("bf16", "bf16", 60), ("f16", "f16", 60), ("f16", "f8", 6), ("bf16", "f8", 60),
                                              ("f32", "f32", 6)])
-def test_what_is_not_seen_does_not_matter(bad, dtype, cache, seq):
+@pytest.mark.parametrize("page", [16, 7])
+def test_what_is_not_seen_does_not_matter(page, bad, dtype, cache, seq):
     """A NaN or infinite key and value of one drafted node: only the rows that see it change."""
     if cache == "f8":
         bad = math.nan
@@ -207,12 +247,28 @@ def test_what_is_not_seen_does_not_matter(bad, dtype, cache, seq):
                         k, v = (torch.full((1, 2, 64), bad) for _ in range(2))
                         c.put(i, [n + node], k, v)
 
-            runs.append(attend(np.random.default_rng(18), [0, 50, 130], [seq] * 3, seq, 8, 2, 64, 16, dtype, cache, tree, change=change, check=False))
+            runs.append(attend(np.random.default_rng(18), [0, 50, 130], [seq] * 3, seq, 8, 2, 64, page, dtype, cache, tree, change=change, check=False))
         (_, _, a, la, sees), (_, _, b, lb, _) = runs
         for i in range(3):
             unseen = torch.from_numpy(~sees[i, :, node])
             assert torch.equal(a[i][unseen], b[i][unseen]) and torch.equal(la[i][unseen], lb[i][unseen])
             assert not bool(torch.isfinite(b[i][~unseen]).all(-1).any())
+
+
+@pytest.mark.parametrize("page", [5, 8, 128])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_an_infinite_value_of_the_prompt(page, dim):
+    """In entries that all rows see, beside and apart from tiles that a mask cuts: every row's element is infinite, and no other."""
+    for seq, at in ((60, 3), (60, 139), (6, 3), (6, 149)):
+        def change(c, sees):
+            where = c.where(0, [at])
+            c.v[where[0], where[1], 1, 7] = -math.inf
+
+        clean = attend(np.random.default_rng(60), [150], [seq], seq, 4, 2, dim, page, "bf16", None, "tree")
+        dirty = attend(np.random.default_rng(60), [150], [seq], seq, 4, 2, dim, page, "bf16", None, "tree", change=change, check=False)
+        want = clean[2][0].clone()
+        want[:, 2:, 7] = -math.inf
+        assert torch.equal(dirty[2][0], want)
 
 
 @pytest.mark.parametrize("dtype,cache,seq", [("bf16", "bf16", 6), ("bf16", "bf16", 60), ("f16", "f8", 6), ("f16", "f8", 60), ("f32", "f32", 6)])
