@@ -58,11 +58,11 @@ struct AppendToken {
 
 // A block finds its tokens' places and cosines once, while its first loads are on their way. Bound: launch and a chain of
 // dependent loads (count and length, page, entry) for a few tokens (32 tokens of 32 + 2 x 8 heads of 128: 3.0 us in a captured
-// graph); for many the blocks' phases, which follow one another (2 x 8192 tokens, 403 MB: 94 us, 63% of the copy rate). Four
-// heads a thread and three blocks an SM are the best of what was tried: 97 us with two blocks and no spilled
-// registers, 106 us with two heads and four blocks.
+// graph); for many the blocks' phases, which follow one another (2 x 8192 tokens, 403 MB: 72 us, 82% of the copy
+// rate). Six heads a thread and two blocks an SM are the best of what was tried: four heads and three blocks, with a quarter of
+// the threads idle at 48 heads and some registers spilled, 94 us; three heads 78 us; three heads and four blocks 104 us.
 template <int DT, int V, int U, bool INTER, bool F8>
-__global__ void __launch_bounds__(256, 3) append_kernel(const __grid_constant__ AppendPlan p, const AppendTile t, int total_tokens,
+__global__ void __launch_bounds__(256, U > 1 ? 2 : 3) append_kernel(const __grid_constant__ AppendPlan p, const AppendTile t, int total_tokens,
                                                         int total_heads) {
   extern __shared__ __align__(16) char mem[];
   AppendToken* const info = reinterpret_cast<AppendToken*>(mem);
@@ -186,8 +186,12 @@ cudaError_t run_append(const AppendPlan& p, cudaStream_t s) {
   // U heads a thread: then as many tokens a block as there are threads for, but not more than 40 KB of cosines
   t.slots = std::min(groups, (heads + U - 1) / U);
   const int cap = p.pairs ? std::max(1, 5120 / p.pairs) : groups;
-  t.tokens = std::max(1, std::min({groups / t.slots, tokens, cap}));
   t.heads = std::min(heads, t.slots * U);
+  if (U > 1) {  // a power of two leaves no thread without a token where items are one too; a block has all heads then
+    while (t.slots & (t.slots - 1)) t.slots &= t.slots - 1;
+    t.heads = heads;
+  }
+  t.tokens = std::max(1, std::min({groups / t.slots, tokens, cap}));
   const int gx = (tokens + t.tokens - 1) / t.tokens, gy = (heads + t.heads - 1) / t.heads;
   const size_t smem = t.tokens * (sizeof(AppendToken) + (size_t)p.pairs * sizeof(float2));
   return launch_after(append_kernel<DT, V, U, INTER, F8>, dim3(gx, gy), dim3(256), smem, s, 1, p, t, tokens, heads);
@@ -212,8 +216,8 @@ cudaError_t run_append_type(const AppendPlan& p, cudaStream_t s) {
   if (!fits) return run_append<DT, 1, 1, false, F8>(p, s);
   // several heads a thread once one each fills the device twice over
   const bool many = (int64_t)p.m.batch * p.m.seq * (p.heads + 2 * p.kv) * (p.dim / V / 2) >= (int64_t)device_sm_count() * 8 * 1024;
-  if (p.interleaved) return many ? run_append<DT, V, 4, true, F8>(p, s) : run_append<DT, V, 1, true, F8>(p, s);
-  return many ? run_append<DT, V, 4, false, F8>(p, s) : run_append<DT, V, 1, false, F8>(p, s);
+  if (p.interleaved) return many ? run_append<DT, V, 6, true, F8>(p, s) : run_append<DT, V, 1, true, F8>(p, s);
+  return many ? run_append<DT, V, 6, false, F8>(p, s) : run_append<DT, V, 1, false, F8>(p, s);
 }
 
 cudaError_t launch_append(const AppendPlan& p, cudaStream_t s) {
